@@ -11,6 +11,7 @@ the HIP runtime torch already loaded (both name it libamdhip64.so.7).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -19,6 +20,20 @@ Q4_0, Q8_0, Q4_K, Q6_K = 0, 1, 2, 3
 FORMATS = {"q4_0": Q4_0, "q8_0": Q8_0, "q4_k": Q4_K, "q6_k": Q6_K}
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmat.so")
 _lib = None
+
+
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+class AttnArgs(ctypes.Structure):
+    """The C struct qmat_attn_args."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("k_fmt", "v_fmt", "dtype", "causal")] +
+                [(n, ctypes.c_void_p) for n in ("q", "out", "k_cache", "v_cache", "page_table",
+                                                "q_start", "kv_len")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "out_stride", "n_tokens", "n_seqs",
+                                               "max_q", "max_kv", "heads", "kv_heads", "head_dim",
+                                               "cells", "page_size", "pages_per_seq", "window")] +
+                [("scale", ctypes.c_float)])
 
 
 class QmatError(RuntimeError):
@@ -71,6 +86,14 @@ def load_library():
     lib.qmat_prefill_noalloc.restype = i32
     lib.qmat_noalloc_scratch_bytes.argtypes = []
     lib.qmat_noalloc_scratch_bytes.restype = i64
+    lib.qmat_kv_store.argtypes = [i32, i32, i32, p, i64, p, i64, p, p, p, p, i64, i64, i64, p]
+    lib.qmat_kv_store.restype = i32
+    lib.qmat_kv_load.argtypes = [i32, i32, i32, p, p, p, p, p, i64, p, i64, i64, i64, i64, p]
+    lib.qmat_kv_load.restype = i32
+    lib.qmat_attn_workspace_bytes.argtypes = [ctypes.POINTER(AttnArgs)]
+    lib.qmat_attn_workspace_bytes.restype = i64
+    lib.qmat_attn.argtypes = [ctypes.POINTER(AttnArgs), p, i64, p]
+    lib.qmat_attn.restype = i32
     _lib = lib
     return lib
 
@@ -316,3 +339,170 @@ def kv_write(fmt, rows: torch.Tensor, cache: torch.Tensor, cell0: int,
         f, rows.data_ptr(), bp or None, cache.data_ptr(), int(cell0), n, cache.shape[0], dim,
         _stream(rows)))
     return cache
+
+
+def _rows2d(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
+    """Token stride of t, a GPU tensor [n, ...] whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor (no CPU path exists)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    row = 1
+    for d in range(t.dim() - 1, 0, -1):
+        if t.shape[d] != 1 and t.stride(d) != row:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        row *= t.shape[d]
+    return t.stride(0) if t.shape[0] > 1 else max(row, 1)
+
+
+def _same_device(**tensors):
+    first = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if first is None:
+            first = t.device
+        elif t.device != first:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {first}")
+
+
+def _dtype(dtype) -> int:
+    if dtype not in DTYPES:
+        raise TypeError(f"element type must be one of {list(DTYPES)}, got {dtype}")
+    return DTYPES[dtype]
+
+
+def _kv_rows(k_fmt, v_fmt, k, v, slots, k_cache, v_cache, k_bias, dim: int):
+    """Checks common to kv_store and kv_load; returns (k_fmt, v_fmt, dtype,
+    k_stride, v_stride, k_bias pointer, n, cells)."""
+    kf, vf, dt = _fmt(k_fmt), _fmt(v_fmt), _dtype(k.dtype)
+    ks, vs = _rows2d(k, "k", k.dtype), _rows2d(v, "v", k.dtype)
+    _gpu(slots, "slots", torch.int32)
+    _gpu(k_cache, "k_cache", torch.uint8)
+    _gpu(v_cache, "v_cache", torch.uint8)
+    n = slots.numel()
+    if k.shape[0] != n or v.shape[0] != n or k.numel() != n * dim or v.numel() != n * dim:
+        raise ValueError("k, v and slots do not match")
+    if k_cache.dim() != 2 or v_cache.dim() != 2 or k_cache.shape[0] != v_cache.shape[0]:
+        raise ValueError("k_cache and v_cache must be 2-D with the same cells")
+    if k_cache.shape[1] != row_bytes(kf, dim) or v_cache.shape[1] != row_bytes(vf, dim):
+        raise ValueError("cache rows do not match the formats and dim")
+    bp = None
+    if k_bias is not None:
+        _gpu(k_bias, "k_bias", torch.float32)
+        if k_bias.numel() != dim:
+            raise ValueError("k_bias must hold dim values")
+        bp = k_bias.data_ptr()
+    _same_device(k=k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache, k_bias=k_bias)
+    return kf, vf, dt, ks, vs, bp, n, k_cache.shape[0]
+
+
+def kv_store(k_fmt, v_fmt, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+             k_cache: torch.Tensor, v_cache: torch.Tensor,
+             k_bias: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Quantize the rows k, v [n, dim] or [n, heads, head_dim] (fp32, fp16 or
+    bf16; tokens any stride apart; K minus k_bias [dim] if given) into the
+    cells slots [n] (int32) of k_cache and v_cache (uint8 [cells,
+    row_bytes(fmt, dim)]); a slot outside the cache skips its row."""
+    dim = math.prod(k.shape[1:])
+    kf, vf, dt, ks, vs, bp, n, cells = _kv_rows(k_fmt, v_fmt, k, v, slots, k_cache, v_cache,
+                                                k_bias, dim)
+    with torch.cuda.device(k.device):
+        _check("qmat_kv_store", load_library().qmat_kv_store(
+            kf, vf, dt, k.data_ptr(), ks, v.data_ptr(), vs, bp, slots.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), n, cells, dim, _stream(k)))
+    return k_cache, v_cache
+
+
+def kv_load(k_fmt, v_fmt, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor,
+            dim: int, dtype: torch.dtype = torch.float32, k_bias: torch.Tensor | None = None,
+            k: torch.Tensor | None = None,
+            v: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Rows (k, v) [n, dim] of the cells slots [n] (int32), dequantized to
+    dtype (K plus k_bias if given); a slot outside the cache gives zeros."""
+    n = slots.numel()
+    if k is None:
+        k = torch.empty((n, dim), dtype=dtype, device=slots.device)
+    if v is None:
+        v = torch.empty((n, dim), dtype=dtype, device=slots.device)
+    if k.dtype != dtype:
+        raise TypeError(f"k must be {dtype}, got {k.dtype}")
+    kf, vf, dt, ks, vs, bp, n, cells = _kv_rows(k_fmt, v_fmt, k, v, slots, k_cache, v_cache,
+                                                k_bias, dim)
+    with torch.cuda.device(k.device):
+        _check("qmat_kv_load", load_library().qmat_kv_load(
+            kf, vf, dt, k_cache.data_ptr(), v_cache.data_ptr(), bp, slots.data_ptr(),
+            k.data_ptr(), ks, v.data_ptr(), vs, n, cells, dim, _stream(k)))
+    return k, v
+
+
+def attn_workspace_bytes(args: AttnArgs) -> int:
+    """Workspace bytes attn needs for these arguments (0: none)."""
+    n = int(load_library().qmat_attn_workspace_bytes(ctypes.byref(args)))
+    if n < 0:
+        raise ValueError("invalid attention shape, formats or element type")
+    return n
+
+
+def attn(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+         page_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, kv_heads: int,
+         page_size: int, scale: float | None = None, causal: bool = True, window: int = 0,
+         max_q: int | None = None, max_kv: int | None = None, out: torch.Tensor | None = None,
+         workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of q [tokens, heads, head_dim] (fp32, fp16 or bf16) over the
+    paged caches k_cache, v_cache (uint8 [cells, row_bytes]): sequence b has
+    the tokens q_start[b] .. q_start[b + 1] - 1 and kv_len[b] cells, found by
+    page_table [seqs, pages] (all int32). scale: 1 / sqrt(head_dim) if None.
+    max_q: an upper bound of a sequence's tokens (all tokens if None);
+    max_kv: of kv_len, as an estimate (what the table holds if None). A
+    workspace of attn_workspace_bytes() is allocated when none is given. Rows
+    of out that belong to no sequence are left as they were (zeros in an out
+    allocated here)."""
+    kf, vf, dt = _fmt(k_fmt), _fmt(v_fmt), _dtype(q.dtype)
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D [tokens, heads, head_dim]")
+    T, heads, head_dim = q.shape
+    qs = _rows2d(q, "q", q.dtype)
+    if out is None:
+        out = torch.zeros((T, heads, head_dim), dtype=q.dtype, device=q.device)
+    os_ = _rows2d(out, "out", q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    for t, name in ((page_table, "page_table"), (q_start, "q_start"), (kv_len, "kv_len")):
+        _gpu(t, name, torch.int32)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _gpu(t, name, torch.uint8)
+    n_seqs = kv_len.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n_seqs or q_start.numel() != n_seqs + 1:
+        raise ValueError("page_table, q_start and kv_len do not match")
+    dim = kv_heads * head_dim
+    if k_cache.dim() != 2 or v_cache.dim() != 2 or k_cache.shape[0] != v_cache.shape[0]:
+        raise ValueError("k_cache and v_cache must be 2-D with the same cells")
+    if k_cache.shape[1] != row_bytes(kf, dim) or v_cache.shape[1] != row_bytes(vf, dim):
+        raise ValueError("cache rows do not match the formats, kv_heads and head_dim")
+    _same_device(q=q, out=out, k_cache=k_cache, v_cache=v_cache, page_table=page_table,
+                 q_start=q_start, kv_len=kv_len, workspace=workspace)
+    a = AttnArgs()
+    a.k_fmt, a.v_fmt, a.dtype, a.causal = kf, vf, dt, 1 if causal else 0
+    a.q, a.out, a.q_stride, a.out_stride = q.data_ptr(), out.data_ptr(), qs, os_
+    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    a.page_table, a.q_start, a.kv_len = (page_table.data_ptr(), q_start.data_ptr(),
+                                         kv_len.data_ptr())
+    a.n_tokens, a.n_seqs = T, n_seqs
+    a.max_q = T if max_q is None else int(max_q)
+    a.max_kv = page_table.shape[1] * page_size if max_kv is None else int(max_kv)
+    a.heads, a.kv_heads, a.head_dim = heads, kv_heads, head_dim
+    a.cells, a.page_size, a.pages_per_seq = k_cache.shape[0], page_size, page_table.shape[1]
+    a.window = int(window)
+    a.scale = head_dim ** -0.5 if scale is None else float(scale)
+    lib = load_library()
+    need = int(lib.qmat_attn_workspace_bytes(ctypes.byref(a)))
+    if need > 0 and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        _gpu(workspace, "workspace", torch.uint8)
+    wp = workspace.data_ptr() if workspace is not None else None
+    wn = workspace.numel() if workspace is not None else 0
+    with torch.cuda.device(q.device):
+        _check("qmat_attn", lib.qmat_attn(ctypes.byref(a), wp, wn, _stream(q)))
+    return out

@@ -1,0 +1,251 @@
+// kv.hip — rows of keys and values into the cells of a quantized KV cache
+// and back (include/qmat.h: qmat_kv_store, qmat_kv_load).
+//
+// Per 32-element block x of a row: d = max|x| / 7 (Q4_0) or / 127 (Q8_0),
+// D = fp16(d), code = clamp(rnd(x / D)); a cell is read back as D * code. The
+// rule and its rounding are quantize.hip's, so the bytes are the same.
+//
+// Both are copies with a little arithmetic: bound by HBM bandwidth where n is
+// large, by the launch where it is not. So K and V go in one launch
+// (blockIdx.y), and the rows are addressed by their slots directly.
+//
+// Work split: four lanes per block, eight elements each. A wave then reads
+// 16 whole blocks side by side (a lane's own 32 elements would be 64 or 128
+// bytes apart from the next lane's), the block's maximum takes two quad
+// permutes, and every lane's codes are one aligned piece of the block's code
+// bytes: for Q4_0 lane q holds elements 4q.. and 16+4q.., the two nibbles of
+// code bytes 4q..4q+3.
+#include "kv_device.hpp"
+#include "qmat_launch.hpp"
+
+namespace qmat {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlocksPerWG = kThreads / 4;
+
+template <int kCtrl>
+__device__ __forceinline__ float quad_max(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, true);
+  return fmaxf(v, __builtin_bit_cast(float, o));
+}
+
+// Row and block column of block i of rows of nb blocks; 32-bit division
+// wherever the counts fit.
+__device__ __forceinline__ void split_index(int64_t i, int64_t total, int nb, int64_t* row,
+                                            int* col) {
+  if (total <= 0xFFFFFFFFLL) {
+    const uint32_t r = (uint32_t)i / (uint32_t)nb;
+    *row = r;
+    *col = (int)((uint32_t)i - r * (uint32_t)nb);
+  } else {
+    *row = i / nb;
+    *col = (int)(i - *row * nb);
+  }
+}
+
+template <bool kQ4, typename T>
+__device__ __forceinline__ void store_blocks(const T* __restrict__ x, int64_t stride,
+                                             const float* __restrict__ bias,
+                                             const int32_t* __restrict__ slots,
+                                             uint8_t* __restrict__ cache, int64_t n,
+                                             int64_t cells, int nb) {
+  constexpr int kBB = kv_block_bytes<kQ4>();
+  constexpr float kQmax = kQ4 ? 7.0f : 127.0f;
+  const int q = threadIdx.x & 3;
+  const int64_t total = n * nb;
+  // a Q4_0 lane's two groups of four elements, a Q8_0 lane's eight
+  const int e0 = kQ4 ? 4 * q : 8 * q, e1 = kQ4 ? 16 + 4 * q : 8 * q + 4;
+  for (int64_t i = (int64_t)blockIdx.x * kBlocksPerWG + (threadIdx.x >> 2); i < total;
+       i += (int64_t)gridDim.x * kBlocksPerWG) {
+    int64_t row;
+    int col;
+    split_index(i, total, nb, &row, &col);
+    const int32_t slot = slots[row];
+    if (slot < 0 || slot >= cells) continue;  // the block's four lanes together
+    const T* src = x + row * stride + 32 * col;
+    float v[8];
+    if constexpr (kQ4) {
+      load_f32<T, 4>(src + e0, v);
+      load_f32<T, 4>(src + e1, v + 4);
+    } else {
+      load_f32<T, 8>(src + e0, v);
+    }
+    if (bias != nullptr) {
+      float b[8];
+      load_f32<float, 4>(bias + 32 * col + e0, b);
+      load_f32<float, 4>(bias + 32 * col + e1, b + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] -= b[e];
+    }
+    float a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
+    a = quad_max<0xB1>(a);  // lanes 1,0,3,2
+    a = quad_max<0x4E>(a);  // lanes 2,3,0,1
+    const uint32_t h = f32_to_f16_bits(a / kQmax);
+    const float D = f16_bits_to_f32(h);
+    uint32_t w0 = kQ4 ? 0x88888888u : 0u, w1 = 0u;
+    if (D != 0.0f) {
+      const float y = 1.0f / D;
+      w0 = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = (int)clampf(roundf(div_shared(v[e], D, y)), kQ4 ? -8.0f : -127.0f, kQmax);
+        if constexpr (kQ4)
+          w0 |= (uint32_t)(c + 8) << (8 * (e & 3) + (e >= 4 ? 4 : 0));
+        else if (e < 4)
+          w0 |= ((uint32_t)c & 0xFFu) << (8 * e);
+        else
+          w1 |= ((uint32_t)c & 0xFFu) << (8 * (e - 4));
+      }
+    }
+    uint8_t* dst = cache + ((int64_t)slot * nb + col) * kBB;
+    if (q == 0) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)h;
+    if constexpr (kQ4)
+      *reinterpret_cast<u32_a2*>(dst + 2 + 4 * q) = w0;
+    else
+      *reinterpret_cast<u32x2_a2*>(dst + 2 + 8 * q) = u32x2_a2{w0, w1};
+  }
+}
+
+template <bool kQ4, typename T>
+__device__ __forceinline__ void load_blocks(const uint8_t* __restrict__ cache,
+                                            const float* __restrict__ bias,
+                                            const int32_t* __restrict__ slots,
+                                            T* __restrict__ out, int64_t stride, int64_t n,
+                                            int64_t cells, int nb) {
+  constexpr int kBB = kv_block_bytes<kQ4>();
+  const int q = threadIdx.x & 3;
+  const int64_t total = n * nb;
+  const int e0 = kQ4 ? 4 * q : 8 * q, e1 = kQ4 ? 16 + 4 * q : 8 * q + 4;
+  for (int64_t i = (int64_t)blockIdx.x * kBlocksPerWG + (threadIdx.x >> 2); i < total;
+       i += (int64_t)gridDim.x * kBlocksPerWG) {
+    int64_t row;
+    int col;
+    split_index(i, total, nb, &row, &col);
+    const int32_t slot = slots[row];
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (slot >= 0 && slot < cells) {
+      const uint8_t* src = cache + ((int64_t)slot * nb + col) * kBB;
+      const float D = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(src));
+      if constexpr (kQ4) {
+        const uint32_t w = *reinterpret_cast<const u32_a2*>(src + 2 + 4 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = D * (float)((int)((w >> (8 * e)) & 15u) - 8);
+          v[4 + e] = D * (float)((int)((w >> (8 * e + 4)) & 15u) - 8);
+        }
+      } else {
+        const u32x2_a2 w = *reinterpret_cast<const u32x2_a2*>(src + 2 + 8 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = D * (float)(int8_t)(w.x >> (8 * e));
+          v[4 + e] = D * (float)(int8_t)(w.y >> (8 * e));
+        }
+      }
+      if (bias != nullptr) {
+        float b[8];
+        load_f32<float, 4>(bias + 32 * col + e0, b);
+        load_f32<float, 4>(bias + 32 * col + e1, b + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += b[e];
+      }
+    }
+    T* dst = out + row * stride + 32 * col;
+    if constexpr (kQ4) {
+      store_f32<T, 4>(dst + e0, v);
+      store_f32<T, 4>(dst + e1, v + 4);
+    } else {
+      store_f32<T, 8>(dst + e0, v);
+    }
+  }
+}
+
+template <bool kKQ4, bool kVQ4, typename T>
+__global__ __launch_bounds__(kThreads) void kv_store_kernel(
+    const T* __restrict__ k, int64_t k_stride, const T* __restrict__ v, int64_t v_stride,
+    const float* __restrict__ k_bias, const int32_t* __restrict__ slots,
+    uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, int64_t n, int64_t cells,
+    int nb) {
+  if (blockIdx.y == 0)
+    store_blocks<kKQ4, T>(k, k_stride, k_bias, slots, k_cache, n, cells, nb);
+  else
+    store_blocks<kVQ4, T>(v, v_stride, nullptr, slots, v_cache, n, cells, nb);
+}
+
+template <bool kKQ4, bool kVQ4, typename T>
+__global__ __launch_bounds__(kThreads) void kv_load_kernel(
+    const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
+    const float* __restrict__ k_bias, const int32_t* __restrict__ slots, T* __restrict__ k,
+    int64_t k_stride, T* __restrict__ v, int64_t v_stride, int64_t n, int64_t cells, int nb) {
+  if (blockIdx.y == 0)
+    load_blocks<kKQ4, T>(k_cache, k_bias, slots, k, k_stride, n, cells, nb);
+  else
+    load_blocks<kVQ4, T>(v_cache, nullptr, slots, v, v_stride, n, cells, nb);
+}
+
+constexpr int64_t kMaxGrid = 1 << 22;
+
+dim3 grid_for(int64_t n, int64_t nb) {
+  const int64_t wgs = (n * nb + kBlocksPerWG - 1) / kBlocksPerWG;
+  return dim3((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid), 2);
+}
+
+template <bool kKQ4, bool kVQ4, typename T>
+void store_as(const KvRows& r, hipStream_t stream) {
+  hipLaunchKernelGGL((kv_store_kernel<kKQ4, kVQ4, T>), grid_for(r.n, r.dim / 32), dim3(kThreads),
+                     0, stream, static_cast<const T*>(r.k), r.k_stride,
+                     static_cast<const T*>(r.v), r.v_stride, r.k_bias, r.slots,
+                     static_cast<uint8_t*>(r.k_cache), static_cast<uint8_t*>(r.v_cache), r.n,
+                     r.cells, (int)(r.dim / 32));
+}
+
+template <bool kKQ4, bool kVQ4, typename T>
+void load_as(const KvRows& r, hipStream_t stream) {
+  hipLaunchKernelGGL((kv_load_kernel<kKQ4, kVQ4, T>), grid_for(r.n, r.dim / 32), dim3(kThreads),
+                     0, stream, static_cast<const uint8_t*>(r.k_cache),
+                     static_cast<const uint8_t*>(r.v_cache), r.k_bias, r.slots,
+                     static_cast<T*>(r.k), r.k_stride, static_cast<T*>(r.v), r.v_stride, r.n,
+                     r.cells, (int)(r.dim / 32));
+}
+
+template <bool kStore, typename T>
+void launch_as(int k_fmt, int v_fmt, const KvRows& r, hipStream_t stream) {
+  const auto go = [&](auto kq, auto vq) {
+    if constexpr (kStore)
+      store_as<decltype(kq)::value, decltype(vq)::value, T>(r, stream);
+    else
+      load_as<decltype(kq)::value, decltype(vq)::value, T>(r, stream);
+  };
+  const std::true_type q4{};
+  const std::false_type q8{};
+  if (k_fmt == kFmtQ4_0)
+    v_fmt == kFmtQ4_0 ? go(q4, q4) : go(q4, q8);
+  else
+    v_fmt == kFmtQ4_0 ? go(q8, q4) : go(q8, q8);
+}
+
+template <bool kStore>
+hipError_t launch(int k_fmt, int v_fmt, int dtype, const KvRows& r, hipStream_t stream) {
+  if (r.n == 0 || r.dim == 0) return hipSuccess;
+  if (dtype == kDtypeF32)
+    launch_as<kStore, float>(k_fmt, v_fmt, r, stream);
+  else if (dtype == kDtypeF16)
+    launch_as<kStore, _Float16>(k_fmt, v_fmt, r, stream);
+  else
+    launch_as<kStore, __bf16>(k_fmt, v_fmt, r, stream);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_store(int k_fmt, int v_fmt, int dtype, const KvRows& r, hipStream_t stream) {
+  return launch<true>(k_fmt, v_fmt, dtype, r, stream);
+}
+
+hipError_t launch_kv_load(int k_fmt, int v_fmt, int dtype, const KvRows& r, hipStream_t stream) {
+  return launch<false>(k_fmt, v_fmt, dtype, r, stream);
+}
+
+}  // namespace qmat

@@ -138,7 +138,8 @@ const char* qmat_strerror(int status) {
       return "the Q8_0 activations (N * row bytes) exceed the static workspace of "
              "qmat_prefill_noalloc (qmat_noalloc_scratch_bytes())";
     case QMAT_E_WORKSPACE:
-      return "the workspace is NULL or smaller than qmat_gemm_workspace_bytes()";
+      return "the workspace is NULL or smaller than the call's *_workspace_bytes()";
+    case QMAT_E_DTYPE: return "unknown element type";
     default: return "unknown status";
   }
 }

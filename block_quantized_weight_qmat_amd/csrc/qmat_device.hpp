@@ -41,6 +41,23 @@ __device__ __forceinline__ uint32_t as_u32(half2_t v) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+__device__ __forceinline__ float clampf(float v, float lo, float hi) {
+  return fminf(fmaxf(v, lo), hi);
+}
+
+// a / b correctly rounded, for a divisor shared by many quotients: with
+// y = 1/b correctly rounded (one IEEE division per block), q0 = a * y and
+// the residual a - q0 * b exact in one fma, q0 + residual * y rounded once
+// is the correctly rounded quotient whenever it can round to a code. Checked
+// against IEEE division on the CPU (tests/shared_divisor_check.c) over the
+// fp16 divisor range, quotients within +-135 (half-integer neighbourhoods
+// included) and random operands: only subnormal numerators differ, and
+// those round to code 0 either way.
+__device__ __forceinline__ float div_shared(float a, float b, float y) {
+  const float q0 = a * y;
+  return fmaf(fmaf(-q0, b, a), y, q0);
+}
+
 // Byte permute: result byte k = byte sel[k] of the 8-byte value {hi:lo}
 // (bytes 0..3 from lo, 4..7 from hi; selector 0x0c gives 0x00).
 __device__ __forceinline__ uint32_t perm_b32(uint32_t hi, uint32_t lo, uint32_t sel) {

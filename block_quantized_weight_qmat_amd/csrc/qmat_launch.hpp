@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "gemm_split.hpp"
+#include "qmat.h"
 
 namespace qmat {
 
@@ -21,6 +22,28 @@ hipError_t launch_quantize(int fmt, const float* W, void* blocks, int64_t rows, 
 // or Q8_0 rows at dst (16-byte aligned).
 hipError_t launch_kv_write(int fmt, const float* rows, const float* bias, void* dst, int64_t n,
                            int64_t dim, hipStream_t stream);
+
+constexpr int kDtypeF32 = 0;
+constexpr int kDtypeF16 = 1;
+constexpr int kDtypeBF16 = 2;
+
+// K and V rows of named cells (kv.hip): rows k, v of dim elements of one
+// element type, k_stride and v_stride elements apart; slots on the device.
+struct KvRows {
+  void *k, *v;  // read by the store, written by the load
+  int64_t k_stride, v_stride;
+  const float* k_bias;
+  const int32_t* slots;
+  void *k_cache, *v_cache;
+  int64_t n, cells, dim;
+};
+hipError_t launch_kv_store(int k_fmt, int v_fmt, int dtype, const KvRows& r, hipStream_t stream);
+hipError_t launch_kv_load(int k_fmt, int v_fmt, int dtype, const KvRows& r, hipStream_t stream);
+
+// Attention over the quantized cache (attn.hip): validated arguments;
+// workspace of attn_workspace_bytes() bytes.
+int64_t attn_workspace_bytes(const qmat_attn_args& a);
+hipError_t launch_attn(const qmat_attn_args& a, void* workspace, hipStream_t stream);
 
 hipError_t launch_gemv(int fmt, const void* blocks, const float* x, float* y, int64_t M,
                        int64_t K, hipStream_t stream);

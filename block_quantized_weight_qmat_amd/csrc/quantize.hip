@@ -22,10 +22,6 @@ namespace {
 
 constexpr int kQThreads = 256;
 
-__device__ __forceinline__ float clampf(float v, float lo, float hi) {
-  return fminf(fmaxf(v, lo), hi);
-}
-
 // Staging of 64 consecutive 32-element blocks (8 KB) of one wave, copied
 // from memory straight into LDS (1 KB per instruction, 16 bytes per lane).
 // Part k (elements 4k..4k+3) of block b sits in column (k + b / 2) mod 8 of
@@ -59,19 +55,6 @@ __device__ __forceinline__ void read_block(const float* lds, int lane, bool vali
     v[4 * k + 2] = valid ? t.z : 0.0f;
     v[4 * k + 3] = valid ? t.w : 0.0f;
   }
-}
-
-// a / b correctly rounded, for a divisor shared by many quotients: with
-// y = 1/b correctly rounded (one IEEE division per block), q0 = a * y and
-// the residual a - q0 * b exact in one fma, q0 + residual * y rounded once
-// is the correctly rounded quotient whenever it can round to a code. Checked
-// against IEEE division on the CPU (tests/shared_divisor_check.c) over the
-// fp16 divisor range, quotients within +-135 (half-integer neighbourhoods
-// included) and random operands: only subnormal numerators differ, and
-// those round to code 0 either way.
-__device__ __forceinline__ float div_shared(float a, float b, float y) {
-  const float q0 = a * y;
-  return fmaf(fmaf(-q0, b, a), y, q0);
 }
 
 // Q4_0 (kQ4 = true) or Q8_0 (false): one lane per 32-element block, 64

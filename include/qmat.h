@@ -1,7 +1,7 @@
 /*
  * qmat.h — C ABI of the block-quantized weight matmul for MI355X (gfx950).
  *
- * Six operations, all enqueued asynchronously on a caller-supplied HIP
+ * Nine operations, all enqueued asynchronously on a caller-supplied HIP
  * stream:
  *   qmat_quantize  fp32 matrix  -> packed weight (or activation) blocks
  *   qmat_gemv      packed W × fp32 x        -> fp32 y        (decode)
@@ -9,6 +9,9 @@
  *   qmat_gemm      packed W × Q8_0 X blocks -> fp32 Y        (prefill)
  *   qmat_prefill   packed W × fp32 X        -> fp32 Y        (prefill, one call)
  *   qmat_kv_write  fp32 K or V rows -> Q4_0 / Q8_0 rows of a KV cache
+ *   qmat_kv_store  fp32 / fp16 / bf16 K and V rows -> the named cache cells
+ *   qmat_kv_load   the named cache cells -> fp32 / fp16 / bf16 K and V rows
+ *   qmat_attn      attention of new tokens over a paged Q4_0 / Q8_0 cache
  * and qmat_prefill_noalloc, qmat_prefill without a caller workspace for
  * callers that cannot allocate device memory.
  *
@@ -120,9 +123,14 @@ typedef enum qmat_status {
   QMAT_E_ALIGN = 5, /* a pointer is not 16-byte aligned                   */
   QMAT_E_SCRATCH = 6, /* qmat_prefill_noalloc: the activation workspace it
                         needs exceeds its static scratch                   */
-  QMAT_E_WORKSPACE = 7 /* qmat_gemm_ws: workspace NULL or smaller than
-                          qmat_gemm_workspace_bytes()                      */
+  QMAT_E_WORKSPACE = 7, /* qmat_gemm_ws, qmat_attn: workspace NULL or smaller
+                           than qmat_gemm_workspace_bytes() /
+                           qmat_attn_workspace_bytes()                     */
+  QMAT_E_DTYPE = 8      /* unknown element type                            */
 } qmat_status;
+
+/* Element type of the activations of qmat_kv_store, qmat_kv_load, qmat_attn. */
+typedef enum qmat_dtype { QMAT_F32 = 0, QMAT_F16 = 1, QMAT_BF16 = 2 } qmat_dtype;
 
 /* Bytes of the static device workspace of qmat_prefill_noalloc (16 MiB):
  * room for the Q8_0 activations of N tokens of K elements while
@@ -362,6 +370,134 @@ int64_t qmat_noalloc_scratch_bytes(void);
 int qmat_kv_write(int fmt, const float *rows, const float *bias, void *cache,
                   int64_t cell0, int64_t n, int64_t cells, int64_t dim,
                   void *stream);
+
+/*
+ * qmat_kv_store — quantize the new K and V rows of a step into the cells of
+ *   a KV cache, in one launch. [KVQ] as for qmat_kv_write, whose rule it
+ *   applies: every written cell holds exactly the bytes that
+ *   qmat_quantize(fmt, f32(row) - bias, ...) would write (fp16 and bf16
+ *   inputs are widened to fp32 exactly; the bias is subtracted in fp32).
+ *   k_fmt, v_fmt: QMAT_Q4_0 or QMAT_Q8_0 each (others: QMAT_E_FMT).
+ *   dtype:  element type of k and v (others: QMAT_E_DTYPE).
+ *   k, v:   n rows of dim elements (dim = KV heads x head dimension, a
+ *           multiple of 32), rows k_stride and v_stride elements apart (for
+ *           slices of one fused projection), at least dim.
+ *   k_bias: fp32 [dim] subtracted from every K row, or NULL.
+ *   slots:  DEVICE int32 [n]: the cell that row i is written to. A slot
+ *           outside [0, cells) skips its row (padding of a batch). The other
+ *           slots of a call must differ from each other; a cell named twice
+ *           is left with blocks of either row.
+ *   k_cache, v_cache: cells rows of qmat_row_bytes(k_fmt, dim) and
+ *           qmat_row_bytes(v_fmt, dim) bytes; bytes of other cells stay.
+ *   All pointers 16-byte aligned, the strides whole multiples of 16 bytes
+ *   (QMAT_E_ALIGN). n == 0 or dim == 0 enqueues nothing; cells == 0 skips
+ *   every row, and the caches may then be NULL.
+ *   Inputs must not overlap the caches.
+ */
+int qmat_kv_store(int k_fmt, int v_fmt, int dtype, const void *k, int64_t k_stride,
+                  const void *v, int64_t v_stride, const float *k_bias,
+                  const int32_t *slots, void *k_cache, void *v_cache, int64_t n,
+                  int64_t cells, int64_t dim, void *stream);
+
+/*
+ * qmat_kv_load — read cells of a KV cache back as rows, K and V in one
+ *   launch: k[i] = T(dequant(k_cache[slots[i]]) + k_bias) and
+ *   v[i] = T(dequant(v_cache[slots[i]])), T = dtype, computed in fp32 (the
+ *   products of a scale and a code are exact there) and rounded once to T,
+ *   to nearest even. A slot outside [0, cells) gives a row of zeros; a slot
+ *   may be named any number of times.
+ *   Arguments as for qmat_kv_store, with k and v the outputs: elements of a
+ *   row past dim (up to its stride) are left as they were.
+ */
+int qmat_kv_load(int k_fmt, int v_fmt, int dtype, const void *k_cache,
+                 const void *v_cache, const float *k_bias, const int32_t *slots,
+                 void *k, int64_t k_stride, void *v, int64_t v_stride, int64_t n,
+                 int64_t cells, int64_t dim, void *stream);
+
+/*
+ * qmat_attn — attention of the newest tokens of several sequences over their
+ *   quantized KV cache: one token per sequence (decode), a few (drafted
+ *   tokens to verify) or whole prompts, mixed in one call.
+ *   [LC05 KV], [KVQ]: K and V are kept as q8_0 or q4_0 rows; they are read
+ *   as such here, without a dequantized copy.
+ *
+ *   Sequence b has the n_b = q_start[b+1] - q_start[b] tokens q_start[b] ..
+ *   q_start[b+1] - 1 of q, and len_b = kv_len[b] cells (its own new tokens'
+ *   included: store them first). Its cell j is cache row
+ *   page_table[b][j / page_size] * page_size + j % page_size. Its token i
+ *   sits at position p = len_b - n_b + i and sees the cells j < len_b with
+ *   j <= p (if causal) and j > p - window (if window > 0). Query head h uses
+ *   cache head h / (heads / kv_heads). Then, for each token and head,
+ *     s_j = scale * q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j)
+ *   over the cells it sees; a token that sees no cell gets zeros.
+ *   A K bias subtracted before storing (k_bias) changes no output: it moves
+ *   all scores of a row alike.
+ *
+ *   Arithmetic: the codes enter the matrix cores as exact integers, and the
+ *   fp16 block scales are applied in fp32 (K) or to the probabilities (V);
+ *   scores, maxima, sums and outputs are held in fp32. For fp16 and bf16
+ *   the queries are exact (within 2^-24 of a row's largest element) and the
+ *   products probability x V scale are rounded once to 11 bits; for fp32 both
+ *   are carried as pairs of fp16 (22 bits). Relative L2 error against exact
+ *   arithmetic, before rounding to dtype: below 1e-5 (fp32), 5e-4 (others).
+ *   Cells that a token does not see have no effect on it, whatever their
+ *   bytes hold (infinite or NaN scales included).
+ *
+ *   Limits (QMAT_E_SHAPE): head_dim 64, 128 or 256; heads a multiple of
+ *   kv_heads and at most 4096, heads / kv_heads at most 256, max_q * heads /
+ *   kv_heads at most 2^30; page_size a power of two;
+ *   pages_per_seq * page_size <= 2^30; cells <= 2^31 - 1; n_tokens, n_seqs
+ *   <= 2^24; max_q <= 2^24; strides >= heads * head_dim; scale finite.
+ *   Device values outside their range do no harm: len_b is cut to
+ *   [0, pages_per_seq * page_size], n_b to [0, max_q], tokens outside
+ *   [0, n_tokens) are skipped, and the cells of a page number outside
+ *   [0, cells / page_size) count as not seen. Page numbers at and behind
+ *   ceil(len_b / page_size) are not read.
+ *   Rows of out that belong to no sequence are left as they were.
+ */
+typedef struct qmat_attn_args {
+  int32_t k_fmt, v_fmt;      /* QMAT_Q4_0 or QMAT_Q8_0 each                  */
+  int32_t dtype;             /* element type of q and out                    */
+  int32_t causal;            /* nonzero: a token sees no later cell          */
+  const void *q;             /* [n_tokens][heads][head_dim]                  */
+  void *out;                 /* the same                                     */
+  const void *k_cache;       /* [cells][qmat_row_bytes(k_fmt, kv_heads * head_dim)] */
+  const void *v_cache;       /* [cells][qmat_row_bytes(v_fmt, kv_heads * head_dim)] */
+  const int32_t *page_table; /* DEVICE [n_seqs][pages_per_seq]               */
+  const int32_t *q_start;    /* DEVICE [n_seqs + 1], not decreasing          */
+  const int32_t *kv_len;     /* DEVICE [n_seqs]                              */
+  int64_t q_stride;          /* elements between tokens of q                 */
+  int64_t out_stride;        /* elements between tokens of out               */
+  int64_t n_tokens;          /* rows of q and out                            */
+  int64_t n_seqs;
+  int64_t max_q;             /* no sequence has more new tokens than this    */
+  int64_t max_kv;            /* the longest kv_len, or an estimate: it sets
+                                the work split and the workspace alone       */
+  int64_t heads, kv_heads, head_dim;
+  int64_t cells;             /* rows of each cache                           */
+  int64_t page_size;         /* cells per page                               */
+  int64_t pages_per_seq;     /* columns of page_table                        */
+  int64_t window;            /* cells a token sees at most, 0: no limit      */
+  float scale;
+} qmat_attn_args;
+
+/* Bytes of device workspace that qmat_attn needs for these arguments: 0 where
+ * no sequence is split over workgroups. A function of the host values alone
+ * (no pointer is read); -1 for arguments that qmat_attn rejects by their
+ * formats, element type or shapes. */
+int64_t qmat_attn_workspace_bytes(const qmat_attn_args *args);
+
+/* args: HOST struct, read during the call only. workspace: device buffer of
+ * qmat_attn_workspace_bytes() bytes, 16-byte aligned, used only while the
+ * call's work runs (two calls that share one must not overlap in time); NULL
+ * when that is 0. Errors: QMAT_E_NULL for args NULL, QMAT_E_FMT,
+ * QMAT_E_DTYPE, QMAT_E_SHAPE; no tokens or no sequences enqueue nothing; then
+ * QMAT_E_NULL and QMAT_E_ALIGN for the buffers (16 bytes; strides of q and out
+ * whole multiples of 16 bytes; page_table, q_start and kv_len 4 bytes;
+ * the caches may be NULL when cells is 0), QMAT_E_SHAPE for
+ * workspace_bytes < 0, QMAT_E_WORKSPACE. */
+int qmat_attn(const qmat_attn_args *args, void *workspace, int64_t workspace_bytes,
+              void *stream);
 
 #ifdef __cplusplus
 }
