@@ -51,13 +51,14 @@ struct Params {
   const int32_t* table;
   const int32_t* q_start;
   const int32_t* kv_len;
-  float* part_o;  // [row][split][D]
-  float2* part_ml;  // [row][split]
+  float* part_o;    // [token][head][split][D], not divided by the sum
+  float2* part_ml;  // [token][head][split]: reference and sum
   int64_t q_stride, out_stride, k_row, v_row;
   int n_tokens, n_seqs, max_q, heads, kv_heads, group;
+  int tiles, search;  // column tiles, found by their place among all tokens
   int page_shift, n_pages, pages_per_seq, max_cells;
   int causal, window;  // window 0: none
-  int col_tiles, splits, chunk, by_unit;
+  int col_tiles, splits, chunk, by_unit, heads_shift;
   float scale_log2;
 };
 
@@ -105,6 +106,29 @@ __device__ __forceinline__ Span tile_span(const Params& p, const Seq& s, int ct)
     r.splits = n < p.splits ? n : p.splits;
   }
   return r;
+}
+
+// Sequence b's first column tile among those of all tokens: tiles never span
+// sequences, so every sequence may open one more.
+__device__ __forceinline__ int first_tile(const Params& p, int b) {
+  return (int)((int64_t)p.q_start[b] * p.group / kCols) + b;
+}
+
+// The last i < n with first(i) <= x, for a first that does not fall: 64 probes
+// at a time, one per lane.
+template <typename F>
+__device__ __forceinline__ int find_last(int n, int x, const F& first) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int at = lane * step;
+    const uint64_t hit = __ballot(at < n && first(lo + at) <= x);
+    const int last = hit == 0 ? 0 : 63 - __builtin_clzll(hit);
+    lo += last * step;
+    n = n - last * step < step ? n - last * step : step;
+  }
+  return lo;
 }
 
 // Work between lanes of one wave through LDS: earlier writes are in order
@@ -163,57 +187,120 @@ __device__ __forceinline__ float half_of(uint32_t w, int hi) {
   return (float)(hi ? as_half2(w).y : as_half2(w).x);
 }
 
-// A tile's codes and scales in LDS, one wave's own. Code plane x holds 16
-// code bytes of every cell (Q4_0: of block x; Q8_0: of half x % 2 of block x / 2),
-// planes 64 bytes further apart than their cells need, so that the lanes of one
-// write, which go through the blocks, hit different banks.
+// The bytes of one head in a cell: D / 32 packed blocks, 9 (Q4_0) or 17 (Q8_0)
+// units of D / 16 bytes, aligned to their size in the cache. A wave loads a
+// tile's units side by side, 64 at a time, in kLoads steps (the last one half
+// used, its upper lanes repeating the lower): memory sees whole lines, where a
+// lane per block would make an access of its own of each (18- and 34-byte
+// strides at 2-byte alignment; measured 3 times the L1 accesses).
 template <int D, bool kQ4>
-struct TileLds {
+struct Piece {
   static constexpr int kNb = D / 32;
-  static constexpr int kPlanes = kQ4 ? kNb : 2 * kNb;
-  static constexpr int kPlane = kCells * 16 + 64;
-  uint8_t codes[kPlanes * kPlane];
-  uint16_t d[kCells * kNb];  // [cell][block]
+  static constexpr int kBB = kv_block_bytes<kQ4>();
+  static constexpr int kBytes = kNb * kBB;
+  static constexpr int kUnit = D / 16;
+  static constexpr int kUnits = kBytes / kUnit;
+  static constexpr int kLoads = (kCells * kUnits + kWave - 1) / kWave;
+  static constexpr int kRaw = kLoads * kWave * kUnit;
+  static constexpr int kWords = kQ4 ? 4 : 8;  // of a block's codes
+  typedef uint32_t Unit __attribute__((ext_vector_type(kUnit / 4)));
+  static_assert(kUnits * kUnit == kBytes, "whole units");
+
+  // Cell and byte of a lane's unit i.
+  static __device__ __forceinline__ int unit(int i, int lane) {
+    const int x = i * kWave + lane;
+    return x < kCells * kUnits ? x : x - kWave / 2;
+  }
+  static __device__ __forceinline__ int cell(int i, int lane) { return unit(i, lane) / kUnits; }
+  static __device__ __forceinline__ int byte(int i, int lane) {
+    return unit(i, lane) % kUnits * kUnit;
+  }
 };
 
-// Registers between a tile's loads and its LDS.
+// V's codes as the second product reads them: plane x holds 16 code bytes of
+// every cell (Q4_0: of block x; Q8_0: of half x % 2 of block x / 2), 64 bytes
+// further apart than the cells need, so that the lanes of one write, which go
+// through the blocks, hit different banks.
+constexpr int kPlane = kCells * 16 + 64;
+
+// One wave's own LDS. Raw tiles lie as in the cache: [cell][piece].
+template <int D, bool kKQ4, bool kVQ4>
+struct WaveLds {
+  static constexpr int kNb = D / 32;
+  uint8_t k[Piece<D, kKQ4>::kRaw];
+  uint8_t v[Piece<D, kVQ4>::kRaw];
+  uint8_t planes[(kVQ4 ? 1 : 2) * kNb * kPlane];
+  uint16_t kd[kCells * kNb];  // block scales, [cell][block]
+  uint16_t vd[kCells * kNb];
+};
+
 template <int D, bool kQ4>
 struct TileRegs {
-  static constexpr int kN = D / 64;  // blocks per lane
-  u32x4 c[kN][kQ4 ? 1 : 2];
-  uint32_t d[kN];
+  typename Piece<D, kQ4>::Unit u[Piece<D, kQ4>::kLoads];
 };
 
+// A tile whose cells are rows in sequence from base (the same for the wave);
+// off: this lane's units. A buffer load adds the two by itself, and where the
+// tile does not exist it reads zeros of a buffer without bytes: no branch, so
+// that nothing waits for the loads before they are used.
 template <int D, bool kQ4>
-__device__ __forceinline__ void load_tile(TileRegs<D, kQ4>& t, int i, bool there,
-                                          const uint8_t* __restrict__ block) {
-  t.d[i] = 0u;
-  t.c[i][0] = u32x4{0u, 0u, 0u, 0u};
-  if constexpr (!kQ4) t.c[i][1] = u32x4{0u, 0u, 0u, 0u};
-  if (there) {
-    t.d[i] = *reinterpret_cast<const uint16_t*>(block);
-    t.c[i][0] = *reinterpret_cast<const u32x4_a2*>(block + 2);
-    if constexpr (!kQ4) t.c[i][1] = *reinterpret_cast<const u32x4_a2*>(block + 18);
+__device__ __forceinline__ void load_rows(TileRegs<D, kQ4>& t, const uint8_t* __restrict__ base,
+                                          bool exists, int64_t row_bytes, const uint32_t* off) {
+  typedef Piece<D, kQ4> P;
+  const __amdgpu_buffer_rsrc_t r =
+      make_rsrc(base, exists ? (kCells - 1) * row_bytes + P::kBytes : 0);
+#pragma unroll
+  for (int i = 0; i < P::kLoads; ++i) {
+    if constexpr (P::kUnit == 4)
+      t.u[i][0] = __builtin_amdgcn_raw_buffer_load_b32(r, off[i], 0, 0);
+    else if constexpr (P::kUnit == 8)
+      t.u[i] = __builtin_amdgcn_raw_buffer_load_b64(r, off[i], 0, 0);
+    else
+      t.u[i] = __builtin_amdgcn_raw_buffer_load_b128(r, off[i], 0, 0);
+  }
+}
+
+// A tile of several pages: lane x % 32 holds the row of cell x.
+template <int D, bool kQ4>
+__device__ __forceinline__ void load_paged(TileRegs<D, kQ4>& t, const uint8_t* __restrict__ base,
+                                           uint32_t row_bytes, uint32_t row, int lane) {
+#pragma unroll
+  for (int i = 0; i < Piece<D, kQ4>::kLoads; ++i) {
+    const uint32_t r = (uint32_t)__shfl((int)row, Piece<D, kQ4>::cell(i, lane), kWave);
+    t.u[i] = *reinterpret_cast<const typename Piece<D, kQ4>::Unit*>(
+        base + ((uint64_t)r * row_bytes + Piece<D, kQ4>::byte(i, lane)));
   }
 }
 
 template <int D, bool kQ4>
-__device__ __forceinline__ void write_tile(TileLds<D, kQ4>& s, const TileRegs<D, kQ4>& t,
-                                           int lane) {
-  constexpr int kNb = D / 32;
+__device__ __forceinline__ void write_raw(uint8_t* raw, const TileRegs<D, kQ4>& t, int lane) {
+  typedef typename Piece<D, kQ4>::Unit Unit;
 #pragma unroll
-  for (int i = 0; i < TileRegs<D, kQ4>::kN; ++i) {
-    const int cell = i * (kWave / kNb) + lane / kNb, b = lane % kNb;
-    s.d[cell * kNb + b] = (uint16_t)t.d[i];
-    if constexpr (kQ4) {
-      *reinterpret_cast<u32x4*>(s.codes + b * s.kPlane + cell * 16) = t.c[i][0];
-    } else {
-      // flipped sign bits: bytes 0..255 stand for -128..127
-      *reinterpret_cast<u32x4*>(s.codes + 2 * b * s.kPlane + cell * 16) = t.c[i][0] ^ 0x80808080u;
-      *reinterpret_cast<u32x4*>(s.codes + (2 * b + 1) * s.kPlane + cell * 16) =
-          t.c[i][1] ^ 0x80808080u;
-    }
-  }
+  for (int i = 0; i < Piece<D, kQ4>::kLoads; ++i)
+    reinterpret_cast<Unit*>(raw)[i * kWave + lane] = t.u[i];
+}
+
+// N words of a raw piece from an address that is `shift` (2 or 0) bytes past a
+// multiple of 4: LDS reads off their alignment would go lane by lane.
+template <int N, int kShift>
+__device__ __forceinline__ void read_words_at(const uint8_t* at, uint32_t* w) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(at - kShift);
+  uint32_t t[N + 1];
+#pragma unroll
+  for (int i = 0; i < N + (kShift != 0); ++i) t[i] = p[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    w[i] = kShift == 0 ? t[i] : __builtin_amdgcn_alignbyte(t[i + (kShift != 0)], t[i], kShift);
+}
+
+template <int N>
+__device__ __forceinline__ void read_words(const uint8_t* at, uint32_t shift, uint32_t* w) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(at - shift);
+  uint32_t t[N + 1];
+#pragma unroll
+  for (int i = 0; i <= N; ++i) t[i] = p[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = __builtin_amdgcn_alignbyte(t[i + 1], t[i], shift);
 }
 
 typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
@@ -238,7 +325,10 @@ template <uint32_t kMask>
 __device__ __forceinline__ uint32_t signed_codes(uint32_t w) {
   constexpr uint32_t kLess = kMask == 0x000F000Fu ? 0xE408E408u   // -(1024 + 8)
                                                   : 0xE480E480u;  // -(1024 + 128)
-  return as_u32(as_half2((w & kMask) | 0x64006400u) + as_half2(kLess));
+  // the constant in a register: then the mask and it are one operation
+  uint32_t one = 0x64006400u;
+  asm("" : "+v"(one));
+  return as_u32(as_half2((w & kMask) | one) + as_half2(kLess));
 }
 
 // The pairs of a lane's operand from its code word: raw subnormals or signed.
@@ -248,6 +338,35 @@ __device__ __forceinline__ uint32_t codes(uint32_t w) {
 }
 
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, kByte = 0x00FF00FFu;
+
+// N pairs of block scales from LDS.
+template <int N>
+__device__ __forceinline__ void read_scales(const uint16_t* at, uint32_t* d) {
+  const u32x4* p = reinterpret_cast<const u32x4*>(at);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const u32x4 t = p[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[4 * i + e] = t[e];
+  }
+}
+
+// A cell's block scales as the K index of a product with q_z: the same number
+// at x and at kNb + x (the lane group's share of x = 0..31; beyond 2 kNb the
+// queries are 0, and so is what is multiplied with them).
+template <int kNb>
+__device__ __forceinline__ half8_t scales_of(const uint16_t* at) {
+  if constexpr (kNb == 2) {
+    const uint32_t d = *reinterpret_cast<const uint32_t*>(at);
+    return as_half8(d, d, 0u, 0u);
+  } else if constexpr (kNb == 4) {
+    const u32x2 d = *reinterpret_cast<const u32x2*>(at);
+    return as_half8(d.x, d.y, d.x, d.y);
+  } else {
+    const u32x4 d = *reinterpret_cast<const u32x4*>(at);
+    return as_half8(d.x, d.y, d.z, d.w);
+  }
+}
 
 // The operand order of a lane's 8 cells or 8 elements: byte pairs (0, 2) and
 // (1, 3) of each word.
@@ -270,38 +389,61 @@ struct State {
 // One workgroup: one sequence, cache head, column tile and split; its waves
 // take the split's 32-cell tiles in turn, each with its own LDS and no barrier,
 // and join at the end.
-template <int D, bool kKQ4, bool kVQ4, typename T>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(const Params p) {
+//
+// kWhole: pages of 32 cells or more, which hold whole tiles, so that a tile's
+// page is one number for the wave. Smaller pages: one per cell.
+template <int D, bool kKQ4, bool kVQ4, bool kWhole, typename T>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3)
+void attn_split_kernel(const Params p) {
   constexpr bool kPair = sizeof(T) == 4;
   constexpr int kNb = D / 32;
-  constexpr int kPer = D / 64;      // blocks per lane and tile
+  constexpr int kPer = D / 64;        // blocks per lane and tile
   constexpr int kStep = kWave / kNb;  // cells between them
-  struct WaveLds {
-    TileLds<D, kKQ4> k;
-    TileLds<D, kVQ4> v;
-  };
+  typedef Piece<D, kKQ4> KP;
+  typedef Piece<D, kVQ4> VP;
+  typedef WaveLds<D, kKQ4, kVQ4> Lds;
   constexpr int kJoin = kWaves * (D / 16) * kWave * 16;
-  constexpr int kLds = sizeof(WaveLds) * kWaves > kJoin ? sizeof(WaveLds) * kWaves : kJoin;
+  constexpr int kLds = (int)sizeof(Lds) * kWaves > kJoin ? (int)sizeof(Lds) * kWaves : kJoin;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   __shared__ float join_m[kWaves][kCols], join_l[kWaves][kCols];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
-  WaveLds& mine = reinterpret_cast<WaveLds*>(lds)[wave];
+  Lds& mine = reinterpret_cast<Lds*>(lds)[wave];
 
-  // Workgroups go to the 8 XCDs in turn. All heads and column tiles of one
+  uint32_t k_off[KP::kLoads], v_off[VP::kLoads];
+#pragma unroll
+  for (int i = 0; i < KP::kLoads; ++i)
+    k_off[i] = KP::cell(i, lane) * (uint32_t)p.k_row + KP::byte(i, lane);
+#pragma unroll
+  for (int i = 0; i < VP::kLoads; ++i)
+    v_off[i] = kKQ4 == kVQ4 ? k_off[i] : VP::cell(i, lane) * (uint32_t)p.v_row + VP::byte(i, lane);
+
+  // Workgroups go to the 8 XCDs in turn. All heads (and column tiles) of one
   // sequence and split get the same XCD, whose L2 then holds the cache lines
   // they share; too few such units for 8 XCDs are dealt out head by head.
-  const int64_t inner = (int64_t)p.kv_heads * p.col_tiles;
-  const int64_t units = (int64_t)p.n_seqs * p.splits;
-  const int64_t total = p.by_unit ? (units + 7) / 8 * 8 * inner : units * inner;
-  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const int64_t unit = p.by_unit ? (id >> 3) / inner * 8 + (id & 7) : id / inner;
+  // A workgroup's waves share a split's tiles of one head, or take a head each.
+  const int sub = kWaves >> p.heads_shift;  // waves per head
+  const int part = wave & (sub - 1);
+  const uint32_t head_groups = (uint32_t)p.kv_heads >> p.heads_shift;
+  const uint32_t inner = head_groups * (p.search ? 1 : p.col_tiles);
+  const uint32_t units = (uint32_t)(p.search ? p.tiles : p.n_seqs) * p.splits;
+  const uint32_t total = p.by_unit ? (units + 7) / 8 * 8 * inner : units * inner;
+  for (uint32_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const uint32_t turn = p.by_unit ? id >> 3 : id;
+    const uint32_t unit = p.by_unit ? turn / inner * 8 + (id & 7) : turn / inner;
     if (unit >= units) continue;
-    const int64_t in = (p.by_unit ? id >> 3 : id) % inner;
-    const int head = (int)(in % p.kv_heads), ct = p.col_tiles - 1 - (int)(in / p.kv_heads);
-    const int b = (int)(unit / p.splits), split = (int)(unit % p.splits);
+    const uint32_t in = turn % inner;
+    const int head = (int)(in % head_groups << p.heads_shift) + (wave >> (2 - p.heads_shift));
+    const int split = (int)(unit % p.splits);
+    int b = (int)(unit / p.splits), ct = p.col_tiles - 1 - (int)(in / head_groups);
+    if (p.search) {
+      const int x = p.tiles - 1 - b;  // late tiles first: causal ones see more
+      b = find_last(p.n_seqs, x, [&](int i) { return first_tile(p, i); });
+      ct = x - first_tile(p, b);
+      if (ct < 0) continue;
+    }
     const Seq s = sequence(p, b);
     const int cols = s.nq * p.group;
     if (ct * kCols >= cols) continue;
@@ -325,13 +467,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
     const int all_hi = last_cell(p, s, ct * kCols / p.group);
 
     half8_t q_hi[kNb], q_lo[kPair ? kNb : 1];
-    float start[kNb];  // -z times the block's query sum, for unsigned codes
+    half8_t q_z;  // unsigned codes: -z times the blocks' query sums, see scales_of
     float cs;          // from an S accumulator to a score
     {
       float q[kNb][8];
       const T* row = static_cast<const T*>(p.q) + (live ? at : 0) * p.q_stride +
                      ((int64_t)head * p.group + c % p.group) * D;
-      float a = 0.0f;
+      float a = 0.0f, z_sum[kNb];
 #pragma unroll
       for (int i = 0; i < kNb; ++i) {
 #pragma unroll
@@ -362,7 +504,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
           l[e] = kPair ? (float)(_Float16)(x - h[e]) : 0.0f;
           sum += h[e] + l[e];
         }
-        if constexpr (!kPair) start[i] = (kKQ4 ? -8.0f : -128.0f) * 0x1p-24f * groups_sum(sum);
+        z_sum[i] = kPair ? 0.0f : (kKQ4 ? -8.0f : -128.0f) * 0x1p-24f * groups_sum(sum);
         half8_t vh, vl;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -375,6 +517,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
         q_hi[i] = vh;
         if constexpr (kPair) q_lo[i] = vl;
       }
+      // K index x: block x's sum for x < kNb, its rounding error for the next kNb
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kNb; ++i) {
+          const float top = (float)(_Float16)z_sum[i];
+          if (8 * g + e == i) v = top;
+          if (8 * g + e == kNb + i) v = z_sum[i] - top;
+        }
+        q_z[e] = (_Float16)v;
+      }
     }
 
     State<D> st;
@@ -385,96 +539,117 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
     st.e = 0;
 
     const int32_t* pages = p.table + (int64_t)b * p.pages_per_seq;
-    const int my_block = lane % kNb, my_cell = lane / kNb;
-    const uint8_t* k_base = p.kc + ((int64_t)head * kNb + my_block) * kv_block_bytes<kKQ4>();
-    const uint8_t* v_base = p.vc + ((int64_t)head * kNb + my_block) * kv_block_bytes<kVQ4>();
-    int32_t page[kPer];
-    const auto load_pages = [&](int j0) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int j = j0 + my_cell + i * kStep;
-        page[i] = j < end ? pages[j >> p.page_shift] : -1;
-      }
+    const uint8_t* k_base = p.kc + (int64_t)head * KP::kBytes;
+    const uint8_t* v_base = p.vc + (int64_t)head * VP::kBytes;
+    const int in_page = (1 << p.page_shift) - 1;
+    int page = -1;  // of the tile to load next; small pages: of cell lane % 32
+    const auto load_page = [&](int j0) {
+      const int j = kWhole ? j0 : j0 + (lane & 31);
+      const int got = pages[(j < end ? j : begin) >> p.page_shift];
+      page = j < end ? got : -1;
     };
     TileRegs<D, kKQ4> rk;
     TileRegs<D, kVQ4> rv;
-    bool there[kPer];
+    uint32_t next_seen = 0;  // cells of the loaded tile that exist, by bit
     const auto load = [&](int j0) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int j = j0 + my_cell + i * kStep;
-        there[i] = page[i] >= 0 && page[i] < p.n_pages;
-        const int64_t cell =
-            ((int64_t)page[i] << p.page_shift) + (j & ((1 << p.page_shift) - 1));
-        load_tile<D, kKQ4>(rk, i, there[i], k_base + cell * p.k_row);
-        load_tile<D, kVQ4>(rv, i, there[i], v_base + cell * p.v_row);
+      if constexpr (kWhole) {
+        const int first = __builtin_amdgcn_readfirstlane(page);
+        const bool ok = first >= 0 && first < p.n_pages;
+        const int64_t row = ok ? ((int64_t)first << p.page_shift) + (j0 & in_page) : 0;
+        load_rows<D, kKQ4>(rk, k_base + row * p.k_row, ok, p.k_row, k_off);
+        load_rows<D, kVQ4>(rv, v_base + row * p.v_row, ok, p.v_row, v_off);
+        next_seen = ok ? ~0u : 0u;
+      } else {  // cells that do not exist load row 0
+        const bool ok = page >= 0 && page < p.n_pages;
+        const uint32_t row = ok ? (page << p.page_shift) + ((j0 + (lane & 31)) & in_page) : 0;
+        load_paged<D, kKQ4>(rk, k_base, (uint32_t)p.k_row, row, lane);
+        load_paged<D, kVQ4>(rv, v_base, (uint32_t)p.v_row, row, lane);
+        next_seen = (uint32_t)__ballot(ok);
       }
+      const int left = end - j0;
+      if (left < kCells) next_seen &= left > 0 ? (1u << left) - 1 : 0u;
     };
 
-    const int step = kWaves * kCells;
-    int j0 = begin + wave * kCells;
-    if (j0 < end) {
-      load_pages(j0);
+    const int step = sub * kCells;
+    int j0 = begin + part * kCells;
+    const bool any = j0 < end && p.n_pages > 0;
+    if (any) {
+      load_page(j0);
       load(j0);
-      if (j0 + step < end) load_pages(j0 + step);
+      load_page(j0 + step);
     }
-    for (; j0 < end; j0 += step) {
-      // tile j0: registers to LDS
-      uint64_t seen[kPer];
+    for (; any && j0 < end; j0 += step) {
+      // tile j0: registers to LDS, then the next tile's loads
+      const uint32_t seen = next_seen;
+      write_raw<D, kKQ4>(mine.k, rk, lane);
+      write_raw<D, kVQ4>(mine.v, rv, lane);
+      load(j0 + step);
+      load_page(j0 + 2 * step);
+      if (seen == 0) continue;
+      wave_sync();
+      // scales side by side, V's codes into planes
       uint32_t d_max = 0u;
-      bool all = j0 >= all_lo && j0 + kCells <= all_hi;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        seen[i] = __ballot(there[i]);
-        all = all && seen[i] == ~0ull;
-        const uint32_t d = rv.d[i] & 0x7FFFu;
-        d_max = d > d_max ? d : d_max;
+        const int cell = i * kStep + lane / kNb, blk = lane % kNb;
+        mine.kd[cell * kNb + blk] =
+            *reinterpret_cast<const uint16_t*>(mine.k + cell * KP::kBytes + blk * KP::kBB);
+        const uint8_t* vp = mine.v + cell * VP::kBytes + blk * VP::kBB;
+        const uint32_t d = *reinterpret_cast<const uint16_t*>(vp);
+        mine.vd[cell * kNb + blk] = (uint16_t)d;
+        const uint32_t size = (seen >> cell) & 1 ? d & 0x7FFFu : 0u;
+        d_max = size > d_max ? size : d_max;
+        uint32_t w[VP::kWords];
+        read_words<VP::kWords>(vp + 2, blk & 1 ? 0 : 2, w);
+        if constexpr (kVQ4) {
+          *reinterpret_cast<u32x4*>(mine.planes + blk * kPlane + cell * 16) =
+              u32x4{w[0], w[1], w[2], w[3]};
+        } else {
+          // flipped sign bits: bytes 0..255 stand for -128..127
+          *reinterpret_cast<u32x4*>(mine.planes + 2 * blk * kPlane + cell * 16) =
+              u32x4{w[0], w[1], w[2], w[3]} ^ 0x80808080u;
+          *reinterpret_cast<u32x4*>(mine.planes + (2 * blk + 1) * kPlane + cell * 16) =
+              u32x4{w[4], w[5], w[6], w[7]} ^ 0x80808080u;
+        }
       }
-      write_tile<D, kKQ4>(mine.k, rk, lane);
-      write_tile<D, kVQ4>(mine.v, rv, lane);
       d_max = wave_max_u(d_max);
-      if (j0 + step < end) {
-        load(j0 + step);
-        if (j0 + 2 * step < end) load_pages(j0 + 2 * step);
-      }
+      const bool all = seen == ~0u && j0 >= all_lo && j0 + kCells <= all_hi;
       wave_sync();
 
       // scores of cells 8g..8g+7
       float sc[8];
       {
-        uint32_t dk[8 * kNb / 2];
-        const u32x4* src = reinterpret_cast<const u32x4*>(mine.k.d + 8 * g * kNb);
-#pragma unroll
-        for (int i = 0; i < kNb; ++i) {
-          const u32x4 t = src[i];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dk[4 * i + e] = t[e];
-        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int cell = 8 * (col >> 2) + 4 * t + (col & 3);
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          uint32_t dk[4 * kNb / 2];
+          read_scales<4 * kNb / 2>(mine.kd + (8 * g + 4 * t) * kNb, dk);
+          f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (!kPair) sum = mfma(scales_of<kNb>(mine.kd + cell * kNb), q_z, sum);
 #pragma unroll
           for (int i = 0; i < kNb; ++i) {
             half8_t a;
+            // codes of block i of this cell, 4 (Q4_0) or 8 bytes of them
+            const uint8_t* kp = mine.k + cell * KP::kBytes + i * KP::kBB + 2;
             if constexpr (kKQ4) {
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                  mine.k.codes + i * mine.k.kPlane + cell * 16 + 4 * g);
+              uint32_t w;
+              i & 1 ? read_words_at<1, 0>(kp + 4 * g, &w) : read_words_at<1, 2>(kp + 4 * g, &w);
               const uint32_t x = w >> 8;
               a = as_half8(codes<kLow, kPair>(w), codes<kHigh, kPair>(w), codes<kLow, kPair>(x),
                            codes<kHigh, kPair>(x));
             } else {
-              const u32x2 w = *reinterpret_cast<const u32x2*>(
-                  mine.k.codes + (2 * i + (g >> 1)) * mine.k.kPlane + cell * 16 + 8 * (g & 1));
-              a = as_half8(codes<kByte, kPair>(w.x), codes<kByte, kPair>(w.x >> 8),
-                           codes<kByte, kPair>(w.y), codes<kByte, kPair>(w.y >> 8));
+              uint32_t w[2];
+              i & 1 ? read_words_at<2, 0>(kp + 8 * g, w) : read_words_at<2, 2>(kp + 8 * g, w);
+              w[0] ^= 0x80808080u;
+              w[1] ^= 0x80808080u;
+              a = as_half8(codes<kByte, kPair>(w[0]), codes<kByte, kPair>(w[0] >> 8),
+                           codes<kByte, kPair>(w[1]), codes<kByte, kPair>(w[1] >> 8));
             }
-            const float z = kPair ? 0.0f : start[i];
-            f32x4 acc = mfma(a, q_hi[i], f32x4{z, z, z, z});
+            f32x4 acc = mfma(a, q_hi[i], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
             if constexpr (kPair) acc = mfma(a, q_lo[i], acc);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int x = (4 * t + r) * kNb + i;
+              const int x = r * kNb + i;
               sum[r] = fmaf(acc[r], half_of(dk[x / 2], x & 1), sum[r]);
             }
           }
@@ -483,34 +658,17 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
         }
       }
 
-      uint32_t dv[8 * kNb / 2];
-      {
-        const u32x4* src = reinterpret_cast<const u32x4*>(mine.v.d + 8 * g * kNb);
-#pragma unroll
-        for (int i = 0; i < kNb; ++i) {
-          const u32x4 t = src[i];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dv[4 * i + e] = t[e];
-        }
-      }
+      uint32_t unseen = 0u;  // of this lane's cells and row, by bit
       if (!all) {
         // a cell that a row does not see: its score counts as -inf and its V
         // scale as 0, whatever its bytes hold
-        uint64_t bits;
-        if constexpr (kNb == 2)
-          bits = seen[0] >> (16 * g);
-        else if constexpr (kNb == 4)
-          bits = (g & 2 ? seen[1] : seen[0]) >> (32 * (g & 1));
-        else
-          bits = g & 2 ? (g & 1 ? seen[3] : seen[2]) : (g & 1 ? seen[1] : seen[0]);
+        const uint32_t bits = seen >> (8 * g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int j = j0 + 8 * g + e;
-          const bool on = ((bits >> (kNb * e)) & 1) != 0 && j >= lo && j < hi;
+          const bool on = ((bits >> e) & 1) != 0 && j >= lo && j < hi;
           sc[e] = on ? sc[e] : -INFINITY;
-#pragma unroll
-          for (int i = 0; i < kNb / 2; ++i)
-            dv[e * kNb / 2 + i] = on ? dv[e * kNb / 2 + i] : 0u;
+          unseen |= on ? 0u : 1u << e;
         }
       }
 
@@ -539,6 +697,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
         pr[e] = exp2_raw(sc[e] - ref);
         st.l += pr[e];
       }
+      uint32_t dv[8 * kNb / 2];
+      read_scales<8 * kNb / 2>(mine.vd + 8 * g * kNb, dv);
+      if (!all) {
+        asm volatile("");
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int i = 0; i < kNb / 2; ++i)
+            dv[e * kNb / 2 + i] = (unseen >> e) & 1 ? 0u : dv[e * kNb / 2 + i];
+      }
 
 #pragma unroll
       for (int i = 0; i < kNb; ++i) {
@@ -554,13 +722,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
         for (int h = 0; h < 2; ++h) {
           half8_t a;
           if constexpr (kVQ4) {
-            const u32x2 w = read_column(mine.v.codes + i * mine.v.kPlane, lane);
+            const u32x2 w = read_column(mine.planes + i * kPlane, lane);
             a = h ? as_half8(signed_codes<kHigh>(w.x), signed_codes<kHigh>(w.x >> 8),
                              signed_codes<kHigh>(w.y), signed_codes<kHigh>(w.y >> 8))
                   : as_half8(signed_codes<kLow>(w.x), signed_codes<kLow>(w.x >> 8),
                              signed_codes<kLow>(w.y), signed_codes<kLow>(w.y >> 8));
           } else {
-            const u32x2 w = read_column(mine.v.codes + (2 * i + h) * mine.v.kPlane, lane);
+            const u32x2 w = read_column(mine.planes + (2 * i + h) * kPlane, lane);
             a = as_half8(signed_codes<kByte>(w.x), signed_codes<kByte>(w.x >> 8),
                          signed_codes<kByte>(w.y), signed_codes<kByte>(w.y >> 8));
           }
@@ -571,8 +739,32 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
       wave_sync();
     }
 
-    // join the waves
     const float l = groups_sum(st.l);
+    const int64_t row = at * p.heads + head * p.group + c % p.group;
+    // dimensions 16 i + 4 g .. + 3 of this lane's row
+    const auto put = [&](int i, f32x4 o, float sum) {
+      if (!live) return;
+      if (kVQ4 && (i & 1)) o *= 0.0625f;
+      const int dim = 16 * i + 4 * g;
+      if (p.splits == 1) {
+        const float inv = 1.0f / sum;
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : o[e] * inv;
+        store_f32<T, 4>(static_cast<T*>(p.out) + at * p.out_stride +
+                            ((int64_t)head * p.group + c % p.group) * D + dim,
+                        y);
+      } else {
+        *reinterpret_cast<f32x4*>(p.part_o + (row * p.splits + split) * D + dim) = o;
+      }
+    };
+    if (sub == 1) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) put(i, st.o[i], l);
+      if (live && p.splits > 1 && g == 0) p.part_ml[row * p.splits + split] = float2{st.m, l};
+      continue;
+    }
+    // join the waves of this head
     __syncthreads();
     f32x4* join = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
@@ -582,36 +774,24 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_split_kernel(
       join_l[wave][col] = l;
     }
     __syncthreads();
-    float m = join_m[0][col];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, join_m[w][col]);
+    const int first = wave - part;
+    float m = join_m[first][col];
+    for (int w = 1; w < sub; ++w) m = fmaxf(m, join_m[first + w][col]);
     const float ref = m == -INFINITY ? 0.0f : m;
     float weight[kWaves], sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      weight[w] = exp2_raw(join_m[w][col] - ref);
-      sum += weight[w] * join_l[w][col];
+      weight[w] = w < sub ? exp2_raw(join_m[first + w][col] - ref) : 0.0f;
+      sum += w < sub ? weight[w] * join_l[first + w][col] : 0.0f;
     }
-    const int64_t row = (((int64_t)b * p.kv_heads + head) * p.col_tiles + ct) * kCols + col;
-    for (int i = wave; i < D / 16; i += kWaves) {
-      f32x4 o = join[i * kWave + lane] * weight[0];
+    for (int i = part; i < D / 16; i += sub) {
+      f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) o += join[(w * (D / 16) + i) * kWave + lane] * weight[w];
-      if (kVQ4 && (i & 1)) o *= 0.0625f;
-      const int dim = 16 * i + 4 * g;
-      if (live && p.splits == 1) {
-        const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : NAN;
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : o[e] * inv;
-        T* dst = static_cast<T*>(p.out) + at * p.out_stride +
-                 ((int64_t)head * p.group + c % p.group) * D + dim;
-        store_f32<T, 4>(dst, y);
-      } else if (live) {
-        *reinterpret_cast<f32x4*>(p.part_o + (row * p.splits + split) * D + dim) = o;
-      }
+      for (int w = 0; w < kWaves; ++w)
+        if (w < sub) o += join[((first + w) * (D / 16) + i) * kWave + lane] * weight[w];
+      put(i, o, sum);
     }
-    if (live && p.splits > 1 && wave == 0 && g == 0)
+    if (live && p.splits > 1 && part == 0 && g == 0)
       p.part_ml[row * p.splits + split] = float2{m, sum};
     __syncthreads();  // the join's LDS is the next unit's
   }
@@ -626,30 +806,44 @@ template <int D, typename T>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p) {
   constexpr int kX = D / 4, kY = kJoinThreads / kX;
   __shared__ f32x4 part[kY][kX];
-  __shared__ float part_l[kY];
+  __shared__ float part_l[kY], wave_m[kJoinThreads / kWave];
   const int x = threadIdx.x % kX, y = threadIdx.x / kX;
-  const int64_t rows = (int64_t)p.n_seqs * p.kv_heads * p.col_tiles * kCols;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int64_t tile = row / kCols;
-    const int ct = (int)(tile % p.col_tiles);
-    const int head = (int)(tile / p.col_tiles % p.kv_heads);
-    const int b = (int)(tile / p.col_tiles / p.kv_heads);
+  const uint32_t rows = (uint32_t)(p.search ? p.n_tokens : p.n_seqs * p.max_q) * p.heads;
+  for (uint32_t id = blockIdx.x; id < rows; id += gridDim.x) {
+    const int head = (int)(id % p.heads);
+    int b, tok;
+    if (p.search) {
+      tok = (int)(id / p.heads);
+      b = find_last(p.n_seqs + 1, tok, [&](int i) { return p.q_start[i]; });
+      if (b == p.n_seqs) continue;
+      tok -= p.q_start[b];
+    } else {
+      b = (int)(id / p.heads) / p.max_q;
+      tok = (int)(id / p.heads) % p.max_q;
+    }
     const Seq s = sequence(p, b);
-    const int c = ct * kCols + (int)(row % kCols);
-    if (c >= s.nq * p.group) continue;
-    const int64_t at = (int64_t)s.t0 + c / p.group;
-    if (at < 0 || at >= p.n_tokens) continue;
-    const int splits = tile_span(p, s, ct).splits;
+    const int64_t at = (int64_t)s.t0 + tok;
+    if (tok < 0 || tok >= s.nq || at < 0 || at >= p.n_tokens) continue;
+    const int64_t row = at * p.heads + head;
+    const int splits = tile_span(p, s, (tok * p.group + head % p.group) / kCols).splits;
     const float2* ml = p.part_ml + row * p.splits;
     float m = -INFINITY;
-    for (int i = 0; i < splits; ++i) m = fmaxf(m, ml[i].x);
+    for (int i = threadIdx.x; i < splits; i += kJoinThreads) m = fmaxf(m, ml[i].x);
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) m = fmaxf(m, shfl_xor_f(m, k));
+    if ((threadIdx.x & 63) == 0) wave_m[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / kWave; ++k) m = fmaxf(m, wave_m[k]);
     const float ref = m == -INFINITY ? 0.0f : m;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     float l = 0.0f;
+    const float* src = p.part_o + row * p.splits * D + 4 * x;
+#pragma unroll 4
     for (int i = y; i < splits; i += kY) {
       const float w = exp2_raw(ml[i].x - ref);
       l += w * ml[i].y;
-      o += w * *reinterpret_cast<const f32x4*>(p.part_o + (row * p.splits + i) * D + 4 * x);
+      o += w * *reinterpret_cast<const f32x4*>(src + (int64_t)i * D);
     }
     part[y][x] = o;
     if (x == 0) part_l[y] = l;
@@ -663,17 +857,23 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
       float r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[e] = l == 0.0f ? 0.0f : o[e] * inv;
-      store_f32<T, 4>(static_cast<T*>(p.out) + at * p.out_stride +
-                          ((int64_t)head * p.group + c % p.group) * D + 4 * x,
-                      r);
+      store_f32<T, 4>(static_cast<T*>(p.out) + at * p.out_stride + (int64_t)head * D + 4 * x, r);
     }
     __syncthreads();
   }
 }
 
+constexpr int64_t kMaxGrid = 1 << 22;
+constexpr int64_t kFill = 3072;      // waves that fill the GPU
+constexpr int64_t kMinChunk = 256;   // cells of a split that a workgroup shares
+constexpr int64_t kMaxChunk = 512;   // cells of a split
+constexpr int64_t kMaxUnits = 32768; // tiles and heads from which on nothing is split
+
 // How the cells are divided, from host values alone.
 struct Plan {
-  int64_t col_tiles, splits, chunk, rows;
+  int64_t col_tiles, tiles, splits, chunk, rows;
+  int heads_shift;  // log2 of the cache heads of a workgroup
+  bool search;
 };
 
 Plan plan(const qmat_attn_args& a) {
@@ -681,19 +881,34 @@ Plan plan(const qmat_attn_args& a) {
   const int64_t group = a.heads / a.kv_heads;
   const int64_t max_q = a.max_q < a.n_tokens ? a.max_q : a.n_tokens;
   r.col_tiles = (max_q * group + kCols - 1) / kCols;
+  // Column tiles by sequence where every sequence may have max_q tokens, or by
+  // their place among all tokens where those bound them better.
+  const int64_t by_token = a.n_tokens * group / kCols + a.n_seqs;
+  r.search = a.n_seqs * r.col_tiles > by_token;
+  r.tiles = r.search ? by_token : a.n_seqs * r.col_tiles;
   const int64_t limit = a.pages_per_seq * a.page_size;
   int64_t cells = a.max_kv < limit ? a.max_kv : limit;
   if (a.window > 0 && a.window + max_q < cells) cells = a.window + max_q;
-  const int64_t units = a.n_seqs * a.kv_heads * r.col_tiles;
+  const int64_t units = r.tiles * a.kv_heads;
   const int64_t step = kWaves * kCells;
-  // enough workgroups for every CU twice over and for uneven lengths, but no
-  // split below two tiles a wave
-  const int64_t want = (1024 + units - 1) / (units > 0 ? units : 1);
-  int64_t chunk = ((cells + want - 1) / want + step - 1) / step * step;
-  if (chunk < 2 * step) chunk = 2 * step;
-  r.chunk = chunk;
-  r.splits = cells > chunk ? (cells + chunk - 1) / chunk : 1;
-  r.rows = a.n_seqs * a.kv_heads * r.col_tiles * kCols;
+  // Where sequences and heads alone make enough waves, a wave takes a head,
+  // and pieces of kMaxChunk cells, so that the lengths of a ragged batch do not
+  // decide how long the last CU works. Otherwise the waves of a workgroup share
+  // a head's piece, none of fewer than two tiles a wave.
+  r.splits = 1;
+  r.chunk = step;
+  r.heads_shift = 0;
+  const int64_t pieces = (cells + kMaxChunk - 1) / kMaxChunk;
+  if (units >= kFill || units * pieces >= kFill) {
+    while (r.heads_shift < 2 && (a.kv_heads >> r.heads_shift) % 2 == 0) ++r.heads_shift;
+    r.chunk = kMaxChunk;
+    if (units < kMaxUnits && pieces > 1) r.splits = pieces;
+  } else if (cells > kMinChunk) {
+    const int64_t chunk = (cells * units * kWaves / kFill + step - 1) / step * step;
+    r.chunk = chunk < kMinChunk ? kMinChunk : chunk;
+    r.splits = (cells + r.chunk - 1) / r.chunk;
+  }
+  r.rows = a.n_tokens * a.heads;
   return r;
 }
 
@@ -705,12 +920,19 @@ int log2_of(int64_t v) {
 
 template <int D, typename T>
 void launch_for(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
-  const int64_t units = (int64_t)p.n_seqs * p.splits;
-  const int64_t total = (p.by_unit ? (units + 7) / 8 * 8 : units) * p.kv_heads * p.col_tiles;
-  const dim3 grid((unsigned)(total < (1 << 22) ? total : (1 << 22)));
+  const int64_t inner = (int64_t)(p.kv_heads >> p.heads_shift) * (p.search ? 1 : p.col_tiles);
+  const int64_t units = (int64_t)(p.search ? p.tiles : p.n_seqs) * p.splits;
+  const int64_t total = (p.by_unit ? (units + 7) / 8 * 8 : units) * inner;
+  const dim3 grid((unsigned)(total < kMaxGrid ? total : kMaxGrid));
   const auto go = [&](auto kq, auto vq) {
-    hipLaunchKernelGGL((attn_split_kernel<D, decltype(kq)::value, decltype(vq)::value, T>), grid,
-                       dim3(kThreads), 0, stream, p);
+    if (p.page_shift >= 5)
+      hipLaunchKernelGGL(
+          (attn_split_kernel<D, decltype(kq)::value, decltype(vq)::value, true, T>), grid,
+          dim3(kThreads), 0, stream, p);
+    else
+      hipLaunchKernelGGL(
+          (attn_split_kernel<D, decltype(kq)::value, decltype(vq)::value, false, T>), grid,
+          dim3(kThreads), 0, stream, p);
   };
   const std::true_type q4{};
   const std::false_type q8{};
@@ -719,10 +941,10 @@ void launch_for(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
   else
     a.v_fmt == kFmtQ4_0 ? go(q8, q4) : go(q8, q8);
   if (p.splits > 1) {
-    const int64_t rows = (int64_t)p.n_seqs * p.kv_heads * p.col_tiles * kCols;
+    const int64_t rows = (int64_t)(p.search ? p.n_tokens : p.n_seqs * p.max_q) * p.heads;
     hipLaunchKernelGGL((attn_join_kernel<D, T>),
-                       dim3((unsigned)(rows < (1 << 22) ? rows : (1 << 22))), dim3(kJoinThreads),
-                       0, stream, p);
+                       dim3((unsigned)(rows < kMaxGrid ? rows : kMaxGrid)), dim3(kJoinThreads), 0,
+                       stream, p);
   }
 }
 
@@ -774,9 +996,12 @@ hipError_t launch_attn(const qmat_attn_args& a, void* workspace, hipStream_t str
   p.causal = a.causal != 0;
   p.window = a.window < p.max_cells ? (int)a.window : 0;  // a wider one hides nothing ...
   p.col_tiles = (int)r.col_tiles;
+  p.tiles = (int)r.tiles;
+  p.search = r.search;
+  p.heads_shift = r.heads_shift;
+  p.by_unit = (r.search ? r.tiles : a.n_seqs) * r.splits >= 32;
   p.splits = (int)r.splits;
   p.chunk = (int)r.chunk;
-  p.by_unit = a.n_seqs * r.splits >= 32;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   if (a.dtype == kDtypeF32)
     launch_as<float>(a, p, stream);
