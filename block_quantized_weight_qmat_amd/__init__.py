@@ -8,7 +8,7 @@ The compute lives in the HIP library ``libqmat.so`` (C ABI in
 from __future__ import annotations
 
 __all__ = ["quantize", "gemv", "gemv_batch", "gemv_jobs", "gemm", "gemm_ws", "gemm_workspace_bytes", "prefill", "prefill_noalloc", "kv_write",
-           "kv_store", "kv_load", "attn", "attn_workspace_bytes",
+           "kv_store", "kv_load", "attn", "attn_args", "attn_workspace_bytes",
            "block_elems", "block_bytes", "row_bytes", "noalloc_scratch_bytes",
            "Q4_0", "Q8_0", "Q4_K", "Q6_K", "FORMATS", "QmatError", "library_path"]
 
@@ -19,5 +19,6 @@ def __getattr__(name):
     # The binding imports torch; load it only when an entry point is used.
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found here from now on
+        return value
     raise AttributeError(name)

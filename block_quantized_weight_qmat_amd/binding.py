@@ -341,60 +341,92 @@ def kv_write(fmt, rows: torch.Tensor, cache: torch.Tensor, cell0: int,
     return cache
 
 
-def _rows2d(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
+_BLOCK_BYTES = {Q4_0: 18, Q8_0: 34}
+_CACHE_FORMATS = {"q4_0": Q4_0, "q8_0": Q8_0, "Q4_0": Q4_0, "Q8_0": Q8_0, Q4_0: Q4_0, Q8_0: Q8_0}
+
+
+def _cache_fmt(fmt) -> int:
+    f = _CACHE_FORMATS.get(fmt)
+    if f is None:
+        raise ValueError(f"a cache is in q4_0 or q8_0, not {fmt!r}")
+    return f
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
     """Token stride of t, a GPU tensor [n, ...] whose rows are contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor (no CPU path exists)")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
     row = 1
-    for d in range(t.dim() - 1, 0, -1):
-        if t.shape[d] != 1 and t.stride(d) != row:
+    for d in range(len(shape) - 1, 0, -1):
+        if shape[d] != 1 and stride[d] != row:
             raise ValueError(f"the rows of {name} must be contiguous")
-        row *= t.shape[d]
-    return t.stride(0) if t.shape[0] > 1 else max(row, 1)
+        row *= shape[d]
+    return stride[0] if shape[0] > 1 else max(row, 1)
 
 
-def _same_device(**tensors):
-    first = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if first is None:
-            first = t.device
-        elif t.device != first:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {first}")
+def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or \
+            not t.is_contiguous():
+        _gpu(t, name, dtype)
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
 
 
 def _dtype(dtype) -> int:
-    if dtype not in DTYPES:
+    d = DTYPES.get(dtype)
+    if d is None:
         raise TypeError(f"element type must be one of {list(DTYPES)}, got {dtype}")
-    return DTYPES[dtype]
+    return d
 
 
-def _kv_rows(k_fmt, v_fmt, k, v, slots, k_cache, v_cache, k_bias, dim: int):
+def _launch(func: str, call, device: torch.device, *args):
+    """call(*args, stream) with device current and on its current stream."""
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        _check(func, status)
+
+
+def _caches(kf, vf, k_cache, v_cache, dim: int, device) -> int:
+    """Cells of the two caches, whose rows hold dim elements each."""
+    _flat(k_cache, "k_cache", torch.uint8, device)
+    _flat(v_cache, "v_cache", torch.uint8, device)
+    if dim % 32 != 0:
+        raise ValueError(f"{dim} elements per cell are not whole blocks of 32")
+    ks, vs = k_cache.shape, v_cache.shape
+    if len(ks) != 2 or len(vs) != 2 or ks[0] != vs[0]:
+        raise ValueError("k_cache and v_cache must be 2-D with the same cells")
+    if ks[1] != dim // 32 * _BLOCK_BYTES[kf] or vs[1] != dim // 32 * _BLOCK_BYTES[vf]:
+        raise ValueError("cache rows do not match the formats and the elements per cell")
+    return ks[0]
+
+
+def _kv_args(k_fmt, v_fmt, k, v, slots, k_cache, v_cache, k_bias, dim: int):
     """Checks common to kv_store and kv_load; returns (k_fmt, v_fmt, dtype,
     k_stride, v_stride, k_bias pointer, n, cells)."""
-    kf, vf, dt = _fmt(k_fmt), _fmt(v_fmt), _dtype(k.dtype)
-    ks, vs = _rows2d(k, "k", k.dtype), _rows2d(v, "v", k.dtype)
-    _gpu(slots, "slots", torch.int32)
-    _gpu(k_cache, "k_cache", torch.uint8)
-    _gpu(v_cache, "v_cache", torch.uint8)
+    kf, vf, dt = _cache_fmt(k_fmt), _cache_fmt(v_fmt), _dtype(k.dtype)
+    ks, vs = _rows(k, "k", k.dtype), _rows(v, "v", k.dtype)
+    device = k.device
+    _flat(slots, "slots", torch.int32, device)
+    cells = _caches(kf, vf, k_cache, v_cache, dim, device)
     n = slots.numel()
+    if v.device != device:
+        raise ValueError(f"v is on {v.device}, the other tensors on {device}")
     if k.shape[0] != n or v.shape[0] != n or k.numel() != n * dim or v.numel() != n * dim:
         raise ValueError("k, v and slots do not match")
-    if k_cache.dim() != 2 or v_cache.dim() != 2 or k_cache.shape[0] != v_cache.shape[0]:
-        raise ValueError("k_cache and v_cache must be 2-D with the same cells")
-    if k_cache.shape[1] != row_bytes(kf, dim) or v_cache.shape[1] != row_bytes(vf, dim):
-        raise ValueError("cache rows do not match the formats and dim")
     bp = None
     if k_bias is not None:
-        _gpu(k_bias, "k_bias", torch.float32)
+        _flat(k_bias, "k_bias", torch.float32, device)
         if k_bias.numel() != dim:
             raise ValueError("k_bias must hold dim values")
         bp = k_bias.data_ptr()
-    _same_device(k=k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache, k_bias=k_bias)
-    return kf, vf, dt, ks, vs, bp, n, k_cache.shape[0]
+    return kf, vf, dt, ks, vs, bp, n, cells
 
 
 def kv_store(k_fmt, v_fmt, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -405,12 +437,11 @@ def kv_store(k_fmt, v_fmt, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     cells slots [n] (int32) of k_cache and v_cache (uint8 [cells,
     row_bytes(fmt, dim)]); a slot outside the cache skips its row."""
     dim = math.prod(k.shape[1:])
-    kf, vf, dt, ks, vs, bp, n, cells = _kv_rows(k_fmt, v_fmt, k, v, slots, k_cache, v_cache,
+    kf, vf, dt, ks, vs, bp, n, cells = _kv_args(k_fmt, v_fmt, k, v, slots, k_cache, v_cache,
                                                 k_bias, dim)
-    with torch.cuda.device(k.device):
-        _check("qmat_kv_store", load_library().qmat_kv_store(
-            kf, vf, dt, k.data_ptr(), ks, v.data_ptr(), vs, bp, slots.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), n, cells, dim, _stream(k)))
+    _launch("qmat_kv_store", load_library().qmat_kv_store, k.device, kf, vf, dt, k.data_ptr(), ks,
+            v.data_ptr(), vs, bp, slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), n,
+            cells, dim)
     return k_cache, v_cache
 
 
@@ -420,6 +451,8 @@ def kv_load(k_fmt, v_fmt, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: t
             v: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """Rows (k, v) [n, dim] of the cells slots [n] (int32), dequantized to
     dtype (K plus k_bias if given); a slot outside the cache gives zeros."""
+    if not isinstance(slots, torch.Tensor) or not slots.is_cuda:
+        raise TypeError("slots must be a GPU tensor (no CPU path exists)")
     n = slots.numel()
     if k is None:
         k = torch.empty((n, dim), dtype=dtype, device=slots.device)
@@ -427,12 +460,11 @@ def kv_load(k_fmt, v_fmt, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: t
         v = torch.empty((n, dim), dtype=dtype, device=slots.device)
     if k.dtype != dtype:
         raise TypeError(f"k must be {dtype}, got {k.dtype}")
-    kf, vf, dt, ks, vs, bp, n, cells = _kv_rows(k_fmt, v_fmt, k, v, slots, k_cache, v_cache,
+    kf, vf, dt, ks, vs, bp, n, cells = _kv_args(k_fmt, v_fmt, k, v, slots, k_cache, v_cache,
                                                 k_bias, dim)
-    with torch.cuda.device(k.device):
-        _check("qmat_kv_load", load_library().qmat_kv_load(
-            kf, vf, dt, k_cache.data_ptr(), v_cache.data_ptr(), bp, slots.data_ptr(),
-            k.data_ptr(), ks, v.data_ptr(), vs, n, cells, dim, _stream(k)))
+    _launch("qmat_kv_load", load_library().qmat_kv_load, k.device, kf, vf, dt, k_cache.data_ptr(),
+            v_cache.data_ptr(), bp, slots.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, n, cells,
+            dim)
     return k, v
 
 
@@ -442,6 +474,38 @@ def attn_workspace_bytes(args: AttnArgs) -> int:
     if n < 0:
         raise ValueError("invalid attention shape, formats or element type")
     return n
+
+
+def attn_args(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              page_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, kv_heads: int,
+              page_size: int, out: torch.Tensor, scale: float | None = None, causal: bool = True,
+              window: int = 0, max_q: int | None = None, max_kv: int | None = None) -> AttnArgs:
+    """The checked argument struct of attn (for attn_workspace_bytes, and for
+    callers of the C ABI); it holds raw pointers."""
+    kf, vf, dt = _cache_fmt(k_fmt), _cache_fmt(v_fmt), _dtype(q.dtype)
+    qs, os_ = _rows(q, "q", q.dtype), _rows(out, "out", q.dtype)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be 3-D [tokens, heads, head_dim]")
+    T, heads, head_dim = shape
+    device = q.device
+    if out.shape != shape or out.device != device:
+        raise ValueError("out must have the shape and device of q")
+    _flat(page_table, "page_table", torch.int32, device)
+    _flat(q_start, "q_start", torch.int32, device)
+    _flat(kv_len, "kv_len", torch.int32, device)
+    n_seqs = kv_len.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n_seqs or q_start.numel() != n_seqs + 1:
+        raise ValueError("page_table, q_start and kv_len do not match")
+    cells = _caches(kf, vf, k_cache, v_cache, kv_heads * head_dim, device)
+    pages = page_table.shape[1]
+    return AttnArgs(kf, vf, dt, 1 if causal else 0, q.data_ptr(), out.data_ptr(),
+                    k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+                    q_start.data_ptr(), kv_len.data_ptr(), qs, os_, T, n_seqs,
+                    T if max_q is None else max_q,
+                    pages * page_size if max_kv is None else max_kv, heads, kv_heads, head_dim,
+                    cells, page_size, pages, window,
+                    head_dim ** -0.5 if scale is None else scale)
 
 
 def attn(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -458,51 +522,21 @@ def attn(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     workspace of attn_workspace_bytes() is allocated when none is given. Rows
     of out that belong to no sequence are left as they were (zeros in an out
     allocated here)."""
-    kf, vf, dt = _fmt(k_fmt), _fmt(v_fmt), _dtype(q.dtype)
-    if q.dim() != 3:
-        raise ValueError("q must be 3-D [tokens, heads, head_dim]")
-    T, heads, head_dim = q.shape
-    qs = _rows2d(q, "q", q.dtype)
     if out is None:
-        out = torch.zeros((T, heads, head_dim), dtype=q.dtype, device=q.device)
-    os_ = _rows2d(out, "out", q.dtype)
-    if out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    for t, name in ((page_table, "page_table"), (q_start, "q_start"), (kv_len, "kv_len")):
-        _gpu(t, name, torch.int32)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _gpu(t, name, torch.uint8)
-    n_seqs = kv_len.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != n_seqs or q_start.numel() != n_seqs + 1:
-        raise ValueError("page_table, q_start and kv_len do not match")
-    dim = kv_heads * head_dim
-    if k_cache.dim() != 2 or v_cache.dim() != 2 or k_cache.shape[0] != v_cache.shape[0]:
-        raise ValueError("k_cache and v_cache must be 2-D with the same cells")
-    if k_cache.shape[1] != row_bytes(kf, dim) or v_cache.shape[1] != row_bytes(vf, dim):
-        raise ValueError("cache rows do not match the formats, kv_heads and head_dim")
-    _same_device(q=q, out=out, k_cache=k_cache, v_cache=v_cache, page_table=page_table,
-                 q_start=q_start, kv_len=kv_len, workspace=workspace)
-    a = AttnArgs()
-    a.k_fmt, a.v_fmt, a.dtype, a.causal = kf, vf, dt, 1 if causal else 0
-    a.q, a.out, a.q_stride, a.out_stride = q.data_ptr(), out.data_ptr(), qs, os_
-    a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-    a.page_table, a.q_start, a.kv_len = (page_table.data_ptr(), q_start.data_ptr(),
-                                         kv_len.data_ptr())
-    a.n_tokens, a.n_seqs = T, n_seqs
-    a.max_q = T if max_q is None else int(max_q)
-    a.max_kv = page_table.shape[1] * page_size if max_kv is None else int(max_kv)
-    a.heads, a.kv_heads, a.head_dim = heads, kv_heads, head_dim
-    a.cells, a.page_size, a.pages_per_seq = k_cache.shape[0], page_size, page_table.shape[1]
-    a.window = int(window)
-    a.scale = head_dim ** -0.5 if scale is None else float(scale)
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    a = attn_args(k_fmt, v_fmt, q, k_cache, v_cache, page_table, q_start, kv_len, kv_heads,
+                  page_size, out, scale, causal, window, max_q, max_kv)
     lib = load_library()
-    need = int(lib.qmat_attn_workspace_bytes(ctypes.byref(a)))
-    if need > 0 and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if workspace is not None:
-        _gpu(workspace, "workspace", torch.uint8)
-    wp = workspace.data_ptr() if workspace is not None else None
-    wn = workspace.numel() if workspace is not None else 0
-    with torch.cuda.device(q.device):
-        _check("qmat_attn", lib.qmat_attn(ctypes.byref(a), wp, wn, _stream(q)))
+    ref = ctypes.byref(a)
+    if workspace is None:
+        need = lib.qmat_attn_workspace_bytes(ref)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _flat(workspace, "workspace", torch.uint8, q.device)
+    if workspace is None:
+        _launch("qmat_attn", lib.qmat_attn, q.device, ref, None, 0)
+    else:
+        _launch("qmat_attn", lib.qmat_attn, q.device, ref, workspace.data_ptr(),
+                workspace.numel())
     return out

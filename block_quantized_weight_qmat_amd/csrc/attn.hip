@@ -42,6 +42,7 @@ constexpr int kCols = 16;   // query rows of a tile
 constexpr int kCells = 32;  // cells of a tile
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
+constexpr int kMaxItems = 1024;  // items whose tiles are dealt out together
 
 struct Params {
   const void* q;
@@ -51,14 +52,16 @@ struct Params {
   const int32_t* table;
   const int32_t* q_start;
   const int32_t* kv_len;
-  float* part_o;    // [token][head][split][D], not divided by the sum
-  float2* part_ml;  // [token][head][split]: reference and sum
+  // Partial results of a share's part of an item, which share + item numbers:
+  float* part_o;    // [share + item][head][row of the tile][D], not divided by the sum
+  float2* part_ml;  // [share + item][head][row of the tile]: reference and sum
+  int32_t* starts;  // [items + 1]: an item's first tile among all items'
   int64_t q_stride, out_stride, k_row, v_row;
   int n_tokens, n_seqs, max_q, heads, kv_heads, group;
-  int tiles, search;  // column tiles, found by their place among all tokens
+  int items, search;  // column tiles; found by their place among all tokens
   int page_shift, n_pages, pages_per_seq, max_cells;
   int causal, window;  // window 0: none
-  int col_tiles, splits, chunk, by_unit, heads_shift;
+  int col_tiles, part_rows, shares, heads_shift;
   float scale_log2;
 };
 
@@ -88,24 +91,38 @@ __device__ __forceinline__ int last_cell(const Params& p, const Seq& s, int i) {
   return p.causal == 0 ? s.len : hi > 0 ? hi : 0;
 }
 
-// What a column tile's rows see together, its start rounded down to a tile,
-// and how many splits that takes.
+// The cells that a column tile's rows see together, in whole tiles from a
+// multiple of 32 on.
 struct Span {
-  int lo, hi, splits;
+  int lo, hi;
+  __device__ __forceinline__ int tiles() const { return (hi - lo + kCells - 1) / kCells; }
 };
 
 __device__ __forceinline__ Span tile_span(const Params& p, const Seq& s, int ct) {
-  Span r{0, 0, 0};
   const int c0 = ct * kCols;
-  if (c0 >= s.nq * p.group) return r;
+  if (c0 >= s.nq * p.group) return Span{0, 0};
   const int i1 = (c0 + kCols - 1) / p.group;
-  r.lo = first_cell(p, s, c0 / p.group) & ~(kCells - 1);
-  r.hi = last_cell(p, s, i1 < s.nq ? i1 : s.nq - 1);
-  if (r.hi > r.lo) {
-    const int n = (r.hi - r.lo + p.chunk - 1) / p.chunk;
-    r.splits = n < p.splits ? n : p.splits;
-  }
-  return r;
+  const int lo = first_cell(p, s, c0 / p.group) & ~(kCells - 1);
+  const int hi = last_cell(p, s, i1 < s.nq ? i1 : s.nq - 1);
+  return Span{lo, hi > lo ? hi : lo};
+}
+
+// Tiles of all items are dealt out evenly to at most p.shares shares, at least
+// one to each: share w has those in [share_start(w), share_start(w + 1)).
+__device__ __forceinline__ int share_count(const Params& p, int total) {
+  return p.shares < total ? p.shares : total;
+}
+
+__device__ __forceinline__ int share_start(int w, int shares, int total) {
+  return (int)((uint64_t)w * (uint32_t)total / (uint32_t)shares);
+}
+
+// The share that has tile x.
+__device__ __forceinline__ int share_of(int x, int shares, int total) {
+  int w = (int)((uint64_t)x * (uint32_t)shares / (uint32_t)total);
+  while (w + 1 < shares && share_start(w + 1, shares, total) <= x) ++w;
+  while (w > 0 && share_start(w, shares, total) > x) --w;
+  return w;
 }
 
 // Sequence b's first column tile among those of all tokens: tiles never span
@@ -280,28 +297,22 @@ __device__ __forceinline__ void write_raw(uint8_t* raw, const TileRegs<D, kQ4>& 
     reinterpret_cast<Unit*>(raw)[i * kWave + lane] = t.u[i];
 }
 
-// N words of a raw piece from an address that is `shift` (2 or 0) bytes past a
-// multiple of 4: LDS reads off their alignment would go lane by lane.
-template <int N, int kShift>
-__device__ __forceinline__ void read_words_at(const uint8_t* at, uint32_t* w) {
-  const uint32_t* p = reinterpret_cast<const uint32_t*>(at - kShift);
-  uint32_t t[N + 1];
+// Code words of a raw piece from an address that is 2 or 0 bytes past a multiple
+// of 4: LDS reads off their alignment would go lane by lane. Aligned words
+// first (one more where there is something to shift), shifted later.
+template <int N>
+__device__ __forceinline__ void read_aligned(const uint8_t* at, uint32_t* t) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(at);
 #pragma unroll
-  for (int i = 0; i < N + (kShift != 0); ++i) t[i] = p[i];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    w[i] = kShift == 0 ? t[i] : __builtin_amdgcn_alignbyte(t[i + (kShift != 0)], t[i], kShift);
+  for (int i = 0; i < N; ++i) t[i] = p[i];
 }
 
-template <int N>
-__device__ __forceinline__ void read_words(const uint8_t* at, uint32_t shift, uint32_t* w) {
-  const uint32_t* p = reinterpret_cast<const uint32_t*>(at - shift);
-  uint32_t t[N + 1];
-#pragma unroll
-  for (int i = 0; i <= N; ++i) t[i] = p[i];
-#pragma unroll
-  for (int i = 0; i < N; ++i) w[i] = __builtin_amdgcn_alignbyte(t[i + 1], t[i], shift);
+__device__ __forceinline__ uint32_t shifted(const uint32_t* t, int i, uint32_t bytes) {
+  return __builtin_amdgcn_alignbyte(t[i + 1], t[i], bytes);
 }
+
+// Nothing moves over this line: reads before it are under way together.
+__device__ __forceinline__ void reads_end() { __builtin_amdgcn_sched_barrier(0); }
 
 typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
 
@@ -386,14 +397,72 @@ struct State {
   int e;            // exponent field of the largest V scale so far
 };
 
-// One workgroup: one sequence, cache head, column tile and split; its waves
-// take the split's 32-cell tiles in turn, each with its own LDS and no barrier,
-// and join at the end.
+// The items' tiles summed up: starts[i] is item i's first, starts[items] their
+// number, which is returned. An item that sees nothing counts as one tile, so
+// that somebody writes its zeros; one without rows has none.
+__device__ __forceinline__ int count_tiles(const Params& p, int* starts, bool keep) {
+  constexpr int kEach = kMaxItems / kThreads;
+  __shared__ int wave_sum[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int n[kEach], sum = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int item = threadIdx.x * kEach + e;
+    n[e] = 0;
+    if (item < p.items) {
+      const Seq s = sequence(p, item / p.col_tiles);
+      const int ct = item % p.col_tiles;
+      const int tiles = tile_span(p, s, ct).tiles();
+      n[e] = ct * kCols >= s.nq * p.group ? 0 : tiles > 0 ? tiles : 1;
+    }
+    sum += n[e];
+  }
+  int before = sum;  // of this lane and those before it
+#pragma unroll
+  for (int k = 1; k < kWave; k <<= 1) {
+    const int v = __shfl_up(before, k, kWave);
+    before += lane >= k ? v : 0;
+  }
+  if (lane == kWave - 1) wave_sum[wave] = before;
+  __syncthreads();
+  before -= sum;
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? wave_sum[w] : 0;
+    total += wave_sum[w];
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int item = threadIdx.x * kEach + e;
+    if (item < p.items) {
+      starts[item] = before;
+      if (keep) p.starts[item] = before;
+    }
+    before += n[e];
+  }
+  if (threadIdx.x == 0) {
+    starts[p.items] = total;
+    if (keep) p.starts[p.items] = total;
+  }
+  __syncthreads();
+  return total;
+}
+
+// An item is a column tile of a sequence. With p.shares == 0 a workgroup has
+// one item and one to four cache heads. Otherwise every workgroup has the same
+// number of tiles (a share of those of all items, for its heads): it starts
+// inside one item, may pass several and ends inside another, so that neither
+// few long sequences nor ragged ones leave CUs idle. What shares have of an
+// item that is not theirs alone is joined by a second kernel.
+//
+// The waves take a head each, or share the tiles of a head and join at the end;
+// each has its own LDS, and no barrier in its loop.
 //
 // kWhole: pages of 32 cells or more, which hold whole tiles, so that a tile's
 // page is one number for the wave. Smaller pages: one per cell.
 template <int D, bool kKQ4, bool kVQ4, bool kWhole, typename T>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3)
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 || !kWhole ? 2 : 3)
 void attn_split_kernel(const Params p) {
   constexpr bool kPair = sizeof(T) == 4;
   constexpr int kNb = D / 32;
@@ -404,6 +473,7 @@ void attn_split_kernel(const Params p) {
   typedef WaveLds<D, kKQ4, kVQ4> Lds;
   constexpr int kJoin = kWaves * (D / 16) * kWave * 16;
   constexpr int kLds = (int)sizeof(Lds) * kWaves > kJoin ? (int)sizeof(Lds) * kWaves : kJoin;
+  __shared__ int starts[kMaxItems + 1];
   __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   __shared__ float join_m[kWaves][kCols], join_l[kWaves][kCols];
 
@@ -420,39 +490,33 @@ void attn_split_kernel(const Params p) {
   for (int i = 0; i < VP::kLoads; ++i)
     v_off[i] = kKQ4 == kVQ4 ? k_off[i] : VP::cell(i, lane) * (uint32_t)p.v_row + VP::byte(i, lane);
 
-  // Workgroups go to the 8 XCDs in turn. All heads (and column tiles) of one
-  // sequence and split get the same XCD, whose L2 then holds the cache lines
-  // they share; too few such units for 8 XCDs are dealt out head by head.
-  // A workgroup's waves share a split's tiles of one head, or take a head each.
   const int sub = kWaves >> p.heads_shift;  // waves per head
   const int part = wave & (sub - 1);
   const uint32_t head_groups = (uint32_t)p.kv_heads >> p.heads_shift;
-  const uint32_t inner = head_groups * (p.search ? 1 : p.col_tiles);
-  const uint32_t units = (uint32_t)(p.search ? p.tiles : p.n_seqs) * p.splits;
-  const uint32_t total = p.by_unit ? (units + 7) / 8 * 8 * inner : units * inner;
-  for (uint32_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const uint32_t turn = p.by_unit ? id >> 3 : id;
-    const uint32_t unit = p.by_unit ? turn / inner * 8 + (id & 7) : turn / inner;
-    if (unit >= units) continue;
-    const uint32_t in = turn % inner;
-    const int head = (int)(in % head_groups << p.heads_shift) + (wave >> (2 - p.heads_shift));
-    const int split = (int)(unit % p.splits);
-    int b = (int)(unit / p.splits), ct = p.col_tiles - 1 - (int)(in / head_groups);
+  // Workgroups go to the 8 XCDs in turn. All heads of one share get the same
+  // XCD, whose L2 then holds the cache lines they have in common.
+  const bool shared = p.shares > 0;
+  const int all_tiles = shared ? count_tiles(p, starts, blockIdx.x == 0) : 0;
+  const int shares = share_count(p, all_tiles);
+  const uint32_t units = shared ? shares : p.items;
+  const bool by_unit = units >= 32;
+  const uint32_t total = (by_unit ? (units + 7) / 8 * 8 : units) * head_groups;
+
+  // Tiles [from, to) of an item; place: of its partial result, -1: the item is
+  // this workgroup's alone.
+  const auto work = [&](int head, int item, int from, int to, int place) {
+    int b = item / p.col_tiles, ct = item % p.col_tiles;
     if (p.search) {
-      const int x = p.tiles - 1 - b;  // late tiles first: causal ones see more
+      const int x = p.items - 1 - item;  // late tiles first: causal ones see more
       b = find_last(p.n_seqs, x, [&](int i) { return first_tile(p, i); });
       ct = x - first_tile(p, b);
-      if (ct < 0) continue;
     }
     const Seq s = sequence(p, b);
     const int cols = s.nq * p.group;
-    if (ct * kCols >= cols) continue;
+    if (ct < 0 || ct * kCols >= cols) return;
     const Span span = tile_span(p, s, ct);
-    // a tile that sees nothing still writes its zeros where nothing joins it
-    if (split >= span.splits && (p.splits > 1 || split > 0)) continue;
-    const int begin = span.lo + split * p.chunk;
-    const int end = split == p.splits - 1 || span.hi - begin < p.chunk ? span.hi
-                                                                       : begin + p.chunk;
+    const int begin = span.lo + from * kCells;
+    const int end = to < span.tiles() ? span.lo + to * kCells : span.hi;
 
     // this lane's query row
     const int c = ct * kCols + col;
@@ -587,20 +651,42 @@ void attn_split_kernel(const Params p) {
       load_page(j0 + 2 * step);
       if (seen == 0) continue;
       wave_sync();
+      // This lane's blocks' scales and V codes, and its operands' K codes.
+      constexpr int kKW = kKQ4 ? 1 : 2;  // K code words of an operand
+      uint32_t k_d[kPer], v_d[kPer], v_w[kPer][VP::kWords + 1], k_w[2][kNb][kKW + 1];
+      const int blk = lane % kNb;
+      const uint32_t v_shift = blk & 1 ? 0 : 2;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int cell = i * kStep + lane / kNb;
+        k_d[i] = *reinterpret_cast<const uint16_t*>(mine.k + cell * KP::kBytes + blk * KP::kBB);
+        const uint8_t* vp = mine.v + cell * VP::kBytes + blk * VP::kBB;
+        v_d[i] = *reinterpret_cast<const uint16_t*>(vp);
+        read_aligned<VP::kWords + 1>(vp + 2 - v_shift, v_w[i]);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int cell = 8 * (col >> 2) + 4 * t + (col & 3);
+        const uint8_t* kp = mine.k + cell * KP::kBytes + 4 * kKW * g;
+#pragma unroll
+        for (int i = 0; i < kNb; ++i) {
+          if (i & 1)
+            read_aligned<kKW>(kp + i * KP::kBB + 2, k_w[t][i]);
+          else
+            read_aligned<kKW + 1>(kp + i * KP::kBB, k_w[t][i]);
+        }
+      }
+      reads_end();
       // scales side by side, V's codes into planes
       uint32_t d_max = 0u;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int cell = i * kStep + lane / kNb, blk = lane % kNb;
-        mine.kd[cell * kNb + blk] =
-            *reinterpret_cast<const uint16_t*>(mine.k + cell * KP::kBytes + blk * KP::kBB);
-        const uint8_t* vp = mine.v + cell * VP::kBytes + blk * VP::kBB;
-        const uint32_t d = *reinterpret_cast<const uint16_t*>(vp);
-        mine.vd[cell * kNb + blk] = (uint16_t)d;
-        const uint32_t size = (seen >> cell) & 1 ? d & 0x7FFFu : 0u;
-        d_max = size > d_max ? size : d_max;
+        const int cell = i * kStep + lane / kNb;
+        mine.kd[cell * kNb + blk] = (uint16_t)k_d[i];
+        mine.vd[cell * kNb + blk] = (uint16_t)v_d[i];
         uint32_t w[VP::kWords];
-        read_words<VP::kWords>(vp + 2, blk & 1 ? 0 : 2, w);
+#pragma unroll
+        for (int e = 0; e < VP::kWords; ++e) w[e] = shifted(v_w[i], e, v_shift);
         if constexpr (kVQ4) {
           *reinterpret_cast<u32x4*>(mine.planes + blk * kPlane + cell * 16) =
               u32x4{w[0], w[1], w[2], w[3]};
@@ -611,51 +697,65 @@ void attn_split_kernel(const Params p) {
           *reinterpret_cast<u32x4*>(mine.planes + (2 * blk + 1) * kPlane + cell * 16) =
               u32x4{w[4], w[5], w[6], w[7]} ^ 0x80808080u;
         }
+        const uint32_t size = (seen >> cell) & 1 ? v_d[i] & 0x7FFFu : 0u;
+        d_max = size > d_max ? size : d_max;
       }
+      wave_sync();
+      // scales of cells 8g..8g+7 and of the S operands' rows; V's columns
+      uint32_t dk[8 * kNb / 2], dv[8 * kNb / 2];
+      half8_t dz[2];
+      u32x2 v_col[kVQ4 ? kNb : 2 * kNb];
+      read_scales<8 * kNb / 2>(mine.kd + 8 * g * kNb, dk);
+      if constexpr (!kPair) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          dz[t] = scales_of<kNb>(mine.kd + (8 * (col >> 2) + 4 * t + (col & 3)) * kNb);
+      }
+      read_scales<8 * kNb / 2>(mine.vd + 8 * g * kNb, dv);
+#pragma unroll
+      for (int i = 0; i < (kVQ4 ? kNb : 2 * kNb); ++i)
+        v_col[i] = read_column(mine.planes + i * kPlane, lane);
+      reads_end();
       d_max = wave_max_u(d_max);
       const bool all = seen == ~0u && j0 >= all_lo && j0 + kCells <= all_hi;
-      wave_sync();
 
       // scores of cells 8g..8g+7
       float sc[8];
       {
+        f32x4 acc[2][kNb], sum[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const int cell = 8 * (col >> 2) + 4 * t + (col & 3);
-          uint32_t dk[4 * kNb / 2];
-          read_scales<4 * kNb / 2>(mine.kd + (8 * g + 4 * t) * kNb, dk);
-          f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-          if constexpr (!kPair) sum = mfma(scales_of<kNb>(mine.kd + cell * kNb), q_z, sum);
+          sum[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (!kPair) sum[t] = mfma(dz[t], q_z, sum[t]);
 #pragma unroll
           for (int i = 0; i < kNb; ++i) {
             half8_t a;
-            // codes of block i of this cell, 4 (Q4_0) or 8 bytes of them
-            const uint8_t* kp = mine.k + cell * KP::kBytes + i * KP::kBB + 2;
             if constexpr (kKQ4) {
-              uint32_t w;
-              i & 1 ? read_words_at<1, 0>(kp + 4 * g, &w) : read_words_at<1, 2>(kp + 4 * g, &w);
+              const uint32_t w = i & 1 ? k_w[t][i][0] : shifted(k_w[t][i], 0, 2);
               const uint32_t x = w >> 8;
               a = as_half8(codes<kLow, kPair>(w), codes<kHigh, kPair>(w), codes<kLow, kPair>(x),
                            codes<kHigh, kPair>(x));
             } else {
-              uint32_t w[2];
-              i & 1 ? read_words_at<2, 0>(kp + 8 * g, w) : read_words_at<2, 2>(kp + 8 * g, w);
-              w[0] ^= 0x80808080u;
-              w[1] ^= 0x80808080u;
-              a = as_half8(codes<kByte, kPair>(w[0]), codes<kByte, kPair>(w[0] >> 8),
-                           codes<kByte, kPair>(w[1]), codes<kByte, kPair>(w[1] >> 8));
+              const uint32_t w = (i & 1 ? k_w[t][i][0] : shifted(k_w[t][i], 0, 2)) ^ 0x80808080u;
+              const uint32_t x = (i & 1 ? k_w[t][i][1] : shifted(k_w[t][i], 1, 2)) ^ 0x80808080u;
+              a = as_half8(codes<kByte, kPair>(w), codes<kByte, kPair>(w >> 8),
+                           codes<kByte, kPair>(x), codes<kByte, kPair>(x >> 8));
             }
-            f32x4 acc = mfma(a, q_hi[i], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-            if constexpr (kPair) acc = mfma(a, q_lo[i], acc);
+            acc[t][i] = mfma(a, q_hi[i], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            if constexpr (kPair) acc[t][i] = mfma(a, q_lo[i], acc[t][i]);
+          }
+        }
+        reads_end();
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int x = r * kNb + i;
-              sum[r] = fmaf(acc[r], half_of(dk[x / 2], x & 1), sum[r]);
-            }
+        for (int i = 0; i < kNb; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int x = e * kNb + i;
+            sum[e >> 2][e & 3] =
+                fmaf(acc[e >> 2][i][e & 3], half_of(dk[x / 2], x & 1), sum[e >> 2][e & 3]);
           }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sc[4 * t + r] = sum[r] * cs;
-        }
+        for (int e = 0; e < 8; ++e) sc[e] = sum[e >> 2][e & 3] * cs;
       }
 
       uint32_t unseen = 0u;  // of this lane's cells and row, by bit
@@ -697,8 +797,6 @@ void attn_split_kernel(const Params p) {
         pr[e] = exp2_raw(sc[e] - ref);
         st.l += pr[e];
       }
-      uint32_t dv[8 * kNb / 2];
-      read_scales<8 * kNb / 2>(mine.vd + 8 * g * kNb, dv);
       if (!all) {
         asm volatile("");
 #pragma unroll
@@ -722,13 +820,13 @@ void attn_split_kernel(const Params p) {
         for (int h = 0; h < 2; ++h) {
           half8_t a;
           if constexpr (kVQ4) {
-            const u32x2 w = read_column(mine.planes + i * kPlane, lane);
+            const u32x2 w = v_col[i];
             a = h ? as_half8(signed_codes<kHigh>(w.x), signed_codes<kHigh>(w.x >> 8),
                              signed_codes<kHigh>(w.y), signed_codes<kHigh>(w.y >> 8))
                   : as_half8(signed_codes<kLow>(w.x), signed_codes<kLow>(w.x >> 8),
                              signed_codes<kLow>(w.y), signed_codes<kLow>(w.y >> 8));
           } else {
-            const u32x2 w = read_column(mine.planes + (2 * i + h) * kPlane, lane);
+            const u32x2 w = v_col[2 * i + h];
             a = as_half8(signed_codes<kByte>(w.x), signed_codes<kByte>(w.x >> 8),
                          signed_codes<kByte>(w.y), signed_codes<kByte>(w.y >> 8));
           }
@@ -740,13 +838,12 @@ void attn_split_kernel(const Params p) {
     }
 
     const float l = groups_sum(st.l);
-    const int64_t row = at * p.heads + head * p.group + c % p.group;
-    // dimensions 16 i + 4 g .. + 3 of this lane's row
+    const int64_t part_row = ((int64_t)place * p.kv_heads + head) * p.part_rows + col;
     const auto put = [&](int i, f32x4 o, float sum) {
       if (!live) return;
       if (kVQ4 && (i & 1)) o *= 0.0625f;
       const int dim = 16 * i + 4 * g;
-      if (p.splits == 1) {
+      if (place < 0) {
         const float inv = 1.0f / sum;
         float y[4];
 #pragma unroll
@@ -755,14 +852,14 @@ void attn_split_kernel(const Params p) {
                             ((int64_t)head * p.group + c % p.group) * D + dim,
                         y);
       } else {
-        *reinterpret_cast<f32x4*>(p.part_o + (row * p.splits + split) * D + dim) = o;
+        *reinterpret_cast<f32x4*>(p.part_o + part_row * D + dim) = o;
       }
     };
     if (sub == 1) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) put(i, st.o[i], l);
-      if (live && p.splits > 1 && g == 0) p.part_ml[row * p.splits + split] = float2{st.m, l};
-      continue;
+      if (live && place >= 0 && g == 0) p.part_ml[part_row] = float2{st.m, l};
+      return;
     }
     // join the waves of this head
     __syncthreads();
@@ -791,44 +888,63 @@ void attn_split_kernel(const Params p) {
         if (w < sub) o += join[((first + w) * (D / 16) + i) * kWave + lane] * weight[w];
       put(i, o, sum);
     }
-    if (live && p.splits > 1 && part == 0 && g == 0)
-      p.part_ml[row * p.splits + split] = float2{m, sum};
-    __syncthreads();  // the join's LDS is the next unit's
+    if (live && place >= 0 && part == 0 && g == 0) p.part_ml[part_row] = float2{m, sum};
+    __syncthreads();  // the join's LDS is the next item's
+  };
+
+  for (uint32_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const uint32_t turn = by_unit ? id >> 3 : id;
+    const uint32_t unit = by_unit ? turn / head_groups * 8 + (id & 7) : turn / head_groups;
+    if (unit >= units) continue;
+    const int head = (int)(turn % head_groups << p.heads_shift) + (wave >> (2 - p.heads_shift));
+    if (!shared) {
+      work(head, (int)unit, 0, 0x7FFFFFFF, -1);
+      continue;
+    }
+    const int begin = share_start((int)unit, shares, all_tiles);
+    const int stop = share_start((int)unit + 1, shares, all_tiles);
+    int at = begin;
+    int item = find_last(p.items, at, [&](int i) { return starts[i]; });
+    for (; at < stop; ++item) {
+      const int first = starts[item], last = starts[item + 1];
+      if (first == last) continue;
+      const int to = stop < last ? stop : last;
+      const bool alone = begin <= first && last <= stop;
+      work(head, item, at - first, to - first, alone ? -1 : (int)unit + item);
+      at = to;
+    }
   }
 }
 
-// Joins the splits of one query row: out = sum_s 2^(m_s - m) O_s / sum_s
-// 2^(m_s - m) l_s. One workgroup per row; D / 4 threads cover the row, the
-// others share the splits.
-constexpr int kJoinThreads = 256;
-
-template <int D, typename T>
+// Joins what several shares have of one query row: out = sum_s 2^(m_s - m) O_s /
+// sum_s 2^(m_s - m) l_s. One workgroup per row; D / 4 threads cover the row,
+// the others take shares in turn.
+template <int D, int kJoinThreads, typename T>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p) {
   constexpr int kX = D / 4, kY = kJoinThreads / kX;
   __shared__ f32x4 part[kY][kX];
   __shared__ float part_l[kY], wave_m[kJoinThreads / kWave];
   const int x = threadIdx.x % kX, y = threadIdx.x / kX;
-  const uint32_t rows = (uint32_t)(p.search ? p.n_tokens : p.n_seqs * p.max_q) * p.heads;
+  const int total = p.starts[p.items], shares = share_count(p, total);
+  const uint32_t rows = (uint32_t)(p.n_seqs * p.max_q) * p.heads;
   for (uint32_t id = blockIdx.x; id < rows; id += gridDim.x) {
-    const int head = (int)(id % p.heads);
-    int b, tok;
-    if (p.search) {
-      tok = (int)(id / p.heads);
-      b = find_last(p.n_seqs + 1, tok, [&](int i) { return p.q_start[i]; });
-      if (b == p.n_seqs) continue;
-      tok -= p.q_start[b];
-    } else {
-      b = (int)(id / p.heads) / p.max_q;
-      tok = (int)(id / p.heads) % p.max_q;
-    }
+    const int query_head = (int)(id % p.heads), head = query_head / p.group;
+    const int b = (int)(id / p.heads) / p.max_q, tok = (int)(id / p.heads) % p.max_q;
+    const int c = tok * p.group + query_head % p.group;
+    const int item = b * p.col_tiles + c / kCols;
+    const int first_tile = p.starts[item], last_tile = p.starts[item + 1];
     const Seq s = sequence(p, b);
     const int64_t at = (int64_t)s.t0 + tok;
-    if (tok < 0 || tok >= s.nq || at < 0 || at >= p.n_tokens) continue;
-    const int64_t row = at * p.heads + head;
-    const int splits = tile_span(p, s, (tok * p.group + head % p.group) / kCols).splits;
-    const float2* ml = p.part_ml + row * p.splits;
+    if (tok >= s.nq || at < 0 || at >= p.n_tokens || first_tile >= last_tile) continue;
+    const int first = share_of(first_tile, shares, total);
+    const int n = share_of(last_tile - 1, shares, total) - first + 1;
+    if (n == 1) continue;  // written already
+    // partial result i of this row
+    const auto place = [&](int i) {
+      return ((int64_t)(first + i + item) * p.kv_heads + head) * p.part_rows + c % kCols;
+    };
     float m = -INFINITY;
-    for (int i = threadIdx.x; i < splits; i += kJoinThreads) m = fmaxf(m, ml[i].x);
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) m = fmaxf(m, p.part_ml[place(i)].x);
 #pragma unroll
     for (int k = 32; k > 0; k >>= 1) m = fmaxf(m, shfl_xor_f(m, k));
     if ((threadIdx.x & 63) == 0) wave_m[threadIdx.x >> 6] = m;
@@ -838,12 +954,12 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
     const float ref = m == -INFINITY ? 0.0f : m;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     float l = 0.0f;
-    const float* src = p.part_o + row * p.splits * D + 4 * x;
 #pragma unroll 4
-    for (int i = y; i < splits; i += kY) {
-      const float w = exp2_raw(ml[i].x - ref);
-      l += w * ml[i].y;
-      o += w * *reinterpret_cast<const f32x4*>(src + (int64_t)i * D);
+    for (int i = y; i < n; i += kY) {
+      const float2 ml = p.part_ml[place(i)];
+      const float w = exp2_raw(ml.x - ref);
+      l += w * ml.y;
+      o += w * *reinterpret_cast<const f32x4*>(p.part_o + place(i) * D + 4 * x);
     }
     part[y][x] = o;
     if (x == 0) part_l[y] = l;
@@ -857,21 +973,21 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
       float r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[e] = l == 0.0f ? 0.0f : o[e] * inv;
-      store_f32<T, 4>(static_cast<T*>(p.out) + at * p.out_stride + (int64_t)head * D + 4 * x, r);
+      store_f32<T, 4>(
+          static_cast<T*>(p.out) + at * p.out_stride + (int64_t)query_head * D + 4 * x, r);
     }
     __syncthreads();
   }
 }
 
 constexpr int64_t kMaxGrid = 1 << 22;
-constexpr int64_t kFill = 3072;      // waves that fill the GPU
-constexpr int64_t kMinChunk = 256;   // cells of a split that a workgroup shares
-constexpr int64_t kMaxChunk = 512;   // cells of a split
-constexpr int64_t kMaxUnits = 32768; // tiles and heads from which on nothing is split
+constexpr int64_t kFill = 512;         // workgroups that fill the GPU
+constexpr int64_t kHeadTiles = 16;     // tiles of a wave from which on it takes a head
+constexpr int64_t kSharedCells = 256;  // cells from which on items are shared
 
-// How the cells are divided, from host values alone.
+// How the work is divided, from host values alone.
 struct Plan {
-  int64_t col_tiles, tiles, splits, chunk, rows;
+  int64_t col_tiles, items, shares, part_rows;
   int heads_shift;  // log2 of the cache heads of a workgroup
   bool search;
 };
@@ -881,35 +997,40 @@ Plan plan(const qmat_attn_args& a) {
   const int64_t group = a.heads / a.kv_heads;
   const int64_t max_q = a.max_q < a.n_tokens ? a.max_q : a.n_tokens;
   r.col_tiles = (max_q * group + kCols - 1) / kCols;
+  r.part_rows = max_q * group < kCols ? max_q * group : kCols;
   // Column tiles by sequence where every sequence may have max_q tokens, or by
   // their place among all tokens where those bound them better.
   const int64_t by_token = a.n_tokens * group / kCols + a.n_seqs;
-  r.search = a.n_seqs * r.col_tiles > by_token;
-  r.tiles = r.search ? by_token : a.n_seqs * r.col_tiles;
+  const int64_t by_seq = a.n_seqs * r.col_tiles;
   const int64_t limit = a.pages_per_seq * a.page_size;
   int64_t cells = a.max_kv < limit ? a.max_kv : limit;
   if (a.window > 0 && a.window + max_q < cells) cells = a.window + max_q;
-  const int64_t units = r.tiles * a.kv_heads;
-  const int64_t step = kWaves * kCells;
-  // Where sequences and heads alone make enough waves, a wave takes a head,
-  // and pieces of kMaxChunk cells, so that the lengths of a ragged batch do not
-  // decide how long the last CU works. Otherwise the waves of a workgroup share
-  // a head's piece, none of fewer than two tiles a wave.
-  r.splits = 1;
-  r.chunk = step;
+  r.shares = 0;
   r.heads_shift = 0;
-  const int64_t pieces = (cells + kMaxChunk - 1) / kMaxChunk;
-  if (units >= kFill || units * pieces >= kFill) {
-    while (r.heads_shift < 2 && (a.kv_heads >> r.heads_shift) % 2 == 0) ++r.heads_shift;
-    r.chunk = kMaxChunk;
-    if (units < kMaxUnits && pieces > 1) r.splits = pieces;
-  } else if (cells > kMinChunk) {
-    const int64_t chunk = (cells * units * kWaves / kFill + step - 1) / step * step;
-    r.chunk = chunk < kMinChunk ? kMinChunk : chunk;
-    r.splits = (cells + r.chunk - 1) / r.chunk;
+  r.search = by_seq > by_token;
+  r.items = r.search ? by_token : by_seq;
+  int even = 0;
+  while (even < 2 && (a.kv_heads >> even) % 2 == 0) ++even;
+  if (by_seq <= kMaxItems && cells > kSharedCells &&
+      by_seq * (limit / kCells + 1) <= 0x7FFFFFFF) {
+    r.search = false;
+    r.items = by_seq;
+    const int64_t tiles = r.items * ((cells + kCells - 1) / kCells);  // at most, if max_kv holds
+    // a wave takes a head where that leaves it enough tiles
+    if (tiles * a.kv_heads >= kFill * kWaves * kHeadTiles) r.heads_shift = even;
+    const int64_t groups = a.kv_heads >> r.heads_shift;
+    r.shares = (kFill + groups - 1) / groups;
+    const int64_t most = (tiles + 1) / 2 / (kWaves >> r.heads_shift) + 1;
+    if (r.shares > most) r.shares = most;
+  } else if (r.items * a.kv_heads >= kFill * kWaves) {
+    r.heads_shift = even;
   }
-  r.rows = a.n_tokens * a.heads;
   return r;
+}
+
+// Rows of partial results: share + item is below shares + items.
+int64_t part_count(const qmat_attn_args& a, const Plan& r) {
+  return (r.shares + r.items) * a.kv_heads * r.part_rows;
 }
 
 int log2_of(int64_t v) {
@@ -920,9 +1041,9 @@ int log2_of(int64_t v) {
 
 template <int D, typename T>
 void launch_for(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
-  const int64_t inner = (int64_t)(p.kv_heads >> p.heads_shift) * (p.search ? 1 : p.col_tiles);
-  const int64_t units = (int64_t)(p.search ? p.tiles : p.n_seqs) * p.splits;
-  const int64_t total = (p.by_unit ? (units + 7) / 8 * 8 : units) * inner;
+  const int64_t units = p.shares > 0 ? p.shares : p.items;
+  const int64_t total =
+      (units >= 32 ? (units + 7) / 8 * 8 : units) * (p.kv_heads >> p.heads_shift);
   const dim3 grid((unsigned)(total < kMaxGrid ? total : kMaxGrid));
   const auto go = [&](auto kq, auto vq) {
     if (p.page_shift >= 5)
@@ -940,11 +1061,14 @@ void launch_for(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
     a.v_fmt == kFmtQ4_0 ? go(q4, q4) : go(q4, q8);
   else
     a.v_fmt == kFmtQ4_0 ? go(q8, q4) : go(q8, q8);
-  if (p.splits > 1) {
-    const int64_t rows = (int64_t)(p.search ? p.n_tokens : p.n_seqs * p.max_q) * p.heads;
-    hipLaunchKernelGGL((attn_join_kernel<D, T>),
-                       dim3((unsigned)(rows < kMaxGrid ? rows : kMaxGrid)), dim3(kJoinThreads), 0,
-                       stream, p);
+  if (p.shares > 0) {
+    const int64_t rows = (int64_t)p.n_seqs * p.max_q * p.heads;
+    const dim3 join((unsigned)(rows < kMaxGrid ? rows : kMaxGrid));
+    // few rows of many shares: many threads each; many rows: a wave each
+    if (p.shares > 32 * p.items)
+      hipLaunchKernelGGL((attn_join_kernel<D, 1024, T>), join, dim3(1024), 0, stream, p);
+    else
+      hipLaunchKernelGGL((attn_join_kernel<D, 64, T>), join, dim3(64), 0, stream, p);
   }
 }
 
@@ -963,7 +1087,8 @@ void launch_as(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
 int64_t attn_workspace_bytes(const qmat_attn_args& a) {
   if (a.n_tokens == 0 || a.n_seqs == 0 || a.max_q == 0) return 0;
   const Plan r = plan(a);
-  return r.splits > 1 ? r.rows * r.splits * (a.head_dim + 2) * 4 : 0;
+  if (r.shares == 0) return 0;
+  return part_count(a, r) * (a.head_dim + 2) * 4 + (r.items + 1) * 4;
 }
 
 hipError_t launch_attn(const qmat_attn_args& a, void* workspace, hipStream_t stream) {
@@ -977,7 +1102,8 @@ hipError_t launch_attn(const qmat_attn_args& a, void* workspace, hipStream_t str
   p.q_start = a.q_start;
   p.kv_len = a.kv_len;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + r.rows * r.splits * a.head_dim);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + part_count(a, r) * a.head_dim);
+  p.starts = reinterpret_cast<int32_t*>(p.part_ml + part_count(a, r));
   p.q_stride = a.q_stride;
   p.out_stride = a.out_stride;
   const int64_t dim = a.kv_heads * a.head_dim;
@@ -996,12 +1122,11 @@ hipError_t launch_attn(const qmat_attn_args& a, void* workspace, hipStream_t str
   p.causal = a.causal != 0;
   p.window = a.window < p.max_cells ? (int)a.window : 0;  // a wider one hides nothing ...
   p.col_tiles = (int)r.col_tiles;
-  p.tiles = (int)r.tiles;
+  p.items = (int)r.items;
   p.search = r.search;
+  p.part_rows = (int)r.part_rows;
+  p.shares = (int)r.shares;
   p.heads_shift = r.heads_shift;
-  p.by_unit = (r.search ? r.tiles : a.n_seqs) * r.splits >= 32;
-  p.splits = (int)r.splits;
-  p.chunk = (int)r.chunk;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   if (a.dtype == kDtypeF32)
     launch_as<float>(a, p, stream);
