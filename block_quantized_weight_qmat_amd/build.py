@@ -24,7 +24,7 @@ MICRO_LIB = os.path.join(PKG, "libqmat_micro.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["quantize.hip", "gemv.hip", "decode.hip", "gemm.hip", "kv.hip", "attn.hip",
+SOURCES = ["quantize.hip", "gemv.hip", "decode.hip", "gemm.hip", "kv.hip", "attn.hip", "attn_prompt.hip",
            "qmat_api.cpp", "qmat_kv_api.cpp"]
 MICRO_SOURCES = ["micro.hip"]
 
