@@ -210,9 +210,10 @@ void attn_split_kernel(const Params p) {
     Query<D, kKQ4, T> q;
     q.load(static_cast<const T*>(p.q) + (live ? at : 0) * p.q_stride +
                ((int64_t)head * p.group + c % p.group) * D,
-           live, g);
+           live, g, p.negate != 0);
     // from an S accumulator to a score
-    const float cs = ldexpf(p.scale_log2, (kPair ? 0 : 24) - 14 + q.ex);
+    // (not 0: unseen scores are -inf times this)
+    const float cs = fmaxf(ldexpf(p.scale_log2, (kPair ? 0 : 24) - 14 + q.ex), 0x1p-126f);
     // Unsigned codes: -z times the blocks' query sums, see scales_of. K index
     // x: block x's sum for x < kNb, its rounding error for the next kNb.
     half8_t q_z;
@@ -395,7 +396,7 @@ void attn_split_kernel(const Params p) {
                 fmaf(acc[e >> 2][i][e & 3], half_of(dk[x / 2], x & 1), sum[e >> 2][e & 3]);
           }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sc[e] = sum[e >> 2][e & 3] * cs;
+        for (int e = 0; e < 8; ++e) sc[e] = sum[e >> 2][e & 3];  // not yet scaled
       }
 
       uint32_t unseen = 0u;  // of this lane's cells and row, by bit
@@ -418,7 +419,7 @@ void attn_split_kernel(const Params p) {
       float mx = sc[0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) mx = fmaxf(mx, sc[e]);
-      mx = groups_max(mx);
+      mx = groups_max(mx) * cs;
       const int ex = d_max >> 10 > 30 ? 30 : (int)(d_max >> 10);  // d < 2^(ex - 14)
       st.e = ex > st.e ? ex : st.e;
       st.top = fmaxf(st.top, mx);
@@ -434,7 +435,7 @@ void attn_split_kernel(const Params p) {
       float pr[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        pr[e] = exp2_raw(sc[e] - ref);
+        pr[e] = exp2_raw(fmaf(sc[e], cs, -ref));
         st.l += pr[e];
       }
       if (!all) {
@@ -622,7 +623,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
 
 constexpr int64_t kMaxGrid = 1 << 22;
 constexpr int64_t kPromptRows = 64;    // query rows of a cache head: attn_prompt.hip
-constexpr int64_t kPromptFill = 384;   // its workgroups from which on they are of 128 rows
+constexpr int64_t kPromptFill = 256;   // its large workgroups that fill the GPU
 constexpr int64_t kFill = 512;         // workgroups that fill the GPU
 constexpr int64_t kHeadTiles = 16;     // tiles of a wave from which on it takes a head
 constexpr int64_t kSharedCells = 256;  // cells from which on items are shared
@@ -630,8 +631,8 @@ constexpr int64_t kSharedCells = 256;  // cells from which on items are shared
 // How the work is divided, from host values alone.
 struct Plan {
   int64_t col_tiles, items, shares, part_rows;
-  int heads_shift;   // log2 of the cache heads of a workgroup
-  int prompt_tiles;  // column tiles of a wave of attn_prompt.hip, 0: not there
+  int heads_shift;  // log2 of the cache heads of a workgroup
+  int prompt_rows;  // of an item of attn_prompt.hip, 0: not there
   bool search;
 };
 
@@ -639,7 +640,7 @@ Plan plan(const qmat_attn_args& a) {
   Plan r;
   const int64_t group = a.heads / a.kv_heads;
   const int64_t max_q = a.max_q < a.n_tokens ? a.max_q : a.n_tokens;
-  r.prompt_tiles = 0;
+  r.prompt_rows = 0;
   r.col_tiles = (max_q * group + kCols - 1) / kCols;
   r.part_rows = max_q * group < kCols ? max_q * group : kCols;
   // Column tiles by sequence where every sequence may have max_q tokens, or by
@@ -652,13 +653,10 @@ Plan plan(const qmat_attn_args& a) {
   r.shares = 0;
   r.heads_shift = 0;
   if (max_q * group >= kPromptRows) {
-    for (r.prompt_tiles = 2; r.prompt_tiles > 1; --r.prompt_tiles) {
-      const int64_t rows = kPromptRows * r.prompt_tiles;
-      if (prompt_tiles_fit(a, r.prompt_tiles) &&
-          (a.n_tokens * group / rows + 1) * a.kv_heads >= kPromptFill)
-        break;
-    }
-    const int64_t rows = kPromptRows * r.prompt_tiles;
+    const int64_t many = prompt_rows(a, true);
+    r.prompt_rows =
+        prompt_rows(a, (a.n_tokens * group / many + 1) * a.kv_heads >= kPromptFill);
+    const int64_t rows = r.prompt_rows;
     r.col_tiles = (max_q * group + rows - 1) / rows;
     const int64_t tokens = a.n_tokens * group / rows + a.n_seqs;
     r.search = a.n_seqs * r.col_tiles > tokens;
@@ -785,9 +783,10 @@ hipError_t launch_attn(const qmat_attn_args& a, void* workspace, hipStream_t str
   p.part_rows = (int)r.part_rows;
   p.shares = (int)r.shares;
   p.heads_shift = r.heads_shift;
-  p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
-  if (r.prompt_tiles > 0)
-    launch_prompt(a, p, r.prompt_tiles, stream);
+  p.negate = a.scale < 0.0f;
+  p.scale_log2 = (float)(fabs((double)a.scale) * 1.4426950408889634);
+  if (r.prompt_rows > 0)
+    launch_prompt(a, p, r.prompt_rows, stream);
   else if (a.dtype == kDtypeF32)
     launch_as<float>(a, p, stream);
   else if (a.dtype == kDtypeF16)

@@ -35,7 +35,8 @@ struct Params {
   int page_shift, n_pages, pages_per_seq, max_cells;
   int causal, window;  // window 0: none
   int col_tiles, part_rows, shares, heads_shift;
-  float scale_log2;
+  int negate;        // the scale is negative: its sign goes to the queries
+  float scale_log2;  // its size, times log2(e)
 };
 
 // The new tokens and cells of a sequence.
@@ -346,7 +347,8 @@ struct Query {
   float sum[kNb];  // of this lane's elements of each block
   int ex;          // the row is 2^(ex - 14) times what the operands hold
 
-  __device__ __forceinline__ void load(const T* __restrict__ row, bool live, int g) {
+  __device__ __forceinline__ void load(const T* __restrict__ row, bool live, int g,
+                                       bool negate) {
     float q[kNb][8];
     float a = 0.0f;
 #pragma unroll
@@ -372,7 +374,7 @@ struct Query {
       sum[i] = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float x = ldexpf(q[i][e], 14 - ex);
+        const float x = ldexpf(negate ? -q[i][e] : q[i][e], 14 - ex);
         h[e] = (float)(_Float16)x;
         l[e] = kPair ? (float)(_Float16)(x - h[e]) : 0.0f;
         sum[i] += kPair ? h[e] + l[e] : h[e];
@@ -392,10 +394,10 @@ struct Query {
   }
 };
 
-// attn_prompt.hip: column tiles of a wave (1 or 2, items of 64 times that many
-// rows), and the launch with p.items, p.search and p.col_tiles for such items.
-bool prompt_tiles_fit(const qmat_attn_args& a, int tiles);
-void launch_prompt(const qmat_attn_args& a, const Params& p, int tiles, hipStream_t stream);
+// attn_prompt.hip: query rows of an item where there are few or many of them,
+// and the launch, with p.items, p.search and p.col_tiles for such items.
+int prompt_rows(const qmat_attn_args& a, bool many);
+void launch_prompt(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream);
 
 }  // namespace attn
 }  // namespace qmat

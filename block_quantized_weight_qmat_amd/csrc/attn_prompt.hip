@@ -2,19 +2,28 @@
 // bound by the matrix cores and by what is done to the scores between the two
 // products. Mathematics, exactness and the operand layouts are attn.hip's.
 //
-// One workgroup has an item, kTiles * 64 query rows of one cache head (tokens
-// and the head's group of query heads): four waves, kTiles column tiles of 16
-// each, go through the same cells together, 64 at a time. The cells' codes are
-// unpacked once for all of them, into LDS as the products' operands:
-//  - raw tile -> LDS in aligned units, as memory holds it (next tile's loads
-//    are under way meanwhile);
-//  - threads 0..127 take a K block each, the others a V block: code words to
-//    signed integers in fp16, K in operand order (a lane's 16 bytes side by
-//    side), V in rows that the LDS read transposes (ds_read_b64_tr_b16).
-// Per 64 cells and 16 rows a wave then does 4 D / 32 * 4 products (16 x 16 x 32),
-// and 2 D VALU operations (block scales of K to fp32 sums, of V to
-// probabilities) + about 90 for the softmax, which is what bounds it: the
-// scales cost more issue slots than the products.
+// One workgroup has an item, that is kWv * kTiles * 16 query rows of one cache
+// head (tokens and the head's group of query heads): kWv waves with kTiles
+// column tiles each go through the same cells together, a batch at a time. The
+// cells' codes are unpacked once for all of them, into LDS as the products'
+// operands, in a pipeline with one barrier per batch. Between two barriers
+//  - batch n is multiplied,
+//  - batch n + 1 goes from raw bytes to operands: half of the threads take a K
+//    block each, half a V block; code words to signed integers in fp16, K in
+//    operand order (a lane's 16 bytes side by side), V in rows that the LDS read
+//    transposes (ds_read_b64_tr_b16),
+//  - batch n + 2 goes from registers to LDS as it lies in memory, in aligned
+//    units, and batch n + 3 is asked for.
+// Per 64 cells and 16 rows a wave then does D / 2 products (16 x 16 x 32) and 2 D
+// VALU operations for the block scales (K's on the fp32 sums, V's on the
+// probabilities) + about 70 for the softmax: those bound it, not the products.
+//
+// For fp16 and bf16 activations V's scales are multiplied into the codes when
+// these are unpacked: code x scale rounded to fp16's 11 bits, once more what the
+// probabilities are rounded to anyway. The scales of a cell are first divided by
+// a power of two, which brings the largest to [1, 2) and is given back to the
+// probabilities: one operation for each instead of one per block. (Not for K: an
+// error of a score is multiplied by the score's size. It would save a fifth.)
 #include "attn_device.hpp"
 
 namespace qmat {
@@ -22,24 +31,29 @@ namespace {
 
 using namespace attn;
 
-constexpr int kBatch = 64;  // cells that are staged at a time
-constexpr int kSides = 128; // threads for K, as many for V
+// Cells that are staged at a time: two batches of operands fit LDS.
+template <int D>
+constexpr int batch_for() {
+  return D == 256 ? 32 : 64;
+}
 
-// Staging: threads 0..127 move K's units and blocks, the others V's.
-template <int D, bool kQ4>
+// Staging: the first half of the threads move K's units and blocks, the others V's.
+template <int D, bool kQ4, int kWv>
 struct Side {
   typedef Piece<D, kQ4> P;
+  static constexpr int kBatch = batch_for<D>();
+  static constexpr int kSides = kWv * kWave / 2;  // threads of a side
   static constexpr int kTotal = kBatch * P::kUnits;
   static constexpr int kLoads = (kTotal + kSides - 1) / kSides;
-  static constexpr int kBlocks = kBatch * P::kNb / kSides;  // of a thread
+  static constexpr int kBlocks = (kBatch * P::kNb + kSides - 1) / kSides;  // of a thread
   static constexpr int kRaw = kLoads * kSides * P::kUnit + 16;  // reads go a word further
 };
 
 // A thread's units of the batch that is under way.
-template <int D, bool kKQ4, bool kVQ4>
+template <int D, bool kKQ4, bool kVQ4, int kWv>
 struct Units {
-  typedef Side<D, kKQ4> K;
-  typedef Side<D, kVQ4> V;
+  typedef Side<D, kKQ4, kWv> K;
+  typedef Side<D, kVQ4, kWv> V;
   typedef typename K::P::Unit Unit;
   static constexpr int kLoads = K::kLoads > V::kLoads ? K::kLoads : V::kLoads;
   Unit u[kLoads];
@@ -50,8 +64,8 @@ struct Units {
     asm volatile("" : "+v"(t));  // the units' places are not kept in registers
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int kx = t + i * kSides < K::kTotal ? t + i * kSides : K::kTotal - 1;
-      const int vx = t + i * kSides < V::kTotal ? t + i * kSides : V::kTotal - 1;
+      const int kx = t + i * K::kSides < K::kTotal ? t + i * K::kSides : K::kTotal - 1;
+      const int vx = t + i * K::kSides < V::kTotal ? t + i * K::kSides : V::kTotal - 1;
       const int cell = k ? kx / K::P::kUnits : vx / V::P::kUnits;
       const int unit = k ? kx % K::P::kUnits : vx % V::P::kUnits;
       const uint32_t r = (uint32_t)__shfl((int)row, cell, kWave);
@@ -63,7 +77,7 @@ struct Units {
   __device__ __forceinline__ void write(uint8_t* raw, int n, int t) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      if (i < n) reinterpret_cast<Unit*>(raw)[t + i * kSides] = u[i];
+      if (i < n) reinterpret_cast<Unit*>(raw)[t + i * K::kSides] = u[i];
   }
 };
 
@@ -74,19 +88,26 @@ constexpr int v_row_bytes() {
   return 2 * D + 32;
 }
 
-template <int D, bool kKQ4, bool kVQ4>
-struct PromptLds {
-  uint8_t k_raw[Side<D, kKQ4>::kRaw];
-  uint8_t v_raw[Side<D, kVQ4>::kRaw];
-  // K operands: [32 cells][16 cells][block][lane], 16 bytes each
+template <int D, bool kKQ4, bool kVQ4, int kWv>
+struct Operands {
+  static constexpr int kBatch = batch_for<D>();
+  // K operands: [16 cells][block][lane], 16 bytes each
   uint8_t k[kBatch * D * 2];
   uint8_t v[kBatch * v_row_bytes<D>()];
   uint16_t kd[kBatch * D / 32];  // block scales, [cell][block]
   uint16_t vd[kBatch * D / 32];
+  float v_unit[kBatch];  // of scales in the codes: what they were divided by
   // Of each wave that stages V: its largest |scale| as fp16 bits, and the cells
   // with an infinite one or a NaN, which count as 0 here.
-  uint32_t d_max[2];
-  uint64_t bad[2];
+  uint32_t d_max[kWv / 2];
+  uint32_t bad[kWv / 2][2];
+};
+
+template <int D, bool kKQ4, bool kVQ4, int kWv>
+struct PromptLds {
+  Operands<D, kKQ4, kVQ4, kWv> op[2];
+  uint8_t k_raw[2][Side<D, kKQ4, kWv>::kRaw];
+  uint8_t v_raw[2][Side<D, kVQ4, kWv>::kRaw];
 };
 
 // Barrier of the workgroup that orders its LDS accesses alone: loads from
@@ -112,6 +133,36 @@ __device__ __forceinline__ void read_block(const uint8_t* raw, int cell, int blk
   for (int i = 0; i < P::kWords; ++i) w[i] = shifted(t, i, shift);
 }
 
+// The power of two that scales of a cell are divided by: the exponent field
+// of the largest finite one, as 2^(field - 15).
+template <int D, bool kQ4>
+__device__ __forceinline__ int scale_field(const uint8_t* raw, int cell) {
+  typedef Piece<D, kQ4> P;
+  uint32_t most = 0x0400u;
+#pragma unroll
+  for (int i = 0; i < P::kNb; ++i) {
+    const uint32_t d =
+        *reinterpret_cast<const uint16_t*>(raw + cell * P::kBytes + i * P::kBB) & 0x7FFFu;
+    most = d < 0x7C00u && d > most ? d : most;
+  }
+  return (int)(most >> 10);
+}
+
+__device__ __forceinline__ float power_of(int field) {  // 2^(field - 15)
+  return __builtin_bit_cast(float, (uint32_t)(field - 15 + 127) << 23);
+}
+
+// A scale divided by its cell's power of two, twice as fp16 (times 1/16: for
+// codes that come times 16).
+__device__ __forceinline__ uint32_t scale_pair(uint32_t d, float inverse) {
+  const uint32_t h = f32_to_f16_bits(f16_bits_to_f32(d) * inverse);
+  return h | h << 16;
+}
+
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
+  return as_u32(as_half2(a) * as_half2(b));
+}
+
 // 4 cells of one column: of the four rows that the lane group's lanes name, 16
 // slots each, the lane's slot.
 __device__ __forceinline__ u32x2 read_slots(const uint8_t* rows, int lane) {
@@ -121,23 +172,27 @@ __device__ __forceinline__ u32x2 read_slots(const uint8_t* rows, int lane) {
   return __builtin_bit_cast(u32x2, t);
 }
 
-template <int D, bool kKQ4, bool kVQ4, int kTiles, typename T>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2)
+template <int D, bool kKQ4, bool kVQ4, int kWv, int kTiles, typename T>
+__global__ __launch_bounds__(kWv * kWave, kWv == 8 || D == 64 ? 2 : 1)
 void attn_prompt_kernel(const Params p) {
   constexpr bool kPair = sizeof(T) == 4;
+  constexpr bool kFold = !kPair;  // V's scales go into the codes
   constexpr int kNb = D / 32;
-  constexpr int kItemCols = kWaves * kTiles * kCols;
+  constexpr int kItemCols = kWv * kTiles * kCols;
+  constexpr int kBatch = batch_for<D>(), kQuarters = kBatch / 16;
   typedef Piece<D, kKQ4> KP;
   typedef Piece<D, kVQ4> VP;
-  typedef PromptLds<D, kKQ4, kVQ4> Lds;
+  typedef Side<D, kKQ4, kWv> KS;
+  typedef Side<D, kVQ4, kWv> VS;
+  typedef PromptLds<D, kKQ4, kVQ4, kWv> Lds;
   __shared__ __attribute__((aligned(16))) uint8_t lds_bytes[sizeof(Lds)];
   Lds& lds = *reinterpret_cast<Lds*>(lds_bytes);
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
-  const bool stage_k = wave < 2;
-  const int st = threadIdx.x & (kSides - 1);  // this thread on its side
+  const bool stage_k = wave < kWv / 2;
+  const int st = threadIdx.x % KS::kSides;  // this thread on its side
 
   // Heads of one item next to each other (they share cache lines), late items
   // first (causal ones see more).
@@ -155,6 +210,7 @@ void attn_prompt_kernel(const Params p) {
     if (ct < 0 || ct * kItemCols >= cols) continue;
     const Span span = tile_span<kItemCols>(p, s, ct);
     const int begin = span.lo & ~(kBatch - 1), end = span.hi;
+    lds_barrier();  // the last item's operands are used
 
     // this lane's query rows, and what the wave's rows see: some, all
     const int wave_col = ct * kItemCols + wave * kTiles * kCols;
@@ -173,8 +229,9 @@ void attn_prompt_kernel(const Params p) {
       hi[n] = live[n] ? last_cell(p, s, tok) : 0x7FFFFFFF;
       q[n].load(static_cast<const T*>(p.q) + (live[n] ? at[n] : 0) * p.q_stride +
                     ((int64_t)head * p.group + c % p.group) * D,
-                live[n], g);
-      cs[n] = ldexpf(p.scale_log2, q[n].ex - 14);
+                live[n], g, p.negate != 0);
+      // not 0: unseen scores are -inf times this
+      cs[n] = fmaxf(ldexpf(p.scale_log2, q[n].ex - 14), 0x1p-126f);
     }
     const bool works = wave_col < cols;
     const int last_col = wave_col + kTiles * kCols - 1 < cols ? wave_col + kTiles * kCols - 1
@@ -200,41 +257,40 @@ void attn_prompt_kernel(const Params p) {
     const uint8_t* v_base = p.vc + (int64_t)head * VP::kBytes;
     const int in_page = (1 << p.page_shift) - 1;
     const bool any = begin < end && p.n_pages > 0;
-    int page = -1;  // of cell `lane` of the batch to load next
+    int page = -1;  // of cell lane % kBatch of the batch to load next
+    const int my_cell = lane % kBatch;
     const auto load_page = [&](int j0) {
-      const int j = j0 + lane;
+      const int j = j0 + my_cell;
       const int got = pages[(j < end ? j : begin) >> p.page_shift];
       page = j < end ? got : -1;
     };
-    Units<D, kKQ4, kVQ4> units;
-    uint64_t next_seen = 0;  // cells of the loaded batch that exist, by bit
+    Units<D, kKQ4, kVQ4, kWv> units;
+    // Cells that exist, by bit, of the batches n + 2 (registers), n + 1 (raw), n.
+    uint64_t seen2 = 0, seen1 = 0, seen = 0;
     const auto load = [&](int j0) {  // cells that do not exist load row 0
       const bool ok = page >= 0 && page < p.n_pages;
-      const uint32_t row = ok ? (page << p.page_shift) + ((j0 + lane) & in_page) : 0;
+      const uint32_t row = ok ? (page << p.page_shift) + ((j0 + my_cell) & in_page) : 0;
       units.load(stage_k ? k_base : v_base, (uint32_t)(stage_k ? p.k_row : p.v_row), row, stage_k,
                  st);
-      next_seen = __ballot(ok);
+      seen2 = __ballot(ok);
+      if constexpr (kBatch == 32) seen2 &= 0xFFFFFFFFull;
     };
-    if (any) {
-      load_page(begin);
-      load(begin);
-      load_page(begin + kBatch);
-    }
-    for (int j0 = begin; any && j0 < end; j0 += kBatch) {
-      const uint64_t seen = next_seen;
-      units.write(stage_k ? lds.k_raw : lds.v_raw,
-                  stage_k ? Side<D, kKQ4>::kLoads : Side<D, kVQ4>::kLoads, st);
-      load(j0 + kBatch);
-      load_page(j0 + 2 * kBatch);
-      lds_barrier();  // the raw batch is there, and the last one's operands are used
+    const auto write_raw_batch = [&](int n) {
+      units.write(stage_k ? lds.k_raw[n] : lds.v_raw[n], stage_k ? KS::kLoads : VS::kLoads, st);
+      seen1 = seen2;
+    };
+    // raw bytes to operands
+    const auto unpack = [&](int n) {
+      Operands<D, kKQ4, kVQ4, kWv>& op = lds.op[n];
       if (stage_k) {
 #pragma unroll
-        for (int i = 0; i < Side<D, kKQ4>::kBlocks; ++i) {
-          const int cell = lane, blk = (st >> 6) + 2 * i;
+        for (int i = 0; i < KS::kBlocks; ++i) {
+          const int x = st + i * KS::kSides, cell = x % kBatch, blk = x / kBatch;
+          if (blk >= kNb) break;
           uint32_t d, w[KP::kWords];
-          read_block<D, kKQ4>(lds.k_raw, cell, blk, &d, w);
-          lds.kd[cell * kNb + blk] = (uint16_t)d;
-          uint8_t* to = lds.k + (((cell >> 4) * kNb + blk) * kWave + (cell & 15)) * 16;
+          read_block<D, kKQ4>(lds.k_raw[n], cell, blk, &d, w);
+          op.kd[cell * kNb + blk] = (uint16_t)d;
+          uint8_t* to = op.k + (((cell >> 4) * kNb + blk) * kWave + (cell & 15)) * 16;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             u32x4 a;
@@ -253,104 +309,156 @@ void attn_prompt_kernel(const Params p) {
         uint32_t d_max = 0u;
         uint64_t bad = 0;
 #pragma unroll
-        for (int i = 0; i < Side<D, kVQ4>::kBlocks; ++i) {
-          const int cell = lane, blk = (st >> 6) + 2 * i;
+        for (int i = 0; i < VS::kBlocks; ++i) {
+          const int x = st + i * VS::kSides, cell = x % kBatch, blk = x / kBatch;
+          if (blk >= kNb) break;
           uint32_t d, w[VP::kWords];
-          read_block<D, kVQ4>(lds.v_raw, cell, blk, &d, w);
+          read_block<D, kVQ4>(lds.v_raw[n], cell, blk, &d, w);
           const bool finite = (d & 0x7C00u) != 0x7C00u;
           bad |= __ballot(!finite);
-          lds.vd[cell * kNb + blk] = (uint16_t)(finite ? d : 0u);
-          const uint32_t size = finite && ((seen >> cell) & 1) ? d & 0x7FFFu : 0u;
+          uint32_t low = 0u, high = 0u;
+          if constexpr (kFold) {
+            const int field = scale_field<D, kVQ4>(lds.v_raw[n], cell);
+            const float inverse = finite ? 1.0f / power_of(field) : 0.0f;
+            low = finite ? scale_pair(d, inverse) : 0u;
+            high = finite ? scale_pair(d, inverse * 0.0625f) : 0u;
+            if (blk == 0) op.v_unit[cell] = power_of(field);
+          } else {
+            op.vd[cell * kNb + blk] = (uint16_t)(finite ? d : 0u);
+          }
+          const auto put = [&](int at, u32x4 a, uint32_t scale) {
+            if constexpr (kFold)
+              a = u32x4{times(a.x, scale), times(a.y, scale), times(a.z, scale),
+                        times(a.w, scale)};
+            *reinterpret_cast<u32x4*>(op.v + cell * v_row_bytes<D>() + blk * 64 + at) = a;
+          };
+          const uint32_t size = finite && ((seen1 >> cell) & 1) ? d & 0x7FFFu : 0u;
           d_max = size > d_max ? size : d_max;
-          uint8_t* to = lds.v + cell * v_row_bytes<D>() + blk * 64;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             if constexpr (kVQ4) {  // words 2e, 2e + 1: half of the low and of the high tile
               const uint32_t y = w[2 * e], z = w[2 * e + 1];
-              *reinterpret_cast<u32x4*>(to + 16 * e) =
-                  u32x4{signed_codes<kLow>(y), signed_codes<kLow>(y >> 8),
-                        signed_codes<kLow>(z), signed_codes<kLow>(z >> 8)};
-              *reinterpret_cast<u32x4*>(to + 32 + 16 * e) =
+              put(16 * e,
+                  u32x4{signed_codes<kLow>(y), signed_codes<kLow>(y >> 8), signed_codes<kLow>(z),
+                        signed_codes<kLow>(z >> 8)},
+                  low);
+              put(32 + 16 * e,
                   u32x4{signed_codes<kHigh>(y), signed_codes<kHigh>(y >> 8),
-                        signed_codes<kHigh>(z), signed_codes<kHigh>(z >> 8)};
+                        signed_codes<kHigh>(z), signed_codes<kHigh>(z >> 8)},
+                  high);
             } else {
 #pragma unroll
               for (int f = 0; f < 2; ++f) {
                 const uint32_t y = w[4 * e + 2 * f] ^ 0x80808080u;
                 const uint32_t z = w[4 * e + 2 * f + 1] ^ 0x80808080u;
-                *reinterpret_cast<u32x4*>(to + 32 * e + 16 * f) =
+                put(32 * e + 16 * f,
                     u32x4{signed_codes<kByte>(y), signed_codes<kByte>(y >> 8),
-                          signed_codes<kByte>(z), signed_codes<kByte>(z >> 8)};
+                          signed_codes<kByte>(z), signed_codes<kByte>(z >> 8)},
+                    low);
               }
             }
           }
         }
         d_max = wave_max_u(d_max);
+        if (kBatch == 32) bad = (bad | bad >> 32) & 0xFFFFFFFFull;
         if (lane == 0) {
-          lds.d_max[wave - 2] = d_max;
-          lds.bad[wave - 2] = bad;
+          op.d_max[wave - kWv / 2] = d_max;
+          op.bad[wave - kWv / 2][0] = (uint32_t)bad;
+          op.bad[wave - kWv / 2][1] = (uint32_t)(bad >> 32);
         }
       }
-      lds_barrier();  // the operands are there, and the raw batch is used
-      if (!works || seen == 0 || j0 >= some_hi || j0 + kBatch <= some_lo) continue;
-      const uint32_t d_max = lds.d_max[0] > lds.d_max[1] ? lds.d_max[0] : lds.d_max[1];
+      seen = seen1;
+    };
+    uint64_t now_seen = 0;  // batch n's
+    if (any) {
+      load_page(begin);
+      load(begin);
+      load_page(begin + kBatch);
+      write_raw_batch(0);
+      load(begin + kBatch);
+      load_page(begin + 2 * kBatch);
+      lds_barrier();
+      unpack(0);
+      now_seen = seen;
+      write_raw_batch(1);
+      load(begin + 2 * kBatch);
+      load_page(begin + 3 * kBatch);
+      lds_barrier();
+    }
+    for (int j0 = begin, turn = 0; any && j0 < end; j0 += kBatch, turn ^= 1) {
+      if (j0 > begin) {
+        lds_barrier();
+        now_seen = seen;
+      }
+      unpack(turn ^ 1);
+      write_raw_batch(turn);
+      load(j0 + 3 * kBatch);
+      load_page(j0 + 4 * kBatch);
+      const Operands<D, kKQ4, kVQ4, kWv>& op = lds.op[turn];
+      if (!works || now_seen == 0 || j0 >= some_hi || j0 + kBatch <= some_lo) continue;
+      uint32_t d_max = op.d_max[0], bad_lo = op.bad[0][0], bad_hi = op.bad[0][1];
+#pragma unroll
+      for (int i = 1; i < kWv / 2; ++i) {
+        d_max = op.d_max[i] > d_max ? op.d_max[i] : d_max;
+        bad_lo |= op.bad[i][0];
+        bad_hi |= op.bad[i][1];
+      }
       const int ex_now = __builtin_amdgcn_readfirstlane(d_max >> 10);  // d < 2^(ex - 14)
       ex = ex_now > ex ? ex_now : ex;
-      const bool all = seen == ~0ull && j0 >= all_lo && j0 + kBatch <= all_hi;
+      const uint64_t full = kBatch == 64 ? ~0ull : 0xFFFFFFFFull;
+      const bool all = now_seen == full && j0 >= all_lo && j0 + kBatch <= all_hi;
 
-      // Scores. Of 32 cells from 32 h on a lane has 16 t + 4 g + r, t < 2.
-      float sc[kTiles][16];
+      // Scores, not yet scaled. Of 16 cells from 16 t on a lane has 4 g + r.
+      float sc[kTiles][4 * kQuarters];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int t = 0; t < kQuarters; ++t) {
+        half8_t a[kNb];
+        uint32_t dk[2 * kNb];
+        const uint8_t* from = op.k + (t * kNb * kWave + lane) * 16;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          half8_t a[kNb];
-          uint32_t dk[2 * kNb];
-          const uint8_t* from = lds.k + ((2 * h + t) * kNb * kWave + lane) * 16;
+        for (int i = 0; i < kNb; ++i)
+          a[i] = *reinterpret_cast<const half8_t*>(from + i * kWave * 16);
+        read_scales<2 * kNb>(op.kd + (16 * t + 4 * g) * kNb, dk);
 #pragma unroll
-          for (int i = 0; i < kNb; ++i)
-            a[i] = *reinterpret_cast<const half8_t*>(from + i * kWave * 16);
-          read_scales<2 * kNb>(lds.kd + (32 * h + 16 * t + 4 * g) * kNb, dk);
+        for (int n = 0; n < kTiles; ++n) {
+          f32x4 acc[kNb];
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n) {
-            f32x4 acc[kNb];
+          for (int i = 0; i < kNb; ++i) {
+            acc[i] = mfma(a[i], q[n].hi[i], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            if constexpr (kPair) acc[i] = mfma(a[i], q[n].lo[i], acc[i]);
+          }
 #pragma unroll
-            for (int i = 0; i < kNb; ++i) {
-              acc[i] = mfma(a[i], q[n].hi[i], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-              if constexpr (kPair) acc[i] = mfma(a[i], q[n].lo[i], acc[i]);
-            }
+          for (int r = 0; r < 4; ++r) {
+            float sum = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float sum = acc[0][r] * half_of(dk[r * kNb / 2], 0);
-#pragma unroll
-              for (int i = 1; i < kNb; ++i)
-                sum = fmaf(acc[i][r], half_of(dk[(r * kNb + i) / 2], i & 1), sum);
-              sc[n][8 * h + 4 * t + r] = sum * cs[n];
-            }
+            for (int i = 0; i < kNb; ++i)
+              sum = fmaf(acc[i][r], half_of(dk[(r * kNb + i) / 2], i & 1), sum);
+            sc[n][4 * t + r] = sum;
           }
         }
+      }
 
       if (!all) {
         asm volatile("");
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 4 * kQuarters; ++e) {
             const int cell = 16 * (e >> 2) + 4 * g + (e & 3), j = j0 + cell;
-            const bool on = ((seen >> cell) & 1) != 0 && j >= lo[n] && j < hi[n];
+            const bool on = ((now_seen >> cell) & 1) != 0 && j >= lo[n] && j < hi[n];
             sc[n][e] = on ? sc[n][e] : -INFINITY;
           }
       }
-      const uint64_t bad = lds.bad[0] | lds.bad[1];
-      if (__builtin_amdgcn_readfirstlane((uint32_t)bad | (uint32_t)(bad >> 32)) != 0) {
+      if (__builtin_amdgcn_readfirstlane(bad_lo | bad_hi) != 0) {
         asm volatile("");
         // a row that sees such a cell has no finite result
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 4 * kQuarters; ++e) {
             const int cell = 16 * (e >> 2) + 4 * g + (e & 3);
-            if (((bad >> cell) & 1) != 0 && sc[n][e] != -INFINITY) sc[n][e] = NAN;
+            const uint32_t bad = cell < 32 ? bad_lo >> cell : bad_hi >> (cell - 32);
+            if ((bad & 1) != 0 && sc[n][e] != -INFINITY) sc[n][e] = NAN;
           }
       }
 
@@ -360,8 +468,8 @@ void attn_prompt_kernel(const Params p) {
       for (int n = 0; n < kTiles; ++n) {
         float mx = sc[n][0];
 #pragma unroll
-        for (int e = 1; e < 16; ++e) mx = fmaxf(mx, sc[n][e]);
-        top[n] = fmaxf(top[n], groups_max(mx));
+        for (int e = 1; e < 4 * kQuarters; ++e) mx = fmaxf(mx, sc[n][e]);
+        top[n] = fmaxf(top[n], groups_max(mx) * cs[n]);
         const float now = top[n] + (float)(ex - 28);
         const float ref = now == -INFINITY ? 0.0f : now;
         if (__ballot(now != m[n]) != 0) {
@@ -372,19 +480,31 @@ void attn_prompt_kernel(const Params p) {
           m[n] = now;
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          sc[n][e] = exp2_raw(sc[n][e] - ref);
+        for (int e = 0; e < 4 * kQuarters; ++e) {
+          sc[n][e] = exp2_raw(fmaf(sc[n][e], cs[n], -ref));
           l[n] += sc[n][e];
         }
       }
 
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kBatch / 32; ++h) {
         uint32_t dv[2][2 * kNb];
+        half8_t pf[kTiles];  // scales in the codes: one operand for all blocks
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          read_scales<2 * kNb>(lds.vd + (32 * h + 16 * t + 4 * g) * kNb, dv[t]);
-        const uint8_t* from = lds.v + (32 * h + 4 * g + (col >> 2)) * v_row_bytes<D>() +
+        for (int t = 0; t < 2; ++t) {
+          if constexpr (kFold) {
+            const f32x4 unit =
+                *reinterpret_cast<const f32x4*>(op.v_unit + 32 * h + 16 * t + 4 * g);
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                pf[n][4 * t + r] = (_Float16)(sc[n][8 * h + 4 * t + r] * unit[r]);
+          } else {
+            read_scales<2 * kNb>(op.vd + (32 * h + 16 * t + 4 * g) * kNb, dv[t]);
+          }
+        }
+        const uint8_t* from = op.v + (32 * h + 4 * g + (col >> 2)) * v_row_bytes<D>() +
                               (col & 3) * 8;
 #pragma unroll
         for (int i = 0; i < kNb; ++i) {
@@ -397,6 +517,11 @@ void attn_prompt_kernel(const Params p) {
           }
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) {
+            if constexpr (kFold) {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) o[n][2 * i + y] = mfma(a[y], pf[n], o[n][2 * i + y]);
+              continue;
+            }
             half8_t ph, pl;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -425,7 +550,7 @@ void attn_prompt_kernel(const Params p) {
                ((int64_t)head * p.group + c % p.group) * D + 4 * g;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        const float f = kVQ4 && (i & 1) ? inv * 0.0625f : inv;
+        const float f = kVQ4 && !kFold && (i & 1) ? inv * 0.0625f : inv;
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : o[n][i][e] * f;
@@ -433,27 +558,28 @@ void attn_prompt_kernel(const Params p) {
         store_f32<T, 4>(dst + 16 * i, out);
       }
     }
-    lds_barrier();  // the operands in LDS are the next item's
   }
 }
 
 constexpr int64_t kMaxGrid = 1 << 22;
 
 template <int D, typename T>
-void launch_for(const qmat_attn_args& a, const Params& p, int tiles, hipStream_t stream) {
+void launch_for(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream) {
   const int64_t total = (int64_t)p.items * p.kv_heads;
   const dim3 grid((unsigned)(total < kMaxGrid ? total : kMaxGrid));
   const auto go = [&](auto kq, auto vq) {
     constexpr bool kK = decltype(kq)::value, kV = decltype(vq)::value;
-    // 256 wide heads and pairs of fp16 leave no registers for a second tile
-    if constexpr (D <= 128 && sizeof(T) == 2) {
-      if (tiles == 2) {
-        hipLaunchKernelGGL((attn_prompt_kernel<D, kK, kV, 2, T>), grid, dim3(kThreads), 0, stream,
-                           p);
+    if constexpr (D <= 128) {
+      // a pair of fp16 for each query leaves no registers for a second tile
+      constexpr int kTiles = sizeof(T) == 2 ? 2 : 1;
+      if (rows == 128 * kTiles) {
+        hipLaunchKernelGGL((attn_prompt_kernel<D, kK, kV, 8, kTiles, T>), grid, dim3(8 * kWave), 0,
+                           stream, p);
         return;
       }
     }
-    hipLaunchKernelGGL((attn_prompt_kernel<D, kK, kV, 1, T>), grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((attn_prompt_kernel<D, kK, kV, 4, 1, T>), grid, dim3(4 * kWave), 0, stream,
+                       p);
   };
   const std::true_type q4{};
   const std::false_type q8{};
@@ -464,31 +590,31 @@ void launch_for(const qmat_attn_args& a, const Params& p, int tiles, hipStream_t
 }
 
 template <typename T>
-void launch_as(const qmat_attn_args& a, const Params& p, int tiles, hipStream_t stream) {
+void launch_as(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream) {
   if (a.head_dim == 64)
-    launch_for<64, T>(a, p, tiles, stream);
+    launch_for<64, T>(a, p, rows, stream);
   else if (a.head_dim == 128)
-    launch_for<128, T>(a, p, tiles, stream);
+    launch_for<128, T>(a, p, rows, stream);
   else
-    launch_for<256, T>(a, p, tiles, stream);
+    launch_for<256, T>(a, p, rows, stream);
 }
 
 }  // namespace
 
 namespace attn {
 
-// Column tiles of a wave for items of 64 or 128 rows.
-bool prompt_tiles_fit(const qmat_attn_args& a, int tiles) {
-  return tiles == 1 || (a.head_dim <= 128 && a.dtype != kDtypeF32);
+int prompt_rows(const qmat_attn_args& a, bool many) {
+  if (!many || a.head_dim > 128) return 64;
+  return a.dtype == kDtypeF32 ? 128 : 256;
 }
 
-void launch_prompt(const qmat_attn_args& a, const Params& p, int tiles, hipStream_t stream) {
+void launch_prompt(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream) {
   if (a.dtype == kDtypeF32)
-    launch_as<float>(a, p, tiles, stream);
+    launch_as<float>(a, p, rows, stream);
   else if (a.dtype == kDtypeF16)
-    launch_as<_Float16>(a, p, tiles, stream);
+    launch_as<_Float16>(a, p, rows, stream);
   else
-    launch_as<__bf16>(a, p, tiles, stream);
+    launch_as<__bf16>(a, p, rows, stream);
 }
 
 }  // namespace attn

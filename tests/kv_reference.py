@@ -47,7 +47,8 @@ def element_bound(q, k_blocks_d, z2, n_cells, scale, mag, out, dtype, v_unit):
     2^-24 (D + D/32 + 8) of sum |q| z2 d scale; a probability changes by the factor of the
     score's error, once in the numerator and once in the sum (n/32 + 8 additions, 2^-24
     each). Probability times V scale is rounded to 11 bits (half a step 2^-11; a pair of
-    fp16: 2^-22), and by half of fp16's smallest step, 2^-25, where it is tiny; these numbers
+    fp16: 2^-22); prompts of 16-bit types round the probability and code times V scale, each to
+    11 bits, 2 * 2^-11 together. And by half of fp16's smallest step, 2^-25, where it is tiny; these numbers
     are scaled so that 2^14 stands for probability 1 (relative to the largest) times a power of
     two below 2 d_max, so that is 2^-38 d_max for each cell, times the code: v_unit = d_max * 8
     (Q4_0) or * 128 (Q8_0). It shows where one cell dominates a row and its code is 0. Then the output's own rounding, half a step: a half of eps
@@ -57,7 +58,7 @@ def element_bound(q, k_blocks_d, z2, n_cells, scale, mag, out, dtype, v_unit):
     amp = np.abs(q).sum(-1, keepdims=True) * z2 * k_blocks_d * scale
     score = 2.0 ** -24 * (D + D / 32 + 8) * amp + 2.0 ** -22 * (1 + amp)
     rel = 2 * np.expm1(score) + 2.0 ** -24 * (n_cells / 16 + 40)
-    rel = rel + (2.0 ** -21 if dtype == "f32" else 2.0 ** -11 + 2.0 ** -20)
+    rel = rel + (2.0 ** -21 if dtype == "f32" else 2.0 ** -10 + 2.0 ** -20)
     least = 2.0 ** -25 if dtype == "f16" else 1e-30
     rel_least = n_cells * 2.0 ** -38 * v_unit
     return rel_least + rel * mag + np.abs(out) * EPS[dtype] / 2 * (1 + 2.0 ** -8) + least
