@@ -30,6 +30,8 @@
 // 8g..8g+7 (the rows of two S tiles are dealt that way), which is the K index
 // of the second product. V^T needs 8 cells of one dimension per lane: code
 // bytes are transposed by the LDS read itself (ds_read_b64_tr_b8).
+#include <type_traits>
+
 #include "attn_device.hpp"
 
 namespace qmat {
@@ -73,58 +75,6 @@ struct State {
   float l;          // this lane's part of the sum
   int e;            // exponent field of the largest V scale so far
 };
-
-// The items' tiles summed up: starts[i] is item i's first, starts[items] their
-// number, which is returned. An item that sees nothing counts as one tile, so
-// that somebody writes its zeros; one without rows has none.
-__device__ __forceinline__ int count_tiles(const Params& p, int* starts, bool keep) {
-  constexpr int kEach = kMaxItems / kThreads;
-  __shared__ int wave_sum[kWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int n[kEach], sum = 0;
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int item = threadIdx.x * kEach + e;
-    n[e] = 0;
-    if (item < p.items) {
-      const Seq s = sequence(p, item / p.col_tiles);
-      const int ct = item % p.col_tiles;
-      const int tiles = tile_span<kCols>(p, s, ct).tiles();
-      n[e] = ct * kCols >= s.nq * p.group ? 0 : tiles > 0 ? tiles : 1;
-    }
-    sum += n[e];
-  }
-  int before = sum;  // of this lane and those before it
-#pragma unroll
-  for (int k = 1; k < kWave; k <<= 1) {
-    const int v = __shfl_up(before, k, kWave);
-    before += lane >= k ? v : 0;
-  }
-  if (lane == kWave - 1) wave_sum[wave] = before;
-  __syncthreads();
-  before -= sum;
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? wave_sum[w] : 0;
-    total += wave_sum[w];
-  }
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int item = threadIdx.x * kEach + e;
-    if (item < p.items) {
-      starts[item] = before;
-      if (keep) p.starts[item] = before;
-    }
-    before += n[e];
-  }
-  if (threadIdx.x == 0) {
-    starts[p.items] = total;
-    if (keep) p.starts[p.items] = total;
-  }
-  __syncthreads();
-  return total;
-}
 
 // An item is a column tile of a sequence. With p.shares == 0 a workgroup has
 // one item and one to four cache heads. Otherwise every workgroup has the same
@@ -173,7 +123,7 @@ void attn_split_kernel(const Params p) {
   // Workgroups go to the 8 XCDs in turn. All heads of one share get the same
   // XCD, whose L2 then holds the cache lines they have in common.
   const bool shared = p.shares > 0;
-  const int all_tiles = shared ? count_tiles(p, starts, blockIdx.x == 0) : 0;
+  const int all_tiles = shared ? count_tiles<kCols, kCells, kThreads>(p, starts, blockIdx.x == 0) : 0;
   const int shares = share_count(p, all_tiles);
   const uint32_t units = shared ? shares : p.items;
   const bool by_unit = units >= 32;
@@ -191,9 +141,9 @@ void attn_split_kernel(const Params p) {
     const Seq s = sequence(p, b);
     const int cols = s.nq * p.group;
     if (ct < 0 || ct * kCols >= cols) return;
-    const Span span = tile_span<kCols>(p, s, ct);
+    const Span span = tile_span<kCols, kCells>(p, s, ct);
     const int begin = span.lo + from * kCells;
-    const int end = to < span.tiles() ? span.lo + to * kCells : span.hi;
+    const int end = to < span.tiles<kCells>() ? span.lo + to * kCells : span.hi;
 
     // this lane's query row
     const int c = ct * kCols + col;
@@ -572,7 +522,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
     const int query_head = (int)(id % p.heads), head = query_head / p.group;
     const int b = (int)(id / p.heads) / p.max_q, tok = (int)(id / p.heads) % p.max_q;
     const int c = tok * p.group + query_head % p.group;
-    const int item = b * p.col_tiles + c / kCols;
+    const int item = b * p.col_tiles + c / p.item_rows;
     const int first_tile = p.starts[item], last_tile = p.starts[item + 1];
     const Seq s = sequence(p, b);
     const int64_t at = (int64_t)s.t0 + tok;
@@ -582,7 +532,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
     if (n == 1) continue;  // written already
     // partial result i of this row
     const auto place = [&](int i) {
-      return ((int64_t)(first + i + item) * p.kv_heads + head) * p.part_rows + c % kCols;
+      return ((int64_t)(first + i + item) * p.kv_heads + head) * p.part_rows + c % p.item_rows;
     };
     float m = -INFINITY;
     for (int i = threadIdx.x; i < n; i += kJoinThreads) m = fmaxf(m, p.part_ml[place(i)].x);
@@ -623,7 +573,6 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
 
 constexpr int64_t kMaxGrid = 1 << 22;
 constexpr int64_t kPromptRows = 64;    // query rows of a cache head: attn_prompt.hip
-constexpr int64_t kPromptFill = 256;   // its large workgroups that fill the GPU
 constexpr int64_t kFill = 512;         // workgroups that fill the GPU
 constexpr int64_t kHeadTiles = 16;     // tiles of a wave from which on it takes a head
 constexpr int64_t kSharedCells = 256;  // cells from which on items are shared
@@ -653,14 +602,31 @@ Plan plan(const qmat_attn_args& a) {
   r.shares = 0;
   r.heads_shift = 0;
   if (max_q * group >= kPromptRows) {
-    const int64_t many = prompt_rows(a, true);
-    r.prompt_rows =
-        prompt_rows(a, (a.n_tokens * group / many + 1) * a.kv_heads >= kPromptFill);
-    const int64_t rows = r.prompt_rows;
+    const PromptShape shape = prompt_shape(a, max_q * group);
+    const int64_t rows = shape.rows;
+    r.prompt_rows = shape.rows;
+    r.part_rows = max_q * group < rows ? max_q * group : rows;
     r.col_tiles = (max_q * group + rows - 1) / rows;
     const int64_t tokens = a.n_tokens * group / rows + a.n_seqs;
-    r.search = a.n_seqs * r.col_tiles > tokens;
-    r.items = r.search ? tokens : a.n_seqs * r.col_tiles;
+    const int64_t direct = a.n_seqs * r.col_tiles, units = direct * a.kv_heads;
+    // Items shared out evenly: that saves batches where few items leave most of
+    // the GPU idle, and costs a partial result of every row and their joining,
+    // as long as two batches and, where the GPU is full, 16 more. 100 tokens
+    // behind 16000, 32 / 8 heads of 128, bf16: 983 us unshared, 96 us shared;
+    // 1024 tokens of their own: 82 and 86 us; 2 x 2048: 188 and 307 us.
+    const int64_t batches = (cells + shape.batch - 1) / shape.batch;
+    const int64_t saved = batches - (batches * units + shape.fill - 1) / shape.fill;
+    if (direct <= kMaxItems && saved >= 2 + 16 * units / shape.fill &&
+        direct * (limit / shape.batch + 1) <= 0x7FFFFFFF) {
+      const int64_t tiles = direct * batches;
+      r.search = false;
+      r.items = direct;
+      r.shares = shape.fill / a.kv_heads > 1 ? shape.fill / a.kv_heads : 1;
+      if (r.shares > (tiles + 1) / 2) r.shares = (tiles + 1) / 2;
+    } else {
+      r.search = direct > tokens;
+      r.items = r.search ? tokens : direct;
+    }
     return r;
   }
   r.search = by_seq > by_token;
@@ -675,7 +641,7 @@ Plan plan(const qmat_attn_args& a) {
     // a wave takes a head where that leaves it enough tiles
     if (tiles * a.kv_heads >= kFill * kWaves * kHeadTiles) r.heads_shift = even;
     const int64_t groups = a.kv_heads >> r.heads_shift;
-    r.shares = (kFill + groups - 1) / groups;
+    r.shares = kFill / groups > 1 ? kFill / groups : 1;
     const int64_t most = (tiles + 1) / 2 / (kWaves >> r.heads_shift) + 1;
     if (r.shares > most) r.shares = most;
   } else if (r.items * a.kv_heads >= kFill * kWaves) {
@@ -717,25 +683,40 @@ void launch_for(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
     a.v_fmt == kFmtQ4_0 ? go(q4, q4) : go(q4, q8);
   else
     a.v_fmt == kFmtQ4_0 ? go(q8, q4) : go(q8, q8);
-  if (p.shares > 0) {
-    const int64_t rows = (int64_t)p.n_seqs * p.max_q * p.heads;
-    const dim3 join((unsigned)(rows < kMaxGrid ? rows : kMaxGrid));
+}
+
+// The second kernel, where items are shared.
+template <typename T>
+void launch_join(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
+  const int64_t rows = (int64_t)p.n_seqs * p.max_q * p.heads;
+  const dim3 grid((unsigned)(rows < kMaxGrid ? rows : kMaxGrid));
+  const auto go = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
     // few rows of many shares: many threads each; many rows: a wave each
     if (p.shares > 32 * p.items)
-      hipLaunchKernelGGL((attn_join_kernel<D, 1024, T>), join, dim3(1024), 0, stream, p);
+      hipLaunchKernelGGL((attn_join_kernel<D, 1024, T>), grid, dim3(1024), 0, stream, p);
     else
-      hipLaunchKernelGGL((attn_join_kernel<D, 64, T>), join, dim3(64), 0, stream, p);
-  }
+      hipLaunchKernelGGL((attn_join_kernel<D, 64, T>), grid, dim3(64), 0, stream, p);
+  };
+  if (a.head_dim == 64)
+    go(std::integral_constant<int, 64>{});
+  else if (a.head_dim == 128)
+    go(std::integral_constant<int, 128>{});
+  else
+    go(std::integral_constant<int, 256>{});
 }
 
 template <typename T>
-void launch_as(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
-  if (a.head_dim == 64)
+void launch_as(const qmat_attn_args& a, const Params& p, int prompt_rows, hipStream_t stream) {
+  if (prompt_rows > 0)
+    launch_prompt(a, p, prompt_rows, stream);
+  else if (a.head_dim == 64)
     launch_for<64, T>(a, p, stream);
   else if (a.head_dim == 128)
     launch_for<128, T>(a, p, stream);
   else
     launch_for<256, T>(a, p, stream);
+  if (p.shares > 0) launch_join<T>(a, p, stream);
 }
 
 }  // namespace
@@ -781,18 +762,17 @@ hipError_t launch_attn(const qmat_attn_args& a, void* workspace, hipStream_t str
   p.items = (int)r.items;
   p.search = r.search;
   p.part_rows = (int)r.part_rows;
+  p.item_rows = (int)(r.prompt_rows > 0 ? r.prompt_rows : kCols);
   p.shares = (int)r.shares;
   p.heads_shift = r.heads_shift;
   p.negate = a.scale < 0.0f;
   p.scale_log2 = (float)(fabs((double)a.scale) * 1.4426950408889634);
-  if (r.prompt_rows > 0)
-    launch_prompt(a, p, r.prompt_rows, stream);
-  else if (a.dtype == kDtypeF32)
-    launch_as<float>(a, p, stream);
+  if (a.dtype == kDtypeF32)
+    launch_as<float>(a, p, r.prompt_rows, stream);
   else if (a.dtype == kDtypeF16)
-    launch_as<_Float16>(a, p, stream);
+    launch_as<_Float16>(a, p, r.prompt_rows, stream);
   else
-    launch_as<__bf16>(a, p, stream);
+    launch_as<__bf16>(a, p, r.prompt_rows, stream);
   return hipGetLastError();
 }
 

@@ -34,7 +34,7 @@ struct Params {
   int items, search;  // column tiles; found by their place among all tokens
   int page_shift, n_pages, pages_per_seq, max_cells;
   int causal, window;  // window 0: none
-  int col_tiles, part_rows, shares, heads_shift;
+  int col_tiles, item_rows, part_rows, shares, heads_shift;
   int negate;        // the scale is negative: its sign goes to the queries
   float scale_log2;  // its size, times log2(e)
 };
@@ -66,18 +66,21 @@ __device__ __forceinline__ int last_cell(const Params& p, const Seq& s, int i) {
 }
 
 // The cells that a column tile's rows see together, in whole tiles from a
-// multiple of 32 on.
+// multiple of a tile's cells on.
 struct Span {
   int lo, hi;
-  __device__ __forceinline__ int tiles() const { return (hi - lo + kCells - 1) / kCells; }
+  template <int kTile>
+  __device__ __forceinline__ int tiles() const {
+    return (hi - lo + kTile - 1) / kTile;
+  }
 };
 
-template <int kItemCols>
+template <int kItemCols, int kTile>
 __device__ __forceinline__ Span tile_span(const Params& p, const Seq& s, int ct) {
   const int c0 = ct * kItemCols;
   if (c0 >= s.nq * p.group) return Span{0, 0};
   const int i1 = (c0 + kItemCols - 1) / p.group;
-  const int lo = first_cell(p, s, c0 / p.group) & ~(kCells - 1);
+  const int lo = first_cell(p, s, c0 / p.group) & ~(kTile - 1);
   const int hi = last_cell(p, s, i1 < s.nq ? i1 : s.nq - 1);
   return Span{lo, hi > lo ? hi : lo};
 }
@@ -122,6 +125,59 @@ __device__ __forceinline__ int find_last(int n, int x, const F& first) {
     n = n - last * step < step ? n - last * step : step;
   }
   return lo;
+}
+
+// The items' tiles summed up: starts[i] is item i's first, starts[items] their
+// number, which is returned. An item that sees nothing counts as one tile, so
+// that somebody writes its zeros; one without rows has none.
+template <int kItemCols, int kTile, int kThr>
+__device__ __forceinline__ int count_tiles(const Params& p, int* starts, bool keep) {
+  constexpr int kEach = kMaxItems / kThr, kWv = kThr / kWave;
+  __shared__ int wave_sum[kWv];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int n[kEach], sum = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int item = threadIdx.x * kEach + e;
+    n[e] = 0;
+    if (item < p.items) {
+      const Seq s = sequence(p, item / p.col_tiles);
+      const int ct = item % p.col_tiles;
+      const int tiles = tile_span<kItemCols, kTile>(p, s, ct).template tiles<kTile>();
+      n[e] = ct * kItemCols >= s.nq * p.group ? 0 : tiles > 0 ? tiles : 1;
+    }
+    sum += n[e];
+  }
+  int before = sum;  // of this lane and those before it
+#pragma unroll
+  for (int k = 1; k < kWave; k <<= 1) {
+    const int v = __shfl_up(before, k, kWave);
+    before += lane >= k ? v : 0;
+  }
+  if (lane == kWave - 1) wave_sum[wave] = before;
+  __syncthreads();
+  before -= sum;
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kWv; ++w) {
+    before += w < wave ? wave_sum[w] : 0;
+    total += wave_sum[w];
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int item = threadIdx.x * kEach + e;
+    if (item < p.items) {
+      starts[item] = before;
+      if (keep) p.starts[item] = before;
+    }
+    before += n[e];
+  }
+  if (threadIdx.x == 0) {
+    starts[p.items] = total;
+    if (keep) p.starts[p.items] = total;
+  }
+  __syncthreads();
+  return total;
 }
 
 // Work between lanes of one wave through LDS: earlier writes are in order
@@ -394,9 +450,13 @@ struct Query {
   }
 };
 
-// attn_prompt.hip: query rows of an item where there are few or many of them,
-// and the launch, with p.items, p.search and p.col_tiles for such items.
-int prompt_rows(const qmat_attn_args& a, bool many);
+// attn_prompt.hip: the query rows of its items where a sequence has up to
+// seq_rows of them (of one cache head), the cells of a batch, the workgroups
+// that fill the GPU; and the launch, with p.items and so on for such items.
+struct PromptShape {
+  int rows, batch, fill;
+};
+PromptShape prompt_shape(const qmat_attn_args& a, int64_t seq_rows);
 void launch_prompt(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream);
 
 }  // namespace attn

@@ -18,12 +18,20 @@
 // VALU operations for the block scales (K's on the fp32 sums, V's on the
 // probabilities) + about 70 for the softmax: those bound it, not the products.
 //
-// For fp16 and bf16 activations V's scales are multiplied into the codes when
-// these are unpacked: code x scale rounded to fp16's 11 bits, once more what the
-// probabilities are rounded to anyway. The scales of a cell are first divided by
-// a power of two, which brings the largest to [1, 2) and is given back to the
-// probabilities: one operation for each instead of one per block. (Not for K: an
-// error of a score is multiplied by the score's size. It would save a fifth.)
+// For bf16 activations V's scales are multiplied into the codes when these are
+// unpacked: code x scale rounded to fp16's 11 bits, once more what the
+// probabilities are rounded to anyway and an eighth of bf16's own rounding. The
+// scales of a cell are first divided by a power of two, which brings the largest
+// to [1, 2) and is given back to the probabilities: one operation for each
+// instead of one per block. 2048 tokens behind 16000, 32 / 8 heads of 128: 1215
+// us without, 1112 us with it in fp16, where the second rounding would add a
+// quarter to the result's error. (Not for K: an error of a score is multiplied by
+// the score's size. It would save a fifth.)
+//
+// Shares (attn_device.hpp) of such items only where a few long ones would leave
+// most of the GPU idle; attn.hip's plan has the rule.
+#include <type_traits>
+
 #include "attn_device.hpp"
 
 namespace qmat {
@@ -176,7 +184,7 @@ template <int D, bool kKQ4, bool kVQ4, int kWv, int kTiles, typename T>
 __global__ __launch_bounds__(kWv * kWave, kWv == 8 || D == 64 ? 2 : 1)
 void attn_prompt_kernel(const Params p) {
   constexpr bool kPair = sizeof(T) == 4;
-  constexpr bool kFold = !kPair;  // V's scales go into the codes
+  constexpr bool kFold = std::is_same_v<T, __bf16>;  // V's scales go into the codes
   constexpr int kNb = D / 32;
   constexpr int kItemCols = kWv * kTiles * kCols;
   constexpr int kBatch = batch_for<D>(), kQuarters = kBatch / 16;
@@ -194,22 +202,26 @@ void attn_prompt_kernel(const Params p) {
   const bool stage_k = wave < kWv / 2;
   const int st = threadIdx.x % KS::kSides;  // this thread on its side
 
-  // Heads of one item next to each other (they share cache lines), late items
-  // first (causal ones see more).
-  const uint32_t total = (uint32_t)p.items * p.kv_heads;
-  for (uint32_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const int head = (int)(id % p.kv_heads);
-    const int x = p.items - 1 - (int)(id / p.kv_heads);
-    int b = x / p.col_tiles, ct = x % p.col_tiles;
+  __shared__ int starts[kMaxItems + 1];
+  const bool shared = p.shares > 0;
+  const int all_tiles =
+      shared ? count_tiles<kItemCols, kBatch, kWv * kWave>(p, starts, blockIdx.x == 0) : 0;
+  const int shares = share_count(p, all_tiles);
+
+  // Batches [from, to) of an item; place: of its partial result, -1: the item is
+  // this workgroup's alone.
+  const auto work = [&](int head, int item, int from, int to, int place) {
+    int b = item / p.col_tiles, ct = item % p.col_tiles;
     if (p.search) {
-      b = find_last(p.n_seqs, x, [&](int i) { return first_tile<kItemCols>(p, i); });
-      ct = x - first_tile<kItemCols>(p, b);
+      b = find_last(p.n_seqs, item, [&](int i) { return first_tile<kItemCols>(p, i); });
+      ct = item - first_tile<kItemCols>(p, b);
     }
     const Seq s = sequence(p, b);
     const int cols = s.nq * p.group;
-    if (ct < 0 || ct * kItemCols >= cols) continue;
-    const Span span = tile_span<kItemCols>(p, s, ct);
-    const int begin = span.lo & ~(kBatch - 1), end = span.hi;
+    if (ct < 0 || ct * kItemCols >= cols) return;
+    const Span span = tile_span<kItemCols, kBatch>(p, s, ct);
+    const int begin = span.lo + from * kBatch;
+    const int end = to < span.tiles<kBatch>() ? span.lo + to * kBatch : span.hi;
     lds_barrier();  // the last item's operands are used
 
     // this lane's query rows, and what the wave's rows see: some, all
@@ -543,20 +555,50 @@ void attn_prompt_kernel(const Params p) {
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
       const float sum = groups_sum(l[n]);
-      const float inv = 1.0f / sum;
+      const float inv = place >= 0 ? 1.0f : 1.0f / sum;
       if (!live[n]) continue;
       const int c = wave_col + n * kCols + col;
+      const int64_t row = ((int64_t)place * p.kv_heads + head) * p.part_rows + c % kItemCols;
       T* dst = static_cast<T*>(p.out) + at[n] * p.out_stride +
                ((int64_t)head * p.group + c % p.group) * D + 4 * g;
+      if (place >= 0 && g == 0) p.part_ml[row] = float2{m[n], sum};
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const float f = kVQ4 && !kFold && (i & 1) ? inv * 0.0625f : inv;
-        float y[4];
+        f32x4 y = o[n][i] * f;
+        y = f32x4{y[0], y[2], y[1], y[3]};  // slots to dimensions
+        if (place >= 0) {
+          *reinterpret_cast<f32x4*>(p.part_o + row * D + 16 * i + 4 * g) = y;
+        } else {
+          float out[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : o[n][i][e] * f;
-        const float out[4] = {y[0], y[2], y[1], y[3]};  // slots to dimensions
-        store_f32<T, 4>(dst + 16 * i, out);
+          for (int e = 0; e < 4; ++e) out[e] = sum == 0.0f ? 0.0f : y[e];
+          store_f32<T, 4>(dst + 16 * i, out);
+        }
       }
+    }
+  };
+
+  // Heads of one item or share next to each other (they share cache lines).
+  const uint32_t units = shared ? shares : p.items;
+  const uint32_t total = units * p.kv_heads;
+  for (uint32_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const int head = (int)(id % p.kv_heads), unit = (int)(id / p.kv_heads);
+    if (!shared) {
+      work(head, p.items - 1 - unit, 0, 0x7FFFFFFF, -1);  // late ones first: causal ones see more
+      continue;
+    }
+    const int begin = share_start(unit, shares, all_tiles);
+    const int stop = share_start(unit + 1, shares, all_tiles);
+    int at = begin;
+    int item = find_last(p.items, at, [&](int i) { return starts[i]; });
+    for (; at < stop; ++item) {
+      const int first = starts[item], last = starts[item + 1];
+      if (first == last) continue;
+      const int to = stop < last ? stop : last;
+      const bool alone = begin <= first && last <= stop;
+      work(head, item, at - first, to - first, alone ? -1 : unit + item);
+      at = to;
     }
   }
 }
@@ -565,16 +607,16 @@ constexpr int64_t kMaxGrid = 1 << 22;
 
 template <int D, typename T>
 void launch_for(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream) {
-  const int64_t total = (int64_t)p.items * p.kv_heads;
+  const int64_t total = (int64_t)(p.shares > 0 ? p.shares : p.items) * p.kv_heads;
   const dim3 grid((unsigned)(total < kMaxGrid ? total : kMaxGrid));
   const auto go = [&](auto kq, auto vq) {
     constexpr bool kK = decltype(kq)::value, kV = decltype(vq)::value;
+    // a pair of fp16 for each query leaves no registers for a second tile
+    constexpr int kTiles = sizeof(T) == 2 ? 2 : 1, kWv = 8;
     if constexpr (D <= 128) {
-      // a pair of fp16 for each query leaves no registers for a second tile
-      constexpr int kTiles = sizeof(T) == 2 ? 2 : 1;
-      if (rows == 128 * kTiles) {
-        hipLaunchKernelGGL((attn_prompt_kernel<D, kK, kV, 8, kTiles, T>), grid, dim3(8 * kWave), 0,
-                           stream, p);
+      if (rows == kWv * kTiles * kCols) {
+        hipLaunchKernelGGL((attn_prompt_kernel<D, kK, kV, kWv, kTiles, T>), grid,
+                           dim3(kWv * kWave), 0, stream, p);
         return;
       }
     }
@@ -603,9 +645,13 @@ void launch_as(const qmat_attn_args& a, const Params& p, int rows, hipStream_t s
 
 namespace attn {
 
-int prompt_rows(const qmat_attn_args& a, bool many) {
-  if (!many || a.head_dim > 128) return 64;
-  return a.dtype == kDtypeF32 ? 128 : 256;
+PromptShape prompt_shape(const qmat_attn_args& a, int64_t seq_rows) {
+  PromptShape s;
+  s.batch = a.head_dim == 256 ? batch_for<256>() : batch_for<64>();
+  s.fill = 256;
+  const int most = a.head_dim > 128 ? 64 : a.dtype == kDtypeF32 ? 128 : 256;
+  s.rows = seq_rows > 64 ? most : 64;
+  return s;
 }
 
 void launch_prompt(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream) {
