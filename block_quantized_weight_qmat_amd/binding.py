@@ -491,6 +491,8 @@ def attn_args(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     device = q.device
     if out.shape != shape or out.device != device:
         raise ValueError("out must have the shape and device of q")
+    if T > 0 and out.data_ptr() == q.data_ptr():
+        raise ValueError("out must not overlap q")
     _flat(page_table, "page_table", torch.int32, device)
     _flat(q_start, "q_start", torch.int32, device)
     _flat(kv_len, "kv_len", torch.int32, device)
@@ -519,8 +521,8 @@ def attn(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     page_table [seqs, pages] (all int32). scale: 1 / sqrt(head_dim) if None.
     max_q: an upper bound of a sequence's tokens (all tokens if None);
     max_kv: of kv_len, as an estimate (what the table holds if None). A
-    workspace of attn_workspace_bytes() is allocated when none is given. Rows
-    of out that belong to no sequence are left as they were (zeros in an out
+    workspace of attn_workspace_bytes() is allocated when none is given; out
+    and the workspace must not overlap anything else that is used. Rows of out that belong to no sequence are left as they were (zeros in an out
     allocated here)."""
     if out is None:
         out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)

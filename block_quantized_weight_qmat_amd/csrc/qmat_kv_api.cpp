@@ -14,6 +14,7 @@ constexpr int64_t kMaxDim = 0x7FFFFFFFLL;
 constexpr int64_t kMaxTokens = 1LL << 24;  // also sequences
 constexpr int64_t kMaxHeads = 1LL << 12;
 constexpr int64_t kMaxCells = 1LL << 30;   // of one sequence; also query rows of a cache head
+constexpr int64_t kMaxRows = 1LL << 30;    // of all tokens and heads
 
 bool cache_fmt_ok(int fmt) { return fmt == QMAT_Q4_0 || fmt == QMAT_Q8_0; }
 
@@ -73,7 +74,8 @@ int check_attn(const qmat_attn_args& a) {
       a.heads / a.kv_heads > 256)
     return QMAT_E_SHAPE;
   if (a.n_tokens < 0 || a.n_tokens > kMaxTokens || a.n_seqs < 0 || a.n_seqs > kMaxTokens ||
-      a.max_q < 0 || a.max_q > kMaxTokens || a.max_q * (a.heads / a.kv_heads) > kMaxCells)
+      a.max_q < 0 || a.max_q > kMaxTokens || a.max_q * (a.heads / a.kv_heads) > kMaxCells ||
+      a.n_tokens * a.heads > kMaxRows || a.n_seqs * a.kv_heads > kMaxRows)
     return QMAT_E_SHAPE;
   if (a.max_kv < 0 || a.window < 0 || a.window > kMaxDim || a.cells < 0 || a.cells > kMaxDim)
     return QMAT_E_SHAPE;

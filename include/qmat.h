@@ -386,7 +386,7 @@ int qmat_kv_write(int fmt, const float *rows, const float *bias, void *cache,
  *   slots:  DEVICE int32 [n]: the cell that row i is written to. A slot
  *           outside [0, cells) skips its row (padding of a batch). The other
  *           slots of a call must differ from each other; a cell named twice
- *           is left with blocks of either row.
+ *           is left with bytes of either row, mixed even within a block.
  *   k_cache, v_cache: cells rows of qmat_row_bytes(k_fmt, dim) and
  *           qmat_row_bytes(v_fmt, dim) bytes; bytes of other cells stay.
  *   All pointers 16-byte aligned, the strides whole multiples of 16 bytes
@@ -437,15 +437,19 @@ int qmat_kv_load(int k_fmt, int v_fmt, int dtype, const void *k_cache,
  *   fp16 block scales are applied in fp32 (K) or to the probabilities (V);
  *   scores, maxima, sums and outputs are held in fp32. For fp16 and bf16
  *   the queries are exact (within 2^-24 of a row's largest element) and the
- *   products probability x V scale are rounded once to 11 bits; for fp32 both
+ *   products probability x V scale are rounded once to 11 bits (bf16 prompts:
+ *   the probability and the product V code x V scale, once each); for fp32 both
  *   are carried as pairs of fp16 (22 bits). Relative L2 error against exact
  *   arithmetic, before rounding to dtype: below 1e-5 (fp32), 5e-4 (others).
  *   Cells that a token does not see have no effect on it, whatever their
- *   bytes hold (infinite or NaN scales included).
+ *   bytes hold (infinite or NaN scales included); one that sees a cell with
+ *   an infinite or NaN scale has no finite result in some or all elements.
+ *   Scores (scale * q . k) must be within fp32's range.
  *
  *   Limits (QMAT_E_SHAPE): head_dim 64, 128 or 256; heads a multiple of
  *   kv_heads and at most 4096, heads / kv_heads at most 256, max_q * heads /
- *   kv_heads at most 2^30; page_size a power of two;
+ *   kv_heads, n_tokens * heads and n_seqs * kv_heads at most 2^30; page_size a
+ *   power of two;
  *   pages_per_seq * page_size <= 2^30; cells <= 2^31 - 1; n_tokens, n_seqs
  *   <= 2^24; max_q <= 2^24; strides >= heads * head_dim; scale finite.
  *   Device values outside their range do no harm: len_b is cut to
@@ -454,6 +458,7 @@ int qmat_kv_load(int k_fmt, int v_fmt, int dtype, const void *k_cache,
  *   [0, cells / page_size) count as not seen. Page numbers at and behind
  *   ceil(len_b / page_size) are not read.
  *   Rows of out that belong to no sequence are left as they were.
+ *   out and the workspace must not overlap each other or any input.
  */
 typedef struct qmat_attn_args {
   int32_t k_fmt, v_fmt;      /* QMAT_Q4_0 or QMAT_Q8_0 each                  */

@@ -120,6 +120,17 @@ int main() {
   WITH(max_q, -1, QMAT_E_SHAPE, 0);
   WITH(max_q, ((int64_t)1 << 24) + 1, QMAT_E_SHAPE, 0);
   WITH(max_kv, -1, QMAT_E_SHAPE, 0);
+  {
+    qmat_attn_args x = good();  // query rows, and sequences x cache heads, in 2^30
+    x.heads = 512;
+    x.kv_heads = 256;
+    x.q_stride = x.out_stride = x.heads * x.head_dim;
+    x.n_tokens = ((int64_t)1 << 21) + 1;
+    EXPECT(qmat_attn(&x, NULL, 0, NULL), QMAT_E_SHAPE, 0);
+    x.n_tokens = 4;
+    x.n_seqs = ((int64_t)1 << 22) + 1;
+    EXPECT(qmat_attn(&x, NULL, 0, NULL), QMAT_E_SHAPE, 0);
+  }
   WITH(max_kv, INT64_MAX, QMAT_E_WORKSPACE, 0);  // an estimate of any size
   WITH(window, -1, QMAT_E_SHAPE, 0);
   WITH(window, big, QMAT_E_SHAPE, 0);

@@ -107,6 +107,32 @@ def test_load_values(lib, k_fmt, v_fmt, dtype, n, dim, bias):
     assert torch.all(out[:, 2 * dim:] == 9.0).item()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_store_load_large(lib, dtype):
+    """One call for many rows (several blocks a lane; results past the caches) does what calls for a few do."""
+    import torch
+    n, dim, cells = 33001, 1056, 33100
+    g = torch.Generator(device="cuda").manual_seed(7)
+    k, v = (torch.randn((n, dim), generator=g, device="cuda").to(torch_type(dtype)) for _ in range(2))
+    bias = torch.randn(dim, generator=g, device="cuda")
+    slots = torch.randperm(cells, generator=g, device="cuda")[:n].int()
+    slots[::997] = -1
+    slots[-1] = cells
+    caches = [torch.full((cells, oracle.row_bytes(f, dim)), 0xA5, dtype=torch.uint8, device="cuda")
+              for f in ("q8_0", "q4_0") * 2]
+    say(f"store of {n} rows {dtype}")
+    lib.kv_store("q8_0", "q4_0", k, v, slots, *caches[:2], k_bias=bias)
+    step = 2000
+    for i in range(0, n, step):
+        lib.kv_store("q8_0", "q4_0", k[i:i + step], v[i:i + step], slots[i:i + step].clone(), *caches[2:], k_bias=bias)
+    assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    say(f"load of {n} rows {dtype}")
+    got = lib.kv_load("q8_0", "q4_0", *caches[:2], slots, dim, dtype=k.dtype, k_bias=bias)
+    for i in range(0, n, step):
+        want = lib.kv_load("q8_0", "q4_0", *caches[:2], slots[i:i + step].clone(), dim, dtype=k.dtype, k_bias=bias)
+        assert torch.equal(got[0][i:i + step], want[0]) and torch.equal(got[1][i:i + step], want[1])
+
+
 # ------------------------------------------------------------------------ attention
 
 def largest_scale(fmt, packed):
@@ -121,7 +147,7 @@ class Case:
     """A batch with its caches, page table and 64-bit answer. seqs: (new tokens, cells) each."""
 
     def __init__(self, seqs, heads, kv_heads, head_dim, k_fmt="q4_0", v_fmt="q4_0", dtype="f32", page=16, causal=True,
-                 window=0, pad=0, seed=0, q_scale=1.0, v_scale=1.0, bad_pages=(), hurt=()):
+                 window=0, pad=0, seed=0, q_scale=1.0, v_scale=1.0, bad_pages=(), hurt=(), scale=None):
         rng = np.random.default_rng(seed)
         self.__dict__.update(seqs=seqs, heads=heads, kv_heads=kv_heads, head_dim=head_dim, k_fmt=k_fmt, v_fmt=v_fmt,
                              dtype=dtype, page=page, causal=causal, window=window)
@@ -158,7 +184,7 @@ class Case:
         import torch
         self.qt = torch.from_numpy(q).to(torch_type(dtype))
         qd = self.qt.double().numpy()[:, 1:1 + heads]
-        self.scale = head_dim ** -0.5
+        self.scale = head_dim ** -0.5 if scale is None else scale
         self.want, self.bound = np.zeros((T, heads, head_dim)), np.zeros((T, heads, head_dim))
         for b, (n, kv) in enumerate(seqs):
             s = slice(self.start[b], self.start[b + 1])
@@ -166,7 +192,7 @@ class Case:
             rows = maps[b][maps[b] >= 0]
             d, dv = (largest_scale(f, p[rows]) for f, p in ((k_fmt, self.k), (v_fmt, self.v)))
             self.want[s] = o
-            self.bound[s] = ref.element_bound(qd[s], d, 15 if k_fmt == "q4_0" else 255, max(kv, 1), self.scale, mag, o, dtype,
+            self.bound[s] = ref.element_bound(qd[s], d, 15 if k_fmt == "q4_0" else 255, max(kv, 1), abs(self.scale), mag, o, dtype,
                                               dv * (8 if v_fmt == "q4_0" else 128))
         self.T = T
 
@@ -174,7 +200,7 @@ class Case:
         import torch
         q = self.qt.cuda()[:, 1:1 + self.heads]  # a slice: rows are heads + 2 apart
         out = torch.full((self.T, self.heads + 1, self.head_dim), 77.0, dtype=q.dtype, device="cuda")
-        args = dict(causal=self.causal, window=self.window, max_q=max(n for n, _ in self.seqs), out=out[:, :self.heads])
+        args = dict(causal=self.causal, window=self.window, scale=self.scale, max_q=max(n for n, _ in self.seqs), out=out[:, :self.heads])
         args.update(kw)
         lib.attn(self.k_fmt, self.v_fmt, q, dev(self.k), dev(self.v), dev(self.table), dev(self.start), dev(self.kv_len),
                  self.kv_heads, self.page, **args)
@@ -260,6 +286,98 @@ def test_attn_prompt_head_layouts(lib, heads, kv_heads):
     c.check(c.run(lib))
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1e-30, 0.3])
+@pytest.mark.parametrize("n", [1, 70])
+def test_attn_scales(lib, n, scale):
+    """Any finite scale: 0 averages the cells, a negative one prefers the least alike."""
+    for dtype in DTYPES:
+        say(f"attn scale {scale} n={n} {dtype}")
+        c = Case([(n, 300), (n, n - 1), (n, 80)], 4, 2, 64, "q8_0", "q4_0", dtype, window=60, scale=scale, seed=n)
+        c.check(c.run(lib))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_attn_prompts_shared(lib, head_dim, dtype):
+    """Few rows behind many cells: their cells are shared out over workgroups, whole items beside parts of them."""
+    for seqs, fmts, kw in (([(70, 1500)], ("q4_0", "q4_0"), {}),
+                           ([(33, 1000), (0, 50), (90, 700), (1, 1), (40, 64)], ("q8_0", "q4_0"), {"pad": 3}),
+                           ([(80, 900)], ("q8_0", "q8_0"), {"window": 333, "page": 128}),
+                           ([(80, 900)], ("q4_0", "q8_0"), {"causal": False, "page": 1, "bad_pages": (0, 400, 401)})):
+        say(f"attn prompts shared {head_dim} {dtype} {seqs}")
+        c = Case(seqs, 4, 2, head_dim, *fmts, dtype, seed=head_dim + 2, **kw)
+        c.check(c.run(lib))
+        c.check(c.run(lib, max_kv=10 ** 6))
+
+
+def test_attn_many_sequences(lib):
+    """More sequences than are dealt out together, and a batch where one has many more tokens than the others."""
+    rng = np.random.default_rng(41)
+    for n, long in ((1100, 1), (400, 20), (90, 300)):
+        seqs = [(1, int(x)) for x in rng.integers(0, 40, n)]
+        seqs[7], seqs[8] = (long, 280 + long), (0, 12)
+        say(f"attn {n} sequences, one of {long} tokens")
+        c = Case(seqs, 4, 2, 64, "q4_0", "q8_0", "f16", seed=n)
+        c.check(c.run(lib))
+
+
+def test_attn_no_cells(lib):
+    """Empty caches and tables without columns: zeros for every token of a sequence."""
+    import torch
+    for n in (1, 70):
+        for pages, cells in ((0, 0), (0, 32), (3, 0)):
+            say(f"attn no cells n={n} pages={pages} cells={cells}")
+            q = torch.ones((2 * n, 4, 64), device="cuda")
+            out = torch.full_like(q, 3.0)
+            kc = torch.zeros((cells, oracle.row_bytes("q8_0", 128)), dtype=torch.uint8, device="cuda")
+            lib.attn("q8_0", "q8_0", q, kc, kc.clone(), torch.zeros((2, pages), dtype=torch.int32, device="cuda"),
+                     dev(np.array([0, n, 2 * n], np.int32)), dev(np.array([40, 7], np.int32)), 2, 16, out=out)
+            assert torch.all(out == 0).item()
+
+
+def test_attn_sees_a_cell_without_finite_value(lib):
+    """Rows that see a cell with infinite and NaN scales have no finite result; the others are exact (checked above)."""
+    import torch
+    for dtype in DTYPES:
+        for n, cells in ((1, 60), (100, 130), (80, 1200)):
+            say(f"attn hurt {dtype} n={n}")
+            c = Case([(n, cells)], 4, 2, 128, "q8_0", "q4_0", dtype, hurt=[(0, cells - n)], seed=10)
+            out = c.run(lib)[:n, :c.heads]
+            assert not torch.any(torch.isfinite(out).all(-1)).item()
+
+
+def test_attn_two_streams(lib):
+    """Calls on two streams at once, each with its own workspace, give what they give alone."""
+    import torch
+    cases = [Case([(1, 3000), (1, 70)], 8, 2, 128, "q8_0", "q4_0", "bf16", page=32, seed=51),
+             Case([(70, 1500)], 4, 2, 64, "q4_0", "q4_0", "f16", seed=52)]
+    alone = [c.run(lib) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    held = []
+    for c in cases:
+        q = c.qt.cuda()[:, 1:1 + c.heads]
+        held.append((q, dev(c.k), dev(c.v), dev(c.table), dev(c.start), dev(c.kv_len)))
+    outs = [[] for _ in cases]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for c, s, h, o in zip(cases, streams, held, outs):
+            with torch.cuda.stream(s):
+                o.append(lib.attn(c.k_fmt, c.v_fmt, *h, c.kv_heads, c.page, scale=c.scale, max_q=max(n for n, _ in c.seqs)))
+    torch.cuda.synchronize()
+    for c, a, o in zip(cases, alone, outs):
+        for x in o:
+            assert torch.equal(x, a[:, :c.heads])
+
+
+def test_attn_max_q(lib):
+    """A bound above the longest sequence changes nothing."""
+    for seqs in ([(2, 300), (1, 40)], [(70, 80), (1, 40)]):
+        for max_q in (None, 400, 100000):
+            say(f"attn {seqs} max_q={max_q}")
+            c = Case(seqs, 4, 2, 64, "q8_0", "q4_0", "bf16", pad=40, seed=61)
+            c.check(c.run(lib, max_q=max_q))
+
+
 def test_attn_splits(lib):
     """A sequence long enough to be split over workgroups, beside short and empty ones; max_kv too small, too large."""
     for dtype in DTYPES:
@@ -314,7 +432,7 @@ def test_attn_ranges_of_values(lib, dtype, n):
 def test_attn_same_bits_again_and_in_graphs(lib):
     """The same call twice, and captured and replayed with changed inputs, gives the eager call's bits."""
     import torch
-    for seqs, kw in (([(1, 900), (1, 40)], {}), ([(70, 300), (1, 5)], {})):
+    for seqs, kw in (([(1, 900), (1, 40)], {}), ([(70, 300), (1, 5)], {}), ([(70, 1700)], {})):
         c = Case(seqs, 8, 2, 128, dtype="bf16", seed=21)
         q = c.qt.cuda()[:, 1:1 + c.heads].contiguous()
         kc, vc, table, start, kv_len = dev(c.k), dev(c.v), dev(c.table), dev(c.start), dev(c.kv_len)
