@@ -519,7 +519,8 @@ def attn(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     paged caches k_cache, v_cache (uint8 [cells, row_bytes]): sequence b has
     the tokens q_start[b] .. q_start[b + 1] - 1 and kv_len[b] cells, found by
     page_table [seqs, pages] (all int32). scale: 1 / sqrt(head_dim) if None.
-    max_q: an upper bound of a sequence's tokens (all tokens if None);
+    max_q: an upper bound of a sequence's tokens (all tokens if None; it
+    chooses the kernel: give 1 for decode);
     max_kv: of kv_len, as an estimate (what the table holds if None). A
     workspace of attn_workspace_bytes() is allocated when none is given; out
     and the workspace must not overlap anything else that is used. Rows of out that belong to no sequence are left as they were (zeros in an out

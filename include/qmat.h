@@ -475,7 +475,8 @@ typedef struct qmat_attn_args {
   int64_t out_stride;        /* elements between tokens of out               */
   int64_t n_tokens;          /* rows of q and out                            */
   int64_t n_seqs;
-  int64_t max_q;             /* no sequence has more new tokens than this    */
+  int64_t max_q;             /* no sequence has more new tokens than this; it
+                                chooses the kernel, so 1 for decode          */
   int64_t max_kv;            /* the longest kv_len, or an estimate: it sets
                                 the work split and the workspace alone       */
   int64_t heads, kv_heads, head_dim;
