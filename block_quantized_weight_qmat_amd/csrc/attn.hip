@@ -523,18 +523,28 @@ void attn_split_kernel(const Params p) {
 }
 
 // Joins what several shares have of one query row: out = sum_s 2^(m_s - m) O_s /
-// sum_s 2^(m_s - m) l_s. One workgroup per row; D / 4 threads cover the row,
-// the others take shares in turn. A chain of four dependent loads bounds it: 6 us
-// for 32 rows of 250 parts each, 8 us for 4096 rows of two, 10 us for 8192.
-template <int D, int kJoinThreads, typename T>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p) {
-  constexpr int kX = D / 4, kY = kJoinThreads / kX;
-  __shared__ f32x4 part[kY][kX];
-  __shared__ float part_l[kY], wave_m[kJoinThreads / kWave];
-  const int x = threadIdx.x % kX, y = threadIdx.x / kX;
+// sum_s 2^(m_s - m) l_s, in one pass with a running m. D / 4 threads cover a row,
+// the others of the row's take parts in turn: a wave per row, four rows to a
+// workgroup, or a workgroup of 1024 per row where parts are many and rows few.
+// A chain of three dependent loads and the launch bound it: 5.6 us for 32 rows of
+// 64 parts each, 6.5 us for 4096 rows of a few, 9.2 us for 8192 (6.1, 8.4 and 10.4
+// with the maxima in a pass before and a workgroup of 64 for each row).
+template <int D, int kRowThreads, typename T>
+__global__ __launch_bounds__(kRowThreads < 256 ? 256 : kRowThreads)
+void attn_join_kernel(const Params p) {
+  constexpr int kX = D / 4, kY = kRowThreads / kX;
+  constexpr int kEach = 4;  // parts of a thread whose loads are in flight together
+  constexpr bool kAlone = kRowThreads == kWave;
+  constexpr int kWv = kRowThreads / kWave;
+  constexpr int kRows = kAlone ? 256 / kWave : 1;
+  __shared__ f32x4 part[kAlone ? 1 : kWv][kX];
+  __shared__ float part_m[kWv], part_l[kWv];
+  const int thread = threadIdx.x % kRowThreads;
+  const int x = thread % kX, y = thread / kX;
   const int total = p.starts[p.items], shares = share_count(p, total);
   const uint32_t rows = (uint32_t)(p.n_seqs * p.max_q) * p.heads;
-  for (uint32_t id = blockIdx.x; id < rows; id += gridDim.x) {
+  for (uint32_t id = blockIdx.x * kRows + threadIdx.x / kRowThreads; id < rows;
+       id += gridDim.x * kRows) {
     const int query_head = (int)(id % p.heads), head = query_head / p.group;
     const int b = (int)(id / p.heads) / p.max_q, tok = (int)(id / p.heads) % p.max_q;
     const int c = tok * p.group + query_head % p.group;
@@ -550,32 +560,70 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
     const auto place = [&](int i) {
       return ((int64_t)(first + i + item) * p.kv_heads + head) * p.part_rows + c % p.item_rows;
     };
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) m = fmaxf(m, p.part_ml[place(i)].x);
-#pragma unroll
-    for (int k = 32; k > 0; k >>= 1) m = fmaxf(m, shfl_xor_f(m, k));
-    if ((threadIdx.x & 63) == 0) wave_m[threadIdx.x >> 6] = m;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kJoinThreads / kWave; ++k) m = fmaxf(m, wave_m[k]);
-    const float ref = m == -INFINITY ? 0.0f : m;
+    float m = -INFINITY, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    float l = 0.0f;
-#pragma unroll 4
-    for (int i = y; i < n; i += kY) {
-      const float2 ml = p.part_ml[place(i)];
-      const float w = exp2_raw(ml.x - ref);
-      l += w * ml.y;
-      o += w * *reinterpret_cast<const f32x4*>(p.part_o + place(i) * D + 4 * x);
-    }
-    part[y][x] = o;
-    if (x == 0) part_l[y] = l;
-    __syncthreads();
-    if (y == 0) {
-      for (int i = 1; i < kY; ++i) {
-        o += part[i][x];
-        l += part_l[i];
+    for (int i0 = y; i0 < n; i0 += kEach * kY) {
+      float2 ml[kEach];
+      f32x4 v[kEach];
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int i = i0 + e * kY;
+        const int64_t from = place(i < n ? i : i0);
+        ml[e] = p.part_ml[from];
+        v[e] = *reinterpret_cast<const f32x4*>(p.part_o + from * D + 4 * x);
+        if (i >= n) ml[e].x = -INFINITY;
+        top = fmaxf(top, ml[e].x);
       }
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float alpha = exp2_raw(m - ref);
+      l *= alpha;
+      o *= alpha;
+      m = top;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const float w = exp2_raw(ml[e].x - ref);
+        l += w * ml[e].y;
+        o += w * v[e];
+      }
+    }
+    float all = m;  // of the wave's threads that have the same elements
+#pragma unroll
+    for (int k = kX; k < kWave; k <<= 1) all = fmaxf(all, shfl_xor_f(all, k));
+    const float w = exp2_raw(m - (all == -INFINITY ? 0.0f : all));
+    l *= w;
+    o *= w;
+#pragma unroll
+    for (int k = kX; k < kWave; k <<= 1) {
+      l += shfl_xor_f(l, k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += shfl_xor_f(o[e], k);
+    }
+    if constexpr (!kAlone) {
+      const int wave = threadIdx.x / kWave;
+      if ((threadIdx.x & 63) < kX) part[wave][x] = o;
+      if ((threadIdx.x & 63) == 0) {
+        part_m[wave] = all;
+        part_l[wave] = l;
+      }
+      __syncthreads();
+      if (y == 0) {
+        m = part_m[0];
+#pragma unroll
+        for (int i = 1; i < kWv; ++i) m = fmaxf(m, part_m[i]);
+        const float ref = m == -INFINITY ? 0.0f : m;
+        l = 0.0f;
+        o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kWv; ++i) {
+          const float v = exp2_raw(part_m[i] - ref);
+          l += v * part_l[i];
+          o += v * part[i][x];
+        }
+      }
+      __syncthreads();
+    }
+    if (y == 0) {
       const float inv = 1.0f / l;
       float r[4];
 #pragma unroll
@@ -583,7 +631,6 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const Params p)
       store_f32<T, 4>(
           static_cast<T*>(p.out) + at * p.out_stride + (int64_t)query_head * D + 4 * x, r);
     }
-    __syncthreads();
   }
 }
 
@@ -705,14 +752,16 @@ void launch_for(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
 template <typename T>
 void launch_join(const qmat_attn_args& a, const Params& p, hipStream_t stream) {
   const int64_t rows = (int64_t)p.n_seqs * p.max_q * p.heads;
-  const dim3 grid((unsigned)(rows < kMaxGrid ? rows : kMaxGrid));
   const auto go = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
     // few rows of many shares: many threads each; many rows: a wave each
-    if (p.shares > 32 * p.items)
+    const bool many = p.shares > 32 * p.items;
+    const int64_t wgs = many ? rows : (rows + 3) / 4;
+    const dim3 grid((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid));
+    if (many)
       hipLaunchKernelGGL((attn_join_kernel<D, 1024, T>), grid, dim3(1024), 0, stream, p);
     else
-      hipLaunchKernelGGL((attn_join_kernel<D, 64, T>), grid, dim3(64), 0, stream, p);
+      hipLaunchKernelGGL((attn_join_kernel<D, kWave, T>), grid, dim3(256), 0, stream, p);
   };
   if (a.head_dim == 64)
     go(std::integral_constant<int, 64>{});
