@@ -31,7 +31,7 @@
 // Measured: 2048 tokens behind 16384 cells, 32 / 8 heads of 128, Q4_0, bf16:
 // 1005 us, 0.58 PFLOP/s (a large bf16 product: 1.2); ragged prompts of up to 1531
 // tokens, heads of 64, Q8_0 / Q4_0, fp16: 242 us; 512 tokens, 16 / 8 x 128, Q8_0,
-// fp32: 37 us with the join. VALU issue takes half of the cycles, the matrix cores
+// fp32: 36 us with the join. VALU issue takes half of the cycles, the matrix cores
 // a fifth, waiting for LDS and the barrier most of the rest: 8 waves of 16 x 2
 // rows fill the registers, so a SIMD has two waves. Letting K's waves unpack
 // before and V's after their products, so that the two of a SIMD differ: 1000 us,
