@@ -151,11 +151,11 @@ void attn_split_kernel(const Params p) {
     if (p.search) {
       const int x = p.items - 1 - item;  // late tiles first: causal ones see more
       b = find_last(p.n_seqs, x, [&](int i) { return first_tile<kCols>(p, i); });
-      ct = x - first_tile<kCols>(p, b);
+      ct = (int)((uint32_t)x - (uint32_t)first_tile<kCols>(p, b));
     }
     const Seq s = sequence(p, b);
     const int cols = s.nq * p.group;
-    if (ct < 0 || ct * kCols >= cols) return;
+    if (ct < 0 || ct >= (cols + kCols - 1) / kCols) return;  // starts may be any numbers
     const Span span = tile_span<kCols, kCells>(p, s, ct);
     const int begin = span.lo + from * kCells;
     const int end = to < span.tiles<kCells>() ? span.lo + to * kCells : span.hi;

@@ -223,11 +223,11 @@ void attn_prompt_kernel(const Params p) {
     int b = item / p.col_tiles, ct = item % p.col_tiles;
     if (p.search) {
       b = find_last(p.n_seqs, item, [&](int i) { return first_tile<kItemCols>(p, i); });
-      ct = item - first_tile<kItemCols>(p, b);
+      ct = (int)((uint32_t)item - (uint32_t)first_tile<kItemCols>(p, b));
     }
     const Seq s = sequence(p, b);
     const int cols = s.nq * p.group;
-    if (ct < 0 || ct * kItemCols >= cols) return;
+    if (ct < 0 || ct >= (cols + kItemCols - 1) / kItemCols) return;  // starts may be any numbers
     const Span span = tile_span<kItemCols, kBatch>(p, s, ct);
     const int begin = span.lo + from * kBatch;
     const int end = to < span.tiles<kBatch>() ? span.lo + to * kBatch : span.hi;

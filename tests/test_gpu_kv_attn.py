@@ -369,6 +369,25 @@ def test_attn_two_streams(lib):
             assert torch.equal(x, a[:, :c.heads])
 
 
+def test_attn_any_numbers_in_q_start_and_kv_len(lib):
+    """Starts that fall, are negative or past the tokens, lengths outside the table: nothing but rows of out is written."""
+    import torch
+    big = 2 ** 31 - 1
+    for n, cells, max_q in ((8, 40, 8), (8, 400, 8), (90, 100, 90), (90, 1500, 90)):
+        for start in ([3, 1, big, -big, 5, n + 7, n], [-big - 1, -5, 0, 2, big, 1, 0], [0, 2, 2, 4, 4, 6, big]):
+            say(f"attn q_start {start} cells {cells}")
+            q = torch.ones((n, 8, 64), device="cuda", dtype=torch.bfloat16)
+            whole = torch.full((n + 40, 8, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+            kc = torch.zeros((2048, oracle.row_bytes("q4_0", 128)), dtype=torch.uint8, device="cuda")
+            table = torch.arange(6 * 100, device="cuda").int().reshape(6, 100) % 128
+            lib.attn("q4_0", "q4_0", q, kc, kc.clone(), table, dev(np.array(start, np.int64).astype(np.int32)),
+                     dev(np.array([cells, -7, big, cells, -big, 5], np.int32)), 2, 16, max_q=max_q, max_kv=cells,
+                     out=whole[20:20 + n])
+            torch.cuda.synchronize()
+            assert torch.all(whole[:20] == 7.0).item() and torch.all(whole[20 + n:] == 7.0).item()
+            assert torch.all((whole == 7.0) | (whole == 0.0)).item()  # scales of 0: every value is 0
+
+
 def test_attn_max_q(lib):
     """A bound above the longest sequence changes nothing."""
     for seqs in ([(2, 300), (1, 40)], [(70, 80), (1, 40)]):
