@@ -547,10 +547,12 @@ def test_cells_past_32_bit_offsets(lib):
     kd, vd = (oracle.dequant("q8_0", oracle.quantize("q8_0", x), n, dim) for x in (k, v))
     assert np.array_equal(k2.cpu().numpy(), kd.astype(np.float32))
     assert np.array_equal(v2.cpu().numpy(), vd.astype(np.float32))
-    for tokens in (1, 40):
+    small = (table[0][:, None] * 4 + np.arange(4)).reshape(1, 8).astype(np.int32)  # the same cells in pages of 16
+    for tokens, size in ((1, page), (1, 16), (40, page), (70, page), (70, 16)):
+        say(f"attn {tokens} tokens, pages of {size}")
         q = rng.standard_normal((tokens, heads, D)).astype(np.float32)
-        out = lib.attn("q8_0", "q8_0", dev(q), kc, vc, dev(table), dev(np.array([0, tokens], np.int32)),
-                       dev(np.array([n], np.int32)), kv_heads, page)
+        out = lib.attn("q8_0", "q8_0", dev(q), kc, vc, dev(table if size == page else small),
+                       dev(np.array([0, tokens], np.int32)), dev(np.array([n], np.int32)), kv_heads, size)
         want, _ = ref.attention(q.astype(np.float64), kd, vd, np.arange(n), kv_heads, tokens, n, D ** -0.5, True, 0)
         got = out.double().cpu().numpy()
         assert np.linalg.norm(got - want) <= ref.l2_bound("f32") * np.linalg.norm(want)
