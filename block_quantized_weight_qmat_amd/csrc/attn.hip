@@ -69,6 +69,7 @@ struct WaveLds {
   uint8_t planes[(kVQ4 ? 1 : 2) * kNb * kPlane];
   uint16_t kd[kCells * kNb];  // block scales, [cell][block]
   uint16_t vd[kCells * kNb];
+  uint16_t ve[kCells];  // V's exponents, see v_exponent
 };
 
 // 8 bytes of a column: byte n (= lane % 16) of the 16-byte code rows of the
@@ -86,9 +87,7 @@ template <int D>
 struct State {
   f32x4 o[D / 16];  // O^T; odd tiles of Q4_0: times 16
   float m;          // row reference: probabilities are 2^(s - m)
-  float top;        // largest score so far
   float l;          // this lane's part of the sum
-  int e;            // exponent field of the largest V scale so far
 };
 
 // An item is a column tile of a sequence. With p.shares == 0 a workgroup has
@@ -204,9 +203,8 @@ void attn_split_kernel(const Params p) {
     State<D> st;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) st.o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    st.m = st.top = -INFINITY;
+    st.m = -INFINITY;
     st.l = 0.0f;
-    st.e = 0;
 
     const int32_t* pages = p.table + (int64_t)b * p.pages_per_seq;
     const uint8_t* k_base = p.kc + (int64_t)head * KP::kBytes;
@@ -284,7 +282,6 @@ void attn_split_kernel(const Params p) {
       }
       reads_end();
       // scales side by side, V's codes into planes
-      uint32_t d_max = 0u;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int cell = i * kStep + lane / kNb;
@@ -303,8 +300,7 @@ void attn_split_kernel(const Params p) {
           *reinterpret_cast<u32x4*>(mine.planes + (2 * blk + 1) * kPlane + cell * 16) =
               u32x4{w[4], w[5], w[6], w[7]} ^ 0x80808080u;
         }
-        const uint32_t size = (seen >> cell) & 1 ? v_d[i] & 0x7FFFu : 0u;
-        d_max = size > d_max ? size : d_max;
+        mine.ve[cell] = v_exponent<kNb>(v_d[i]);
       }
       wave_sync();
       // scales of cells 8g..8g+7 and of the S operands' rows; V's columns
@@ -322,7 +318,6 @@ void attn_split_kernel(const Params p) {
       for (int i = 0; i < (kVQ4 ? kNb : 2 * kNb); ++i)
         v_col[i] = read_column(mine.planes + i * kPlane, lane);
       reads_end();
-      d_max = wave_max_u(d_max);
       const bool all = seen == ~0u && j0 >= all_lo && j0 + kCells <= all_hi;
 
       // scores of cells 8g..8g+7
@@ -378,17 +373,16 @@ void attn_split_kernel(const Params p) {
         }
       }
 
-      // running maximum. The reference m also carries the exponent of the
-      // largest V scale, so that probability x scale stays below 2^14 and the
-      // largest are far above fp16's subnormals.
-      float mx = sc[0];
+      uint32_t ve[4];  // read here: registers are short above
+      read_scales<4>(mine.ve + 8 * g, ve);
+      // Running maximum: of a score and its cell's V exponent, so that the largest
+      // product of a probability and a V scale lies below 2^14 and near it, far above
+      // fp16's subnormals, whatever the scales of cells that the row does not see or
+      // hardly weighs.
+      float mx = fmaf(sc[0], cs, half_of(ve[0], 0));
 #pragma unroll
-      for (int e = 1; e < 8; ++e) mx = fmaxf(mx, sc[e]);
-      mx = groups_max(mx) * cs;
-      const int ex = d_max >> 10 > 30 ? 30 : (int)(d_max >> 10);  // d < 2^(ex - 14)
-      st.e = ex > st.e ? ex : st.e;
-      st.top = fmaxf(st.top, mx);
-      const float m = st.top + (float)(st.e - 28);
+      for (int e = 1; e < 8; ++e) mx = fmaxf(mx, fmaf(sc[e], cs, half_of(ve[e / 2], e & 1)));
+      const float m = fmaxf(st.m, groups_max(mx) - 28.0f);
       const float ref = m == -INFINITY ? 0.0f : m;
       if (__ballot(m != st.m) != 0) {
         const float alpha = exp2_raw(st.m - ref);

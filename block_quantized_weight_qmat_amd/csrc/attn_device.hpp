@@ -220,16 +220,16 @@ __device__ __forceinline__ uint32_t row_max_u(uint32_t v) {
   return o > v ? o : v;
 }
 
-// Largest value of the wave, as a scalar.
-__device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
-  v = row_max_u<0x121>(v);  // rotations of 16 lanes by 1, 2, 4, 8
-  v = row_max_u<0x122>(v);
-  v = row_max_u<0x124>(v);
-  v = row_max_u<0x128>(v);
-  const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
-  const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
-  const uint32_t e = a > b ? a : b, f = c > d ? c : d;
-  return e > f ? e : f;
+// The exponent e of a cell's V scales as fp16, from a scale of each of the kNb lanes
+// that have its blocks: the largest |scale| is below 2^(e - 14).
+template <int kNb>
+__device__ __forceinline__ uint16_t v_exponent(uint32_t d) {
+  uint32_t v = d & 0x7FFFu;
+  v = row_max_u<0xB1>(v);                              // lanes 1,0,3,2
+  if constexpr (kNb >= 4) v = row_max_u<0x4E>(v);      // lanes 2,3,0,1
+  if constexpr (kNb == 8) v = row_max_u<0x141>(v);     // 8 lanes mirrored
+  v >>= 10;
+  return __builtin_bit_cast(uint16_t, (_Float16)(uint16_t)(v > 30 ? 30 : v));
 }
 
 __device__ __forceinline__ float half_of(uint32_t w, int hi) {

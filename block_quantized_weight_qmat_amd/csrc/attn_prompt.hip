@@ -113,10 +113,10 @@ struct Operands {
   uint8_t v[kBatch * v_row_bytes<D>()];
   uint16_t kd[kBatch * D / 32];  // block scales, [cell][block]
   uint16_t vd[kBatch * D / 32];
+  uint16_t ve[kBatch];   // V's exponents as fp16: a cell's scales are below 2^(e - 14)
   float v_unit[kBatch];  // of scales in the codes: what they were divided by
-  // Of each wave that stages V: its largest |scale| as fp16 bits, and the cells
-  // with an infinite one or a NaN, which count as 0 here.
-  uint32_t d_max[kWv / 2];
+  // Of each wave that stages V: the cells with an infinite scale or a NaN, which
+  // count as 0 here.
   uint32_t bad[kWv / 2][2];
 };
 
@@ -204,6 +204,7 @@ void attn_prompt_kernel(const Params p) {
   typedef PromptLds<D, kKQ4, kVQ4, kWv> Lds;
   __shared__ __attribute__((aligned(16))) uint8_t lds_bytes[sizeof(Lds)];
   Lds& lds = *reinterpret_cast<Lds*>(lds_bytes);
+  static_assert(sizeof(lds.op[0]) % 16 == 0, "16-byte reads of both stay aligned");
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -263,13 +264,12 @@ void attn_prompt_kernel(const Params p) {
     const int all_lo = first_cell(p, s, last_tok), all_hi = last_cell(p, s, first_tok);
 
     f32x4 o[kTiles][D / 16];
-    float m[kTiles], top[kTiles], l[kTiles];
-    int ex = 0;  // exponent field of the largest V scale so far
+    float m[kTiles], l[kTiles];
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[n][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      m[n] = top[n] = -INFINITY;
+      m[n] = -INFINITY;
       l[n] = 0.0f;
     }
 
@@ -327,7 +327,6 @@ void attn_prompt_kernel(const Params p) {
           }
         }
       } else {
-        uint32_t d_max = 0u;
         uint64_t bad = 0;
 #pragma unroll
         for (int i = 0; i < VS::kBlocks; ++i) {
@@ -338,8 +337,11 @@ void attn_prompt_kernel(const Params p) {
           const bool finite = (d & 0x7C00u) != 0x7C00u;
           bad |= __ballot(!finite);
           uint32_t low = 0u, high = 0u;
+          int field = 0;
+          if (kFold || blk == 0) field = scale_field<D, kVQ4>(lds.v_raw[n], cell);
+          if (blk == 0)
+            op.ve[cell] = __builtin_bit_cast(uint16_t, (_Float16)(uint16_t)field);
           if constexpr (kFold) {
-            const int field = scale_field<D, kVQ4>(lds.v_raw[n], cell);
             const float inverse = finite ? 1.0f / power_of(field) : 0.0f;
             low = finite ? scale_pair(d, inverse) : 0u;
             high = finite ? scale_pair(d, inverse * 0.0625f) : 0u;
@@ -353,8 +355,6 @@ void attn_prompt_kernel(const Params p) {
                         times(a.w, scale)};
             *reinterpret_cast<u32x4*>(op.v + cell * v_row_bytes<D>() + blk * 64 + at) = a;
           };
-          const uint32_t size = finite && ((seen1 >> cell) & 1) ? d & 0x7FFFu : 0u;
-          d_max = size > d_max ? size : d_max;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             if constexpr (kVQ4) {  // words 2e, 2e + 1: half of the low and of the high tile
@@ -380,10 +380,8 @@ void attn_prompt_kernel(const Params p) {
             }
           }
         }
-        d_max = wave_max_u(d_max);
         if (kBatch == 32) bad = (bad | bad >> 32) & 0xFFFFFFFFull;
         if (lane == 0) {
-          op.d_max[wave - kWv / 2] = d_max;
           op.bad[wave - kWv / 2][0] = (uint32_t)bad;
           op.bad[wave - kWv / 2][1] = (uint32_t)(bad >> 32);
         }
@@ -417,15 +415,12 @@ void attn_prompt_kernel(const Params p) {
       load_page(j0 + 4 * kBatch);
       const Operands<D, kKQ4, kVQ4, kWv>& op = lds.op[turn];
       if (!works || now_seen == 0 || j0 >= some_hi || j0 + kBatch <= some_lo) continue;
-      uint32_t d_max = op.d_max[0], bad_lo = op.bad[0][0], bad_hi = op.bad[0][1];
+      uint32_t bad_lo = op.bad[0][0], bad_hi = op.bad[0][1];
 #pragma unroll
       for (int i = 1; i < kWv / 2; ++i) {
-        d_max = op.d_max[i] > d_max ? op.d_max[i] : d_max;
         bad_lo |= op.bad[i][0];
         bad_hi |= op.bad[i][1];
       }
-      const int ex_now = __builtin_amdgcn_readfirstlane(d_max >> 10);  // d < 2^(ex - 14)
-      ex = ex_now > ex ? ex_now : ex;
       const uint64_t full = kBatch == 64 ? ~0ull : 0xFFFFFFFFull;
       const bool all = now_seen == full && j0 >= all_lo && j0 + kBatch <= all_hi;
 
@@ -483,15 +478,20 @@ void attn_prompt_kernel(const Params p) {
           }
       }
 
-      // running maximum; its reference also carries the exponent of the largest
-      // V scale, so that probability x scale stays below 2^14
+      // running maximum, of a score and its cell's V exponent: the largest product of
+      // a probability and a V scale lies below 2^14 and near it, whatever the scales of
+      // cells that the row does not see or hardly weighs
+      u32x2 ve[kQuarters];
+#pragma unroll
+      for (int t = 0; t < kQuarters; ++t)
+        ve[t] = *reinterpret_cast<const u32x2*>(op.ve + 16 * t + 4 * g);
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
-        float mx = sc[n][0];
+        float mx = -INFINITY;
 #pragma unroll
-        for (int e = 1; e < 4 * kQuarters; ++e) mx = fmaxf(mx, sc[n][e]);
-        top[n] = fmaxf(top[n], groups_max(mx) * cs[n]);
-        const float now = top[n] + (float)(ex - 28);
+        for (int e = 0; e < 4 * kQuarters; ++e)
+          mx = fmaxf(mx, fmaf(sc[n][e], cs[n], half_of(ve[e >> 2][(e >> 1) & 1], e & 1)));
+        const float now = fmaxf(m[n], groups_max(mx) - 28.0f);
         const float ref = now == -INFINITY ? 0.0f : now;
         if (__ballot(now != m[n]) != 0) {
           const float alpha = exp2_raw(m[n] - ref);

@@ -1,0 +1,100 @@
+"""Attention over the quantized cache where its arithmetic is strained: V scales
+far apart. Held to the 64-bit formula within kv_reference's bounds.
+"""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+import oracle
+from test_gpu_kv_attn import DTYPES, Case, dev, largest_scale, lib, say, torch_type  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_of(c, b):
+    """Cache rows of the cells of sequence b."""
+    j = np.arange(c.seqs[b][1])
+    return c.table[b, j // c.page].astype(np.int64) * c.page + j % c.page
+
+
+def blocks_of(packed, fmt):
+    """A view [cells][blocks][bytes] of packed rows."""
+    return packed.reshape(packed.shape[0], -1, oracle.block_bytes(fmt))
+
+
+def set_scales(packed, fmt, rows, bits):
+    """Gives all blocks of the named rows the fp16 scale of these bits."""
+    blocks_of(packed, fmt)[rows, :, :2] = np.frombuffer(np.uint16(bits).tobytes(), np.uint8)
+
+
+def again(c):
+    """The 64-bit answer and its bound from what c.k, c.v and c.qt hold now."""
+    dim = c.kv_heads * c.head_dim
+    kd, vd = (oracle.dequant(f, p, p.shape[0], dim) for f, p in ((c.k_fmt, c.k), (c.v_fmt, c.v)))
+    qd = c.qt.double().numpy()[:, 1:1 + c.heads]
+    for b, (n, kv) in enumerate(c.seqs):
+        s, rows = slice(c.start[b], c.start[b + 1]), rows_of(c, b)
+        o, mag = ref.attention(qd[s], kd, vd, rows, c.kv_heads, n, kv, c.scale, c.causal, c.window)
+        d, dv = (largest_scale(f, p[rows]) for f, p in ((c.k_fmt, c.k), (c.v_fmt, c.v)))
+        c.want[s] = o
+        c.bound[s] = ref.element_bound(qd[s], d, 15 if c.k_fmt == "q4_0" else 255, max(kv, 1), abs(c.scale), mag, o, c.dtype,
+                                       dv * (8 if c.v_fmt == "q4_0" else 128))
+
+
+def keep_first(c, out, n):
+    """c and its output without the tokens from n on (of one sequence)."""
+    c.start[-1] = c.T = n
+    c.want, c.bound = c.want[:n], c.bound[:n]
+    return out[:n]
+
+
+MAX_HALF, INF, NAN = 0x7BFF, 0x7C00, 0x7E00
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("v_fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_attn_small_values_beside_large_unseen_ones(lib, head_dim, v_fmt, dtype):  # noqa: F811
+    """V scales of cells that a row does not see, the largest there are among them, cost it no precision: cells just before a
+    window, and later tokens' cells of the same tile."""
+    v_scale = 1e-3 if dtype == "f16" else 1e-5  # fp16 results stay above its subnormals
+    for bits in (MAX_HALF, INF, NAN):
+        for seqs, window, away, sure in (([(1, 200)], 50, range(128, 150), 1), ([(4, 60)], 0, (58, 59), 2),
+                                         ([(100, 130)], 0, (128, 129), 98), ([(90, 600)], 70, range(384, 441), 90)):
+            say(f"attn small values {head_dim} {v_fmt} {dtype} {seqs} scale bits {bits:x}")
+            c = Case(seqs, 4, 2, head_dim, "q8_0", v_fmt, dtype, window=window, seed=head_dim, v_scale=v_scale)
+            set_scales(c.v, v_fmt, rows_of(c, 0)[list(away)], bits)
+            c.check(keep_first(c, c.run(lib), sure))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 4, 70])
+def test_attn_small_values_beside_a_large_improbable_one(lib, n, dtype):  # noqa: F811
+    """A cell with the largest V scale whose probability is next to nothing costs the others no precision."""
+    v_scale = 1e-3 if dtype == "f16" else 1e-5
+    for head_dim in (64, 128, 256):
+        for v_fmt in ("q4_0", "q8_0"):
+            for at in (0, 40, 90):  # first, in the middle, last (for prompts: before the first token's own)
+                say(f"attn improbable {head_dim} {v_fmt} {dtype} n={n} at {at}")
+                c = Case([(n, 100 + n)], 2, 2, head_dim, "q8_0", v_fmt, dtype, seed=n, v_scale=v_scale)
+                # all queries lean to one direction, the cell's key is far against it: score about -90
+                rng = np.random.default_rng(1)
+                lean = rng.choice([-1.0, 1.0], head_dim).astype(np.float32)
+                c.qt = (c.qt.float() * 0.25 + torch_of(lean)).to(torch_type(dtype))
+                row = rows_of(c, 0)[at]
+                key = np.tile(-90.0 / head_dim ** 0.5 * lean, 2).astype(np.float32)
+                c.k[row] = oracle.quantize("q8_0", key[None])[0]
+                before = c.v[row].copy()
+                set_scales(c.v, v_fmt, [row], MAX_HALF)
+                again(c)
+                # the bound without that cell, whose part of the result is below 1e-20
+                c.v[row], large = before, c.v[row].copy()
+                want = c.want.copy()
+                again(c)
+                c.want, c.v[row] = want, large
+                c.check(c.run(lib))
+
+
+def torch_of(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a))
