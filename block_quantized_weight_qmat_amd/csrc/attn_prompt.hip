@@ -22,8 +22,10 @@
 // unpacked: code x scale rounded to fp16's 11 bits, once more what the
 // probabilities are rounded to anyway and an eighth of bf16's own rounding. The
 // scales of a cell are first divided by a power of two, which brings the largest
-// to [1, 2) and is given back to the probabilities: one operation for each
-// instead of one per block. 2048 tokens behind 16000, 32 / 8 heads of 128: 1215
+// to [2^11, 2^12) (Q4_0) or [2^7, 2^8) (Q8_0), so that its largest product with a
+// code just fits fp16, and is given back to the probabilities: one operation for
+// each instead of one per block. Blocks keep their 11 bits down to scales 2^-21 of
+// the cell's largest; below, a scale is off by at most 2^-32 of it. 2048 tokens behind 16000, 32 / 8 heads of 128: 1215
 // us without, 1112 us with it in fp16, where the second rounding would add a
 // quarter to the result's error. (Not for K: an error of a score is multiplied by
 // the score's size. It would save a fifth.)
@@ -150,8 +152,8 @@ __device__ __forceinline__ void read_block(const uint8_t* raw, int cell, int blk
   for (int i = 0; i < P::kWords; ++i) w[i] = shifted(t, i, shift);
 }
 
-// The power of two that scales of a cell are divided by: the exponent field
-// of the largest finite one, as 2^(field - 15).
+// The exponent field of the largest finite scale of a cell: that is below
+// 2^(field - 14).
 template <int D, bool kQ4>
 __device__ __forceinline__ int scale_field(const uint8_t* raw, int cell) {
   typedef Piece<D, kQ4> P;
@@ -165,8 +167,12 @@ __device__ __forceinline__ int scale_field(const uint8_t* raw, int cell) {
   return (int)(most >> 10);
 }
 
-__device__ __forceinline__ float power_of(int field) {  // 2^(field - 15)
-  return __builtin_bit_cast(float, (uint32_t)(field - 15 + 127) << 23);
+// The power of two that the scales of a cell are divided by: 2^(field - 15 - kUp),
+// codes of up to 2^(15 - kUp) / 2 reaching 2^15 then.
+template <bool kQ4>
+__device__ __forceinline__ float power_of(int field) {
+  constexpr int kUp = kQ4 ? 11 : 7;
+  return __builtin_bit_cast(float, (uint32_t)(field - 15 - kUp + 127) << 23);
 }
 
 // A scale divided by its cell's power of two, twice as fp16 (times 1/16: for
@@ -195,6 +201,8 @@ void attn_prompt_kernel(const Params p) {
   constexpr bool kPair = sizeof(T) == 4;
   constexpr bool kFold = std::is_same_v<T, __bf16>;  // V's scales go into the codes
   constexpr int kNb = D / 32;
+  // Probabilities times V scales, or times what these were divided by, are below 2^14.
+  constexpr float kAbove = 28.0f + (kFold ? (kVQ4 ? 11.0f : 7.0f) : 0.0f);
   constexpr int kItemCols = kWv * kTiles * kCols;
   constexpr int kBatch = batch_for<D>(), kQuarters = kBatch / 16;
   typedef Piece<D, kKQ4> KP;
@@ -342,10 +350,10 @@ void attn_prompt_kernel(const Params p) {
           if (blk == 0)
             op.ve[cell] = __builtin_bit_cast(uint16_t, (_Float16)(uint16_t)field);
           if constexpr (kFold) {
-            const float inverse = finite ? 1.0f / power_of(field) : 0.0f;
+            const float inverse = finite ? 1.0f / power_of<kVQ4>(field) : 0.0f;
             low = finite ? scale_pair(d, inverse) : 0u;
             high = finite ? scale_pair(d, inverse * 0.0625f) : 0u;
-            if (blk == 0) op.v_unit[cell] = power_of(field);
+            if (blk == 0) op.v_unit[cell] = power_of<kVQ4>(field);
           } else {
             op.vd[cell * kNb + blk] = (uint16_t)(finite ? d : 0u);
           }
@@ -491,7 +499,7 @@ void attn_prompt_kernel(const Params p) {
 #pragma unroll
         for (int e = 0; e < 4 * kQuarters; ++e)
           mx = fmaxf(mx, fmaf(sc[n][e], cs[n], half_of(ve[e >> 2][(e >> 1) & 1], e & 1)));
-        const float now = fmaxf(m[n], groups_max(mx) - 28.0f);
+        const float now = fmaxf(m[n], groups_max(mx) - kAbove);
         const float ref = now == -INFINITY ? 0.0f : now;
         if (__ballot(now != m[n]) != 0) {
           const float alpha = exp2_raw(m[n] - ref);

@@ -1,5 +1,5 @@
 """Attention over the quantized cache where its arithmetic is strained: V scales
-far apart. Held to the 64-bit formula within kv_reference's bounds.
+far apart, between cells and between the blocks of one. Held to the 64-bit formula within kv_reference's bounds.
 """
 import numpy as np
 import pytest
@@ -98,3 +98,31 @@ def test_attn_small_values_beside_a_large_improbable_one(lib, n, dtype):  # noqa
 def torch_of(a):
     import torch
     return torch.from_numpy(np.ascontiguousarray(a))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("v_fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_attn_blocks_of_different_size(lib, head_dim, v_fmt, dtype):  # noqa: F811
+    """Channels whose values are far smaller than others' keep their relative precision."""
+    for n in (1, 70, 300):
+        for ratio in (14, 18, 20):
+            say(f"attn blocks {head_dim} {v_fmt} {dtype} n={n} ratio 2^-{ratio}")
+            c = Case([(n, n + 60)], 4, 2, head_dim, "q8_0", v_fmt, dtype, seed=ratio + n, v_scale=300.0 if dtype == "f16" else 3e3)
+            b = blocks_of(c.v, v_fmt)[:, 1::2, :2]
+            d = np.ascontiguousarray(b).view(np.float16)
+            d = np.where(np.isfinite(d), d.astype(np.float32) * 2.0 ** -ratio, d).astype(np.float16)
+            b[:] = d.view(np.uint8).reshape(b.shape)
+            again(c)
+            out = c.run(lib)
+            c.check(out)
+            if dtype == "f16":
+                continue  # the small channels' results are among fp16's subnormals: held by the bound alone
+            small = (np.arange(head_dim) // 32) % 2 == 1
+            got, want = out[:n, :c.heads].double().cpu().numpy()[..., small], c.want[:n][..., small]
+            # half of fp16's smallest step in each product, as in element_bound: relative to the large blocks' scales
+            least = (n + 60) * 2.0 ** -38 * largest_scale(v_fmt, c.v[rows_of(c, 0)]) * (8 if v_fmt == "q4_0" else 128)
+            norm = np.linalg.norm(want)
+            l2 = np.linalg.norm(got - want) / norm
+            say(f"  small channels rel_l2 {l2:.2e}")
+            assert l2 <= ref.l2_bound(dtype) + least * want.size ** 0.5 / norm
