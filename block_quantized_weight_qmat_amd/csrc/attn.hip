@@ -285,7 +285,7 @@ void attn_split_kernel(const Params p) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int cell = i * kStep + lane / kNb;
-        mine.kd[cell * kNb + blk] = (uint16_t)k_d[i];
+        mine.kd[cell * kNb + blk] = k_scale(k_d[i]);
         mine.vd[cell * kNb + blk] = (uint16_t)v_d[i];
         uint32_t w[VP::kWords];
 #pragma unroll

@@ -220,6 +220,14 @@ __device__ __forceinline__ uint32_t row_max_u(uint32_t v) {
   return o > v ? o : v;
 }
 
+// A K block's scale as it is multiplied with sums of codes: d + 0 d, which is d, or a
+// NaN for an infinity, whose product with a negative sum would be a score of -inf, that
+// of an unseen cell.
+__device__ __forceinline__ uint16_t k_scale(uint32_t d) {
+  const _Float16 h = __builtin_bit_cast(_Float16, (uint16_t)d);
+  return __builtin_bit_cast(uint16_t, __builtin_fmaf16(h, (_Float16)0.0f, h));
+}
+
 // The exponent e of a cell's V scales as fp16, from a scale of each of the kNb lanes
 // that have its blocks: the largest |scale| is below 2^(e - 14).
 template <int kNb>

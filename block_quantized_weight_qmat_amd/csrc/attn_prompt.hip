@@ -318,7 +318,7 @@ void attn_prompt_kernel(const Params p) {
           if (blk >= kNb) break;
           uint32_t d, w[KP::kWords];
           read_block<D, kKQ4>(lds.k_raw[n], cell, blk, &d, w);
-          op.kd[cell * kNb + blk] = (uint16_t)d;
+          op.kd[cell * kNb + blk] = k_scale(d);
           uint8_t* to = op.k + (((cell >> 4) * kNb + blk) * kWave + (cell & 15)) * 16;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

@@ -1,5 +1,6 @@
 """Attention over the quantized cache where its arithmetic is strained: V scales
-far apart, between cells and between the blocks of one. Held to the 64-bit formula within kv_reference's bounds.
+far apart, between cells and between the blocks of one, and infinite key scales.
+Held to the 64-bit formula within kv_reference's bounds.
 """
 import numpy as np
 import pytest
@@ -126,3 +127,21 @@ def test_attn_blocks_of_different_size(lib, head_dim, v_fmt, dtype):  # noqa: F8
             l2 = np.linalg.norm(got - want) / norm
             say(f"  small channels rel_l2 {l2:.2e}")
             assert l2 <= ref.l2_bound(dtype) + least * want.size ** 0.5 / norm
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("k_fmt", ["q4_0", "q8_0"])
+def test_attn_infinite_key_scale(lib, k_fmt, dtype):  # noqa: F811
+    """A row that sees a cell with an infinite key scale has no finite result, whatever the signs of its codes; others do."""
+    import torch
+    for n, cells, at in ((1, 60, 20), (3, 1500, 700), (70, 130, 50), (80, 1300, 100)):
+        for code in (0x00, 0x99, 0xFF):
+            for bits in (INF, INF | 0x8000):
+                say(f"attn infinite key scale {k_fmt} {dtype} n={n} cells={cells} codes {code:x}")
+                c = Case([(n, cells), (1, 40)], 4, 2, 128, k_fmt, "q4_0", dtype, seed=3)
+                c.qt = torch.ones_like(c.qt)
+                blocks_of(c.k, k_fmt)[rows_of(c, 0)[at], :, 2:] = code
+                set_scales(c.k, k_fmt, rows_of(c, 0)[[at]], bits)
+                out = c.run(lib)
+                assert not torch.any(torch.isfinite(out[:n, :c.heads])).item()
+                assert torch.all(torch.isfinite(out[n:])).item()
