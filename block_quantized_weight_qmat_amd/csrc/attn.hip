@@ -629,88 +629,6 @@ void attn_join_kernel(const Params p) {
 }
 
 constexpr int64_t kMaxGrid = 1 << 22;
-constexpr int64_t kPromptRows = 64;    // query rows of a cache head: attn_prompt.hip
-constexpr int64_t kFill = 512;         // workgroups that fill the GPU
-constexpr int64_t kHeadTiles = 16;     // tiles of a wave from which on it takes a head
-constexpr int64_t kSharedCells = 256;  // cells from which on items are shared
-
-// How the work is divided, from host values alone.
-struct Plan {
-  int64_t col_tiles, items, shares, part_rows;
-  int heads_shift;  // log2 of the cache heads of a workgroup
-  int prompt_rows;  // of an item of attn_prompt.hip, 0: not there
-  bool search;
-};
-
-Plan plan(const qmat_attn_args& a) {
-  Plan r;
-  const int64_t group = a.heads / a.kv_heads;
-  const int64_t max_q = a.max_q < a.n_tokens ? a.max_q : a.n_tokens;
-  r.prompt_rows = 0;
-  r.col_tiles = (max_q * group + kCols - 1) / kCols;
-  r.part_rows = max_q * group < kCols ? max_q * group : kCols;
-  // Column tiles by sequence where every sequence may have max_q tokens, or by
-  // their place among all tokens where those bound them better.
-  const int64_t by_token = a.n_tokens * group / kCols + a.n_seqs;
-  const int64_t by_seq = a.n_seqs * r.col_tiles;
-  const int64_t limit = a.pages_per_seq * a.page_size;
-  int64_t cells = a.max_kv < limit ? a.max_kv : limit;
-  if (a.window > 0 && a.window + max_q < cells) cells = a.window + max_q;
-  r.shares = 0;
-  r.heads_shift = 0;
-  if (max_q * group >= kPromptRows) {
-    const PromptShape shape = prompt_shape(a, max_q * group);
-    const int64_t rows = shape.rows;
-    r.prompt_rows = shape.rows;
-    r.part_rows = max_q * group < rows ? max_q * group : rows;
-    r.col_tiles = (max_q * group + rows - 1) / rows;
-    const int64_t tokens = a.n_tokens * group / rows + a.n_seqs;
-    const int64_t direct = a.n_seqs * r.col_tiles, units = direct * a.kv_heads;
-    // Items shared out evenly: that saves batches where few items leave most of
-    // the GPU idle, and costs a partial result of every row and their joining,
-    // as long as two batches and, where the GPU is full, 16 more. 100 tokens
-    // behind 16000, 32 / 8 heads of 128, bf16: 983 us unshared, 96 us shared;
-    // 1024 tokens of their own: 82 and 86 us; 2 x 2048: 188 and 307 us.
-    const int64_t batches = (cells + shape.batch - 1) / shape.batch;
-    const int64_t saved = batches - (batches * units + shape.fill - 1) / shape.fill;
-    if (direct <= kMaxItems && saved >= 2 + 16 * units / shape.fill &&
-        direct * (limit / shape.batch + 1) <= 0x7FFFFFFF) {
-      const int64_t tiles = direct * batches;
-      r.search = false;
-      r.items = direct;
-      r.shares = shape.fill / a.kv_heads > 1 ? shape.fill / a.kv_heads : 1;
-      if (r.shares > (tiles + 1) / 2) r.shares = (tiles + 1) / 2;
-    } else {
-      r.search = direct > tokens;
-      r.items = r.search ? tokens : direct;
-    }
-    return r;
-  }
-  r.search = by_seq > by_token;
-  r.items = r.search ? by_token : by_seq;
-  int even = 0;
-  while (even < 2 && (a.kv_heads >> even) % 2 == 0) ++even;
-  if (by_seq <= kMaxItems && cells > kSharedCells &&
-      by_seq * (limit / kCells + 1) <= 0x7FFFFFFF) {
-    r.search = false;
-    r.items = by_seq;
-    const int64_t tiles = r.items * ((cells + kCells - 1) / kCells);  // at most, if max_kv holds
-    // a wave takes a head where that leaves it enough tiles
-    if (tiles * a.kv_heads >= kFill * kWaves * kHeadTiles) r.heads_shift = even;
-    const int64_t groups = a.kv_heads >> r.heads_shift;
-    r.shares = kFill / groups > 1 ? kFill / groups : 1;
-    const int64_t most = (tiles + 1) / 2 / (kWaves >> r.heads_shift) + 1;
-    if (r.shares > most) r.shares = most;
-  } else if (r.items * a.kv_heads >= kFill * kWaves) {
-    r.heads_shift = even;
-  }
-  return r;
-}
-
-// Rows of partial results: share + item is below shares + items.
-int64_t part_count(const qmat_attn_args& a, const Plan& r) {
-  return (r.shares + r.items) * a.kv_heads * r.part_rows;
-}
 
 int log2_of(int64_t v) {
   int n = 0;

@@ -5,17 +5,14 @@
 
 #include <math.h>
 
+#include "attn_plan.hpp"
 #include "kv_device.hpp"
 #include "qmat_launch.hpp"
 
 namespace qmat {
 namespace attn {
 
-constexpr int kCols = 16;   // query rows of a tile
-constexpr int kCells = 32;  // cells of a tile
-constexpr int kWaves = 4;   // of a workgroup
 constexpr int kThreads = kWaves * kWave;
-constexpr int kMaxItems = 1024;  // items whose tiles are dealt out together
 
 struct Params {
   const void* q;
@@ -458,13 +455,7 @@ struct Query {
   }
 };
 
-// attn_prompt.hip: the query rows of its items where a sequence has up to
-// seq_rows of them (of one cache head), the cells of a batch, the workgroups
-// that fill the GPU; and the launch, with p.items and so on for such items.
-struct PromptShape {
-  int rows, batch, fill;
-};
-PromptShape prompt_shape(const qmat_attn_args& a, int64_t seq_rows);
+// attn_prompt.hip: the launch, with p.items and so on for items of `rows` query rows.
 void launch_prompt(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream);
 
 }  // namespace attn

@@ -40,7 +40,7 @@
 // but 3 to 11 % slower for fp16.
 //
 // Shares (attn_device.hpp) of such items only where a few long ones would leave
-// most of the GPU idle; attn.hip's plan has the rule.
+// most of the GPU idle; attn_plan.hpp has the rule.
 #include <type_traits>
 
 #include "attn_device.hpp"
@@ -50,17 +50,11 @@ namespace {
 
 using namespace attn;
 
-// Cells that are staged at a time: two batches of operands fit LDS.
-template <int D>
-constexpr int batch_for() {
-  return D == 256 ? 32 : 64;
-}
-
 // Staging: the first half of the threads move K's units and blocks, the others V's.
 template <int D, bool kQ4, int kWv>
 struct Side {
   typedef Piece<D, kQ4> P;
-  static constexpr int kBatch = batch_for<D>();
+  static constexpr int kBatch = prompt_batch(D);
   static constexpr int kSides = kWv * kWave / 2;  // threads of a side
   static constexpr int kTotal = kBatch * P::kUnits;
   static constexpr int kLoads = (kTotal + kSides - 1) / kSides;
@@ -109,7 +103,7 @@ constexpr int v_row_bytes() {
 
 template <int D, bool kKQ4, bool kVQ4, int kWv>
 struct Operands {
-  static constexpr int kBatch = batch_for<D>();
+  static constexpr int kBatch = prompt_batch(D);
   // K operands: [16 cells][block][lane], 16 bytes each
   uint8_t k[kBatch * D * 2];
   uint8_t v[kBatch * v_row_bytes<D>()];
@@ -204,7 +198,7 @@ void attn_prompt_kernel(const Params p) {
   // Probabilities times V scales, or times what these were divided by, are below 2^14.
   constexpr float kAbove = 28.0f + (kFold ? (kVQ4 ? 11.0f : 7.0f) : 0.0f);
   constexpr int kItemCols = kWv * kTiles * kCols;
-  constexpr int kBatch = batch_for<D>(), kQuarters = kBatch / 16;
+  constexpr int kBatch = prompt_batch(D), kQuarters = kBatch / 16;
   typedef Piece<D, kKQ4> KP;
   typedef Piece<D, kVQ4> VP;
   typedef Side<D, kKQ4, kWv> KS;
@@ -661,15 +655,6 @@ void launch_as(const qmat_attn_args& a, const Params& p, int rows, hipStream_t s
 }  // namespace
 
 namespace attn {
-
-PromptShape prompt_shape(const qmat_attn_args& a, int64_t seq_rows) {
-  PromptShape s;
-  s.batch = a.head_dim == 256 ? batch_for<256>() : batch_for<64>();
-  s.fill = 256;
-  const int most = a.head_dim > 128 ? 64 : a.dtype == kDtypeF32 ? 128 : 256;
-  s.rows = seq_rows > 64 ? most : 64;
-  return s;
-}
 
 void launch_prompt(const qmat_attn_args& a, const Params& p, int rows, hipStream_t stream) {
   if (a.dtype == kDtypeF32)
