@@ -440,11 +440,18 @@ int qmat_kv_load(int k_fmt, int v_fmt, int dtype, const void *k_cache,
  *   products probability x V scale are rounded once to 11 bits (bf16 prompts:
  *   the probability and the product V code x V scale, once each); for fp32 both
  *   are carried as pairs of fp16 (22 bits). Relative L2 error against exact
- *   arithmetic, before rounding to dtype: below 1e-5 (fp32), 5e-4 (others).
+ *   arithmetic, before rounding to dtype: below 1e-5 (fp32), 5e-4 (others) for
+ *   scores of up to 100 in size, growing in proportion to them above (an fp32
+ *   score is rounded by up to 2^-24 of its size, and a probability changes by as
+ *   much). Products below fp16's normal range lose bits: a probability x V scale
+ *   from 2^-27 of the row's largest such product on, and in bf16 prompts a V scale
+ *   from 2^-21 of the largest in its cell and head on.
  *   Cells that a token does not see have no effect on it, whatever their
  *   bytes hold (infinite or NaN scales included); one that sees a cell with
- *   an infinite or NaN scale has no finite result in some or all elements.
- *   Scores (scale * q . k) must be within fp32's range.
+ *   an infinite or NaN scale has no finite result in some or all elements, and
+ *   neither has a query row with an infinity or NaN.
+ *   Scores (scale * q . k) must stay below 2^22 in size, and scale * |q| below
+ *   2^100: beyond, a row may come out as infinities or NaN.
  *
  *   Limits (QMAT_E_SHAPE): head_dim 64, 128 or 256; heads a multiple of
  *   kv_heads and at most 4096, heads / kv_heads at most 256, max_q * heads /
@@ -453,8 +460,8 @@ int qmat_kv_load(int k_fmt, int v_fmt, int dtype, const void *k_cache,
  *   pages_per_seq * page_size <= 2^30; cells <= 2^31 - 1; n_tokens, n_seqs
  *   <= 2^24; max_q <= 2^24; strides >= heads * head_dim; scale finite.
  *   Device values outside their range do no harm: len_b is cut to
- *   [0, pages_per_seq * page_size], n_b to [0, max_q], tokens outside
- *   [0, n_tokens) are skipped, and the cells of a page number outside
+ *   [0, pages_per_seq * page_size], n_b to [0, min(max_q, n_tokens)] (before
+ *   positions are counted), tokens outside [0, n_tokens) are skipped, and the cells of a page number outside
  *   [0, cells / page_size) count as not seen. Page numbers at and behind
  *   ceil(len_b / page_size) are not read.
  *   Rows of out that belong to no sequence are left as they were.

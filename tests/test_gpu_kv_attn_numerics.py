@@ -1,6 +1,7 @@
 """Attention over the quantized cache where its arithmetic is strained: V scales
-far apart, between cells and between the blocks of one, and infinite key scales.
-Held to the 64-bit formula within kv_reference's bounds.
+far apart, between cells and between the blocks of one, infinite key scales, large
+scores, queries that are not finite. Held to the 64-bit formula within
+kv_reference's bounds.
 """
 import numpy as np
 import pytest
@@ -145,3 +146,72 @@ def test_attn_infinite_key_scale(lib, k_fmt, dtype):  # noqa: F811
                 out = c.run(lib)
                 assert not torch.any(torch.isfinite(out[:n, :c.heads])).item()
                 assert torch.all(torch.isfinite(out[n:])).item()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("k_fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("n", [1, 4, 70])
+def test_attn_large_scores(lib, n, k_fmt, dtype):  # noqa: F811
+    """Queries and keys with means of their own: scores of hundreds and thousands that differ little from each other, where the
+    fp32 rounding of a score, 2^-24 of its size, changes every probability by as much. The header's limits hold to scores of 100
+    and grow with them from there: 2^-24 of 100 is 6e-6 of its 1e-5."""
+    for head_dim in (64, 128, 256):
+        for k_mean, q_mean in ((0, 0), (2, 2), (10, 3), (20, 10), (5, 40)):
+            c = Case([(n, 300 + n)], 4, 2, head_dim, k_fmt, "q8_0", dtype, seed=n + head_dim)
+            rng, rows = np.random.default_rng(n), rows_of(c, 0)
+            c.k[rows] = oracle.quantize(k_fmt, (k_mean + rng.standard_normal((len(rows), 2 * head_dim))).astype(np.float32))
+            c.qt = (q_mean + 0.3 * torch_of(rng.standard_normal(c.qt.shape))).to(torch_type(dtype))
+            again(c)
+            kd = oracle.dequant(k_fmt, c.k[rows], len(rows), 2 * head_dim)
+            qd = c.qt.double().numpy()[:, 1:1 + c.heads]
+            top = max(np.abs(kd[:, (h // 2) * head_dim:(h // 2 + 1) * head_dim] @ qd[:, h].T).max() for h in range(4)) * c.scale
+            out = c.run(lib)[:n, :c.heads].double().cpu().numpy()
+            l2 = np.linalg.norm(out - c.want) / np.linalg.norm(c.want)
+            limit = ref.L2[dtype] * max(1.0, top / 100) + ref.EPS[dtype] / 2
+            say(f"attn large scores {head_dim} {k_fmt} {dtype} n={n} up to {top:.0f}: rel_l2 {l2:.2e} of {limit:.2e}")
+            assert np.all(np.abs(out - c.want) <= c.bound) and l2 <= limit
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 70])
+def test_attn_largest_scores(lib, n, dtype):  # noqa: F811
+    """Scores near the limit of 2^22 and the largest V scales: finite means of the values that are seen."""
+    import torch
+    for head_dim in (64, 128, 256):
+        say(f"attn largest scores {head_dim} {dtype} n={n}")
+        c = Case([(n, 300 + n)], 4, 2, head_dim, "q8_0", "q4_0", dtype, seed=2, q_scale=1e4 / head_dim ** 0.5, scale=80.0,
+                 v_scale=1e4 if dtype == "f16" else 5e4)
+        out = c.run(lib)[:n, :c.heads].double()
+        vd = oracle.dequant("q4_0", c.v[rows_of(c, 0)], 300 + n, 2 * head_dim)
+        assert np.all(np.isfinite(vd))
+        assert torch.all(torch.isfinite(out)).item()
+        assert float(out.abs().max()) <= np.abs(vd).max() * (1 + ref.EPS[dtype]) * (1 + 2.0 ** -10)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 4, 70])
+def test_attn_queries_that_are_not_finite(lib, n, dtype):  # noqa: F811
+    """A query row with a NaN or an infinity has no finite result; every other row has the one it has without it."""
+    import torch
+    for head_dim in (64, 128, 256):
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            say(f"attn query {bad} {head_dim} {dtype} n={n}")
+            c = Case([(n, 90 + n), (1, 700)], 4, 2, head_dim, "q4_0", "q8_0", dtype, seed=6)
+            whole = c.run(lib)
+            c.qt[n - 1, 1 + 2, 5] = bad
+            out = c.run(lib)
+            hit = torch.zeros_like(whole, dtype=torch.bool)
+            hit[n - 1, 2] = True
+            assert not torch.any(torch.isfinite(out[hit])).item() and torch.equal(out[~hit], whole[~hit])
+
+
+def test_attn_more_tokens_than_there_are(lib):  # noqa: F811
+    """Starts past the tokens: a sequence has no more tokens than q has rows, counted from its first."""
+    c = Case([(6, 40), (0, 33)], 4, 2, 64, seed=8)
+    c.start[:] = [0, 9, 7]
+    for max_q in (6, 9, 100):
+        say(f"attn starts past the tokens, max_q {max_q}")
+        out = c.run(lib, max_q=max_q)
+        c.start[-1] = 6
+        c.check(out)
+        c.start[:] = [0, 9, 7]
