@@ -182,7 +182,7 @@ __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
 
 // 4 cells of one column: of the four rows that the lane group's lanes name, 16
 // slots each, the lane's slot.
-__device__ __forceinline__ u32x2 read_slots(const uint8_t* rows, int lane) {
+__device__ __forceinline__ u32x2 read_slots(const uint8_t* rows) {
   typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
   const i16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
       (__attribute__((address_space(3))) i16x4*)(rows));
@@ -534,8 +534,8 @@ void attn_prompt_kernel(const Params p) {
           half8_t a[2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const u32x2 first = read_slots(from + 64 * i + 32 * y, lane);
-            const u32x2 second = read_slots(from + 64 * i + 32 * y + 16 * v_row_bytes<D>(), lane);
+            const u32x2 first = read_slots(from + 64 * i + 32 * y);
+            const u32x2 second = read_slots(from + 64 * i + 32 * y + 16 * v_row_bytes<D>());
             a[y] = as_half8(first.x, first.y, second.x, second.y);
           }
 #pragma unroll

@@ -10,12 +10,8 @@ namespace qmat {
 // takes such addresses in single wide accesses.
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
 typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
-typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 
 template <bool kQ4>
 constexpr int kv_block_bytes() {
@@ -36,19 +32,14 @@ __device__ __forceinline__ void load_f32(const T* __restrict__ p, float* v) {
   }
 }
 
-// ... and back, rounded once to nearest even.
+// ... and N of them back, rounded once to nearest even.
 template <typename T, int N>
 __device__ __forceinline__ void store_f32(T* __restrict__ p, const float* v) {
   typedef T vec __attribute__((ext_vector_type(N)));
-  if constexpr (sizeof(T) == 4 && N == 8) {
-    store_f32<T, 4>(p, v);
-    store_f32<T, 4>(p + 4, v + 4);
-  } else {
-    vec t;
+  vec t;
 #pragma unroll
-    for (int i = 0; i < N; ++i) t[i] = (T)v[i];
-    *reinterpret_cast<vec*>(p) = t;
-  }
+  for (int i = 0; i < N; ++i) t[i] = (T)v[i];
+  *reinterpret_cast<vec*>(p) = t;
 }
 
 }  // namespace qmat
