@@ -215,3 +215,20 @@ def test_attn_more_tokens_than_there_are(lib):  # noqa: F811
         c.start[-1] = 6
         c.check(out)
         c.start[:] = [0, 9, 7]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("k_fmt,v_fmt", [("q4_0", "q4_0"), ("q8_0", "q4_0"), ("q4_0", "q8_0"), ("q8_0", "q8_0")])
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_attn_error_before_the_outputs_rounding(lib, head_dim, k_fmt, v_fmt, dtype):  # noqa: F811
+    """The header's limits without the slack of a whole half step: what the output's rounding does to these very answers is
+    measured on the exact ones (a tenth is left for the two being rounded apart)."""
+    import torch
+    for n in (1, 5, 140):
+        c = Case([(n, 400 + n), (n, 97 + n)], 8, 2, head_dim, k_fmt, v_fmt, dtype, page=32, seed=n)
+        out = c.run(lib)[:2 * n, :c.heads].double().cpu().numpy()
+        rounded = torch.from_numpy(c.want).to(torch_type(dtype)).double().numpy()
+        norm = np.linalg.norm(c.want)
+        own, l2 = np.linalg.norm(rounded - c.want) / norm, np.linalg.norm(out - c.want) / norm
+        say(f"attn error {head_dim} {k_fmt} {v_fmt} {dtype} n={n}: rel_l2 {l2:.2e}, {own:.2e} of it the rounding")
+        assert l2 <= 1.1 * own + ref.L2[dtype]
