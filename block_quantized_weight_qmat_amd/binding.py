@@ -520,11 +520,13 @@ def attn(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     the tokens q_start[b] .. q_start[b + 1] - 1 and kv_len[b] cells, found by
     page_table [seqs, pages] (all int32). scale: 1 / sqrt(head_dim) if None.
     max_q: an upper bound of a sequence's tokens (all tokens if None; it
-    chooses the kernel: give 1 for decode);
+    chooses the kernel for the whole call: give 1 for decode, several times as
+    fast as None in a large batch, and keep prompts in a call of their own);
     max_kv: of kv_len, as an estimate (what the table holds if None). A
     workspace of attn_workspace_bytes() is allocated when none is given; out
-    and the workspace must not overlap anything else that is used. Rows of out that belong to no sequence are left as they were (zeros in an out
-    allocated here)."""
+    and the workspace must not overlap anything else that is used. Rows of out
+    that belong to no sequence are left as they were (zeros in an out allocated
+    here)."""
     if out is None:
         out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
     a = attn_args(k_fmt, v_fmt, q, k_cache, v_cache, page_table, q_start, kv_len, kv_heads,

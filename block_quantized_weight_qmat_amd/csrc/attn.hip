@@ -31,20 +31,22 @@
 // of the second product. V^T needs 8 cells of one dimension per lane: code
 // bytes are transposed by the LDS read itself (ds_read_b64_tr_b8).
 //
-// This file: few query rows (decode, drafted tokens); attn_prompt.hip: many.
-// Bytes bound the first only in principle: every code is unpacked for at most 16
-// columns, about 390 VALU operations a tile of 32 cells (4-bit K and V, heads of
-// 128, bf16), half of the kernel's cycles. Its loads alone take as long as its
-// arithmetic alone (207 and 202 us for the batch of 64 below), and the two overlap
-// to the times here. Tiles go from memory to LDS as whole lines of aligned units,
-// through registers, the next tile's while this one is multiplied: blocks of 18
-// and 34 bytes, loaded where the products want them, cost one cache access a lane
-// (4 times the time), and loads under a branch wait before the products.
-// Measured, with the join, bytes at 4.9 TB/s (a large copy) in brackets:
-//   65521 cells, 32 / 8 heads of 128, Q4_0, bf16          35 us (15)
-//   48 sequences, 32 / 8 x 128, Q8_0, fp32, pages of 16   92 us (44)
-//   64 sequences, 64 / 8 x 128, Q4_0, bf16               185 us (131)
-//   5 tokens each, 32 / 32 x 128, Q8_0 / Q4_0, fp16       60 us (33)
+// This file: few query rows (decode, drafted tokens); attn_prompt.hip: many. Bytes
+// bound the first only in principle: every code is unpacked for at most 16 columns,
+// about 370 VALU operations a tile of 32 cells (counted; 4-bit K and V, heads of 128,
+// bf16), which is half of the kernel's cycles in the batch of 64 below; waves wait for a
+// fifth of theirs, and matrix cores are busy for a tenth. Tiles go from memory to LDS as
+// whole lines of aligned units, through registers, the next tile's while this one is
+// multiplied: blocks of 18 and 34 bytes, loaded where the products want them, cost one
+// cache access a lane (4 times the time), and loads under a branch wait before the
+// products. Pages below 32 cells with 8-bit codes and heads of 128 spill 63 to 79
+// registers a lane (two waves a SIMD leave 256), heads of 256 in fp32 15 to 34.
+// Measured, calls of the Python binding one after the other, with the join; bytes at
+// 4.9 TB/s (a large copy) in brackets:
+//   65521 cells, 32 / 8 heads of 128, Q4_0, bf16          32 us (15)
+//   48 sequences, 16 / 8 x 128, Q8_0, fp32, pages of 16   92 us (44)
+//   64 sequences, 64 / 8 x 128, Q4_0, bf16               169 us (131)
+//   5 tokens each, 32 / 32 x 128, Q8_0 / Q4_0, fp16       57 us (33)
 #include <type_traits>
 
 #include "attn_device.hpp"

@@ -74,8 +74,8 @@ inline Plan plan(const qmat_attn_args& a) {
     // Items shared out evenly: that saves batches where few items leave most of
     // the GPU idle, and costs a partial result of every row and their joining,
     // as long as two batches and, where the GPU is full, 16 more. 100 tokens
-    // behind 16000, 32 / 8 heads of 128, bf16: 983 us unshared, 96 us shared;
-    // 1024 tokens of their own: 82 and 86 us; 2 x 2048: 188 and 307 us.
+    // behind 16000, 32 / 8 heads of 128, bf16: 1015 us unshared, 98 us shared;
+    // 1024 tokens of their own: 85 and 88 us; 2 x 2048: 190 and 316 us.
     bool share = direct <= kMaxItems && direct * (limit / shape.batch + 1) <= 0x7FFFFFFF;
     if (share) {  // now what follows is far from int64's end
       const int64_t units = direct * a.kv_heads;

@@ -1,6 +1,6 @@
 // attn_prompt.hip — qmat_attn where sequences bring many query rows (prompts):
-// bound by the matrix cores and by what is done to the scores between the two
-// products. Mathematics, exactness and the operand layouts are attn.hip's.
+// the time goes into the products and into what is done to codes and scores for
+// them, not into bytes. Mathematics, exactness and the operand layouts are attn.hip's.
 //
 // One workgroup has an item, that is kWv * kTiles * 16 query rows of one cache
 // head (tokens and the head's group of query heads): kWv waves with kTiles
@@ -14,9 +14,11 @@
 //    transposes (ds_read_b64_tr_b16),
 //  - batch n + 2 goes from registers to LDS as it lies in memory, in aligned
 //    units, and batch n + 3 is asked for.
-// Per 64 cells and 16 rows a wave then does D / 2 products (16 x 16 x 32) and 2 D
-// VALU operations for the block scales (K's on the fp32 sums, V's on the
-// probabilities) + about 70 for the softmax: those bound it, not the products.
+// Per 64 cells and 16 rows a wave then does D / 4 products (16 x 16 x 32) and, counted
+// for heads of 128 in bf16, 310 VALU operations: D / 2 for K's block scales on the fp32
+// sums, about 110 for the softmax and the probabilities' conversion, the rest for
+// staging. No unit bounds it: VALU issue takes 51 % of the cycles, the matrix cores
+// 21 %, and waves wait (LDS, barrier) for 40 % of theirs, two of them on a SIMD.
 //
 // For bf16 activations V's scales are multiplied into the codes when these are
 // unpacked: code x scale rounded to fp16's 11 bits, once more what the
@@ -25,19 +27,18 @@
 // to [2^11, 2^12) (Q4_0) or [2^7, 2^8) (Q8_0), so that its largest product with a
 // code just fits fp16, and is given back to the probabilities: one operation for
 // each instead of one per block. Blocks keep their 11 bits down to scales 2^-21 of
-// the cell's largest; below, a scale is off by at most 2^-32 of it. 2048 tokens behind 16000, 32 / 8 heads of 128: 1215
-// us without, 1112 us with it in fp16, where the second rounding would add a
-// quarter to the result's error. (Not for K: an error of a score is multiplied by
-// the score's size. It would save a fifth.)
+// the cell's largest; below, a scale is off by at most 2^-32 of it. In fp16 the second
+// rounding would add a quarter to the result's error, for 8 % less time. (Not for K: an
+// error of a score is multiplied by the score's size. It would save a fifth.)
 //
 // Measured: 2048 tokens behind 16384 cells, 32 / 8 heads of 128, Q4_0, bf16:
-// 1005 us, 0.58 PFLOP/s (a large bf16 product: 1.2); ragged prompts of up to 1531
-// tokens, heads of 64, Q8_0 / Q4_0, fp16: 242 us; 512 tokens, 16 / 8 x 128, Q8_0,
-// fp32: 36 us with the join. VALU issue takes half of the cycles, the matrix cores
-// a fifth, waiting for LDS and the barrier most of the rest: 8 waves of 16 x 2
-// rows fill the registers, so a SIMD has two waves. Letting K's waves unpack
-// before and V's after their products, so that the two of a SIMD differ: 1000 us,
-// but 3 to 11 % slower for fp16.
+// 1042 us, 0.56 PFLOP/s (a large bf16 product: 1.2); ragged prompts of up to 1531
+// tokens, heads of 64, Q8_0 / Q4_0, fp16: 251 us (VALU 43 %, matrix cores 8 %, waits
+// 43 %); 512 tokens, 16 / 8 x 128, Q8_0, fp32: 31 us with the join (9). 8 waves of
+// 16 x 2 rows fill the registers (16-bit types and heads of 128: 10 to 21 of a lane's
+// are spilled), so a SIMD has two waves. Letting K's waves unpack before and V's after
+// their products, so that the two of a SIMD differ: 1 % faster for bf16, 3 to 11 %
+// slower for fp16.
 //
 // Shares (attn_device.hpp) of such items only where a few long ones would leave
 // most of the GPU idle; attn_plan.hpp has the rule.

@@ -8,10 +8,9 @@
 // Both are copies with a little arithmetic: bound by HBM bandwidth where n is
 // large, by the launch where it is not. So K and V go in one launch
 // (blockIdx.y), and the rows are addressed by their slots directly. Q8_0 / Q4_0
-// x 1024 to bf16: 333 cells 2.5 us, 16000 cells 15 us (6.0 TB/s, mostly out of
-// the caches), 131000 cells in order 102 us (7.4 TB/s), at random 164 us (4.6):
-// what is left there are the cache's rows of 1088 and 576 bytes, in DRAM pages
-// that nobody else opens.
+// x 1024 to bf16, 131000 cells (755 MB read and written): 135 us in order and 146 us
+// at random from memory (5.6 and 5.2 TB/s), 115 and 118 us where the last-level cache
+// still holds the cells; 333 cells to fp32: 2.8 us.
 //
 // Work split: four lanes per block, eight elements each. A wave then reads
 // 16 whole blocks side by side (a lane's own 32 elements would be 64 or 128
@@ -248,10 +247,11 @@ constexpr int64_t kMaxGrid = 1 << 22;
 constexpr int64_t kManyBlocks = 1 << 17;
 
 // Results above half of the last-level cache's 256 MB, most of which is gone
-// before somebody reads it, are written past the caches: 131000 x 1024 in order,
-// bf16: 162 us through them, 102 us (7.4 TB/s) past them; 64000: 78 and 52 us.
-// Smaller ones stay for their reader. fp32, whose block is two writes of each
-// lane, gains nothing (312 and 307 us).
+// before somebody reads it, are written past the caches. Where these hold the
+// cells, 131000 x 1024 in order, bf16: 149 us through them, 115 us past them; 64000:
+// 78 and 63 us. With the cells in memory both take the same (135 us, 71 us; at random
+// 140 and 146 us). Smaller results stay for their reader. fp32, whose block is two
+// writes of each lane, gains nothing (312 and 307 us).
 constexpr int64_t kStreamBytes = 128 << 20;
 
 dim3 grid_for(int64_t n, int64_t nb, int each) {
