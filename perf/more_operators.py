@@ -25,33 +25,33 @@ BLOCK = {"q4_0": (32, 18), "q8_0": (32, 34), "q4_k": (256, 144), "q6_k": (256, 2
 def listed():
     return [
         # a decode step of one chat: its token's row of a 0.6B model's embedding (151936 x 1024, tied to the output head)
-        {"name": "embed, one token", "op": "embed", "fmt": "q6_k", "rows": 151936, "K": 1024, "n": 1, "dtype": "f32", "lost": 0},
+        {"name": "embed: one token", "op": "embed", "fmt": "q6_k", "rows": 151936, "K": 1024, "n": 1, "dtype": "f32", "lost": 0},
         # the prompts of a batch, padded to a captured size
-        {"name": "embed, 16384 tokens", "op": "embed", "fmt": "q6_k", "rows": 151936, "K": 1024, "n": 16384, "dtype": "bf16", "lost": 9},
+        {"name": "embed: 16384 tokens", "op": "embed", "fmt": "q6_k", "rows": 151936, "K": 1024, "n": 16384, "dtype": "bf16", "lost": 9},
         # one chat's token in the library's own activation type: all latency
-        {"name": "norm, one token", "op": "norm", "n": 1, "K": 1024, "dtype": "f32", "residual": True, "want": "rows"},
+        {"name": "norm: one token", "op": "norm", "n": 1, "K": 1024, "dtype": "f32", "residual": True, "want": "rows"},
         # a decode batch of a 7B model, from the product before (fp32) to the product behind (Q8_0)
-        {"name": "norm, 61 tokens to Q8_0", "op": "norm", "n": 61, "K": 4096, "dtype": "f32", "residual": True, "want": "q8"},
+        {"name": "norm: 61 tokens to Q8_0", "op": "norm", "n": 61, "K": 4096, "dtype": "f32", "residual": True, "want": "q8"},
         # a long prompt, residual stream in bf16; its rows also go on as they are
-        {"name": "norm, 8192 tokens", "op": "norm", "n": 8192, "K": 4096, "dtype": "bf16", "residual": True, "want": "both"},
+        {"name": "norm: 8192 tokens", "op": "norm", "n": 8192, "K": 4096, "dtype": "bf16", "residual": True, "want": "both"},
         # a decode batch far into long documents, fp32 projections to fp16 queries and keys
-        {"name": "rope, 64 far tokens", "op": "rope", "n": 64, "heads": 32, "kv_heads": 8, "head_dim": 128, "rot": 128, "axes": 1,
+        {"name": "rope: 64 far tokens", "op": "rope", "n": 64, "heads": 32, "kv_heads": 8, "head_dim": 128, "rot": 128, "axes": 1,
          "neighbours": False, "in": "f32", "out": "f16", "norm": False, "far": 1000000, "cycle": False},
         # text with pictures and a video: time, height and width, heads normed before
-        {"name": "rope, 8191 tokens, 3 axes", "op": "rope", "n": 8191, "heads": 32, "kv_heads": 8, "head_dim": 128, "rot": 128, "axes": 3,
+        {"name": "rope: 8191 tokens on 3 axes", "op": "rope", "n": 8191, "heads": 32, "kv_heads": 8, "head_dim": 128, "rot": 128, "axes": 3,
          "neighbours": False, "in": "bf16", "out": "bf16", "norm": True, "far": 30000, "cycle": False},
         # a decode step of 48 requests in small pages, and the token taken back
-        {"name": "pages, decode of 48", "op": "pages", "seqs": 48, "tokens": 1, "past": 4000, "page": 16, "ragged": False, "short": False, "lens": 1},
+        {"name": "pages: decode of 48", "op": "pages", "seqs": 48, "tokens": 1, "past": 4000, "page": 16, "ragged": False, "short": False, "lens": 1},
         # prompts of 200 requests that arrive together behind what they have; not all of them fit
-        {"name": "pages, ragged prompts", "op": "pages", "seqs": 200, "tokens": 600, "past": 3000, "page": 64, "ragged": True, "short": True, "lens": 2},
+        {"name": "pages: ragged prompts", "op": "pages", "seqs": 200, "tokens": 600, "past": 3000, "page": 64, "ragged": True, "short": True, "lens": 2},
         # one chat's adapter on a projection of a 0.6B model
-        {"name": "lora, one token", "op": "lora", "seqs": 1, "tokens": 1, "ragged": False, "adapters": 4, "rank": 16, "K": 1024, "M": 2048,
+        {"name": "lora: one token", "op": "lora", "seqs": 1, "tokens": 1, "ragged": False, "adapters": 4, "rank": 16, "K": 1024, "M": 2048,
          "dtype": "f16", "lens": 1},
         # a decode batch of 64 requests with 24 adapters beside a 7B model's projection
-        {"name": "lora, decode of 64", "op": "lora", "seqs": 64, "tokens": 1, "ragged": False, "adapters": 24, "rank": 16, "K": 4096, "M": 11008,
+        {"name": "lora: decode of 64", "op": "lora", "seqs": 64, "tokens": 1, "ragged": False, "adapters": 24, "rank": 16, "K": 4096, "M": 11008,
          "dtype": "bf16", "lens": 2},
         # ragged prompts of 7 requests, larger ranks
-        {"name": "lora, ragged prompts", "op": "lora", "seqs": 7, "tokens": 509, "ragged": True, "adapters": 5, "rank": 64, "K": 11008, "M": 4096,
+        {"name": "lora: ragged prompts", "op": "lora", "seqs": 7, "tokens": 509, "ragged": True, "adapters": 5, "rank": 64, "K": 11008, "M": 4096,
          "dtype": "bf16", "lens": 3},
     ]
 
