@@ -94,6 +94,8 @@ def load_library():
     lib.qmat_attn_workspace_bytes.restype = i64
     lib.qmat_attn.argtypes = [ctypes.POINTER(AttnArgs), p, i64, p]
     lib.qmat_attn.restype = i32
+    lib.qmat_embed.argtypes = [i32, i32, p, p, p, i64, i64, i64, i64, p]
+    lib.qmat_embed.restype = i32
     _lib = lib
     return lib
 
@@ -544,4 +546,28 @@ def attn(k_fmt, v_fmt, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     else:
         _launch("qmat_attn", lib.qmat_attn, q.device, ref, workspace.data_ptr(),
                 workspace.numel())
+    return out
+
+
+def embed(fmt, blocks: torch.Tensor, K: int, ids: torch.Tensor | None = None,
+          dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows ids [n] (int32; every row in order if None) of the packed matrix
+    blocks (uint8 [rows, row_bytes(fmt, K)]) as [n, K] values of dtype; an id
+    outside the matrix gives zeros."""
+    f = _fmt(fmt)
+    _gpu(blocks, "blocks", torch.uint8)
+    rb = row_bytes(f, K)
+    if blocks.dim() != 2 or blocks.shape[1] != rb:
+        raise ValueError("blocks must be 2-D [rows, row_bytes(fmt, K)]")
+    device, rows = blocks.device, blocks.shape[0]
+    if ids is not None:
+        _flat(ids, "ids", torch.int32, device)
+    n = rows if ids is None else ids.numel()
+    if out is None:
+        out = torch.empty((n, K), dtype=dtype, device=device)
+    dt, stride = _dtype(dtype), _rows(out, "out", dtype)
+    if out.device != device or out.shape[0] != n or out.numel() != n * K:
+        raise ValueError("out must hold n rows of K elements, on the device of blocks")
+    _launch("qmat_embed", load_library().qmat_embed, device, f, dt, blocks.data_ptr(),
+            None if ids is None else ids.data_ptr(), out.data_ptr(), stride, n, rows, K)
     return out

@@ -28,26 +28,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlocksPerWG = kThreads / 4;
 
-template <int kCtrl>
-__device__ __forceinline__ float quad_max(float v) {
-  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, true);
-  return fmaxf(v, __builtin_bit_cast(float, o));
-}
-
-// Row and block column of block i of rows of nb blocks; 32-bit division
-// wherever the counts fit.
-__device__ __forceinline__ void split_index(int64_t i, int64_t total, int nb, int64_t* row,
-                                            int* col) {
-  if (total <= 0xFFFFFFFFLL) {
-    const uint32_t r = (uint32_t)i / (uint32_t)nb;
-    *row = r;
-    *col = (int)((uint32_t)i - r * (uint32_t)nb);
-  } else {
-    *row = i / nb;
-    *col = (int)(i - *row * nb);
-  }
-}
-
 // kEach blocks of a lane at once: all slots and elements are asked for before
 // the first is needed.
 template <bool kQ4, int kEach, typename T>
@@ -122,19 +102,6 @@ __device__ __forceinline__ void store_blocks(const T* __restrict__ x, int64_t st
         *reinterpret_cast<u32x2_a2*>(dst + 2 + 8 * q) = u32x2_a2{w0, w1};
     }
   }
-}
-
-// 16 bytes of elements, rounded once to nearest even; kStream: past the caches.
-template <bool kStream, typename T>
-__device__ __forceinline__ void put16(T* __restrict__ p, const float* v) {
-  typedef T vec __attribute__((ext_vector_type(16 / sizeof(T))));
-  vec t;
-#pragma unroll
-  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) t[i] = (T)v[i];
-  if constexpr (kStream)
-    __builtin_nontemporal_store(t, reinterpret_cast<vec*>(p));
-  else
-    *reinterpret_cast<vec*>(p) = t;
 }
 
 // kEach blocks of a lane at once: their slots, then their codes, are all asked

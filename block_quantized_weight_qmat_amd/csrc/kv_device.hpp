@@ -1,5 +1,5 @@
-// kv_device.hpp — the quantized KV cache as its kernels see it: element
-// types of activations, block geometry, unaligned access to packed blocks.
+// kv_device.hpp — packed blocks and rows of activations as the kernels of the
+// cache and of a step see them: element types, block geometry, unaligned access.
 #pragma once
 
 #include "qmat_device.hpp"
@@ -40,6 +40,41 @@ __device__ __forceinline__ void store_f32(T* __restrict__ p, const float* v) {
 #pragma unroll
   for (int i = 0; i < N; ++i) t[i] = (T)v[i];
   *reinterpret_cast<vec*>(p) = t;
+}
+
+// The larger of v and a neighbour's in a quad of lanes: kCtrl 0xB1 (lanes
+// 1,0,3,2), then 0x4E (lanes 2,3,0,1) give all four the quad's maximum.
+template <int kCtrl>
+__device__ __forceinline__ float quad_max(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, true);
+  return fmaxf(v, __builtin_bit_cast(float, o));
+}
+
+// Row and block column of block i of rows of nb blocks; 32-bit division
+// wherever the counts fit.
+__device__ __forceinline__ void split_index(int64_t i, int64_t total, int nb, int64_t* row,
+                                            int* col) {
+  if (total <= 0xFFFFFFFFLL) {
+    const uint32_t r = (uint32_t)i / (uint32_t)nb;
+    *row = r;
+    *col = (int)((uint32_t)i - r * (uint32_t)nb);
+  } else {
+    *row = i / nb;
+    *col = (int)(i - *row * nb);
+  }
+}
+
+// 16 bytes of elements, rounded once to nearest even; kStream: past the caches.
+template <bool kStream, typename T>
+__device__ __forceinline__ void put16(T* __restrict__ p, const float* v) {
+  typedef T vec __attribute__((ext_vector_type(16 / sizeof(T))));
+  vec t;
+#pragma unroll
+  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) t[i] = (T)v[i];
+  if constexpr (kStream)
+    __builtin_nontemporal_store(t, reinterpret_cast<vec*>(p));
+  else
+    *reinterpret_cast<vec*>(p) = t;
 }
 
 }  // namespace qmat

@@ -6,37 +6,19 @@
 #include <initializer_list>
 
 #include "qmat.h"
+#include "qmat_checks.hpp"
 #include "qmat_launch.hpp"
 
 namespace {
 
-constexpr int64_t kMaxDim = 0x7FFFFFFFLL;
+using namespace qmat;
+
 constexpr int64_t kMaxTokens = 1LL << 24;  // also sequences
 constexpr int64_t kMaxHeads = 1LL << 12;
 constexpr int64_t kMaxCells = 1LL << 30;   // of one sequence; also query rows of a cache head
 constexpr int64_t kMaxRows = 1LL << 30;    // of all tokens and heads
 
 bool cache_fmt_ok(int fmt) { return fmt == QMAT_Q4_0 || fmt == QMAT_Q8_0; }
-
-bool dtype_ok(int dtype) {
-  return dtype == QMAT_F32 || dtype == QMAT_F16 || dtype == QMAT_BF16;
-}
-
-int64_t dtype_bytes(int dtype) { return dtype == QMAT_F32 ? 4 : 2; }
-
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-int check_buf(const void* p) {
-  if (p == nullptr) return QMAT_E_NULL;
-  return aligned(p, 16) ? QMAT_OK : QMAT_E_ALIGN;
-}
-
-// rows of row_elems elements, stride elements apart, addressable in int64 bytes
-bool rows_ok(int64_t rows, int64_t row_elems, int64_t stride, int64_t bytes) {
-  return stride >= row_elems && stride <= INT64_MAX / bytes / (rows > 0 ? rows : 1);
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? QMAT_OK : QMAT_E_HIP; }
 
 // The common checks of qmat_kv_store and qmat_kv_load; *empty when there is
 // nothing to read or write.
@@ -85,8 +67,7 @@ int check_attn(const qmat_attn_args& a) {
   const int64_t row = a.heads * a.head_dim, size = dtype_bytes(a.dtype);
   if (!rows_ok(a.n_tokens, row, a.q_stride, size) || !rows_ok(a.n_tokens, row, a.out_stride, size))
     return QMAT_E_SHAPE;
-  // finite: a NaN or an infinity fails its own subtraction
-  if (!(a.scale - a.scale == 0.0f)) return QMAT_E_SHAPE;
+  if (!finite(a.scale)) return QMAT_E_SHAPE;
   return QMAT_OK;
 }
 

@@ -45,6 +45,11 @@ hipError_t launch_kv_load(int k_fmt, int v_fmt, int dtype, const KvRows& r, hipS
 int64_t attn_workspace_bytes(const qmat_attn_args& a);
 hipError_t launch_attn(const qmat_attn_args& a, void* workspace, hipStream_t stream);
 
+// Rows of a packed matrix as rows of dtype (embed.hip); ids on the device, NULL: 0, 1, ...
+hipError_t launch_embed(int fmt, int dtype, const void* blocks, const int32_t* ids, void* out,
+                        int64_t out_stride, int64_t n, int64_t rows, int64_t K,
+                        hipStream_t stream);
+
 hipError_t launch_gemv(int fmt, const void* blocks, const float* x, float* y, int64_t M,
                        int64_t K, hipStream_t stream);
 

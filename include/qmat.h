@@ -1,7 +1,7 @@
 /*
  * qmat.h — C ABI of the block-quantized weight matmul for MI355X (gfx950).
  *
- * Nine operations, all enqueued asynchronously on a caller-supplied HIP
+ * Ten operations, all enqueued asynchronously on a caller-supplied HIP
  * stream:
  *   qmat_quantize  fp32 matrix  -> packed weight (or activation) blocks
  *   qmat_gemv      packed W × fp32 x        -> fp32 y        (decode)
@@ -12,6 +12,7 @@
  *   qmat_kv_store  fp32 / fp16 / bf16 K and V rows -> the named cache cells
  *   qmat_kv_load   the named cache cells -> fp32 / fp16 / bf16 K and V rows
  *   qmat_attn      attention of new tokens over a paged Q4_0 / Q8_0 cache
+ *   qmat_embed     named rows of a packed matrix -> fp32 / fp16 / bf16 rows
  * and qmat_prefill_noalloc, qmat_prefill without a caller workspace for
  * callers that cannot allocate device memory.
  *
@@ -129,7 +130,8 @@ typedef enum qmat_status {
   QMAT_E_DTYPE = 8      /* unknown element type                            */
 } qmat_status;
 
-/* Element type of the activations of qmat_kv_store, qmat_kv_load, qmat_attn. */
+/* Element type of the activations of qmat_kv_store, qmat_kv_load, qmat_attn,
+ * qmat_embed. */
 typedef enum qmat_dtype { QMAT_F32 = 0, QMAT_F16 = 1, QMAT_BF16 = 2 } qmat_dtype;
 
 /* Bytes of the static device workspace of qmat_prefill_noalloc (16 MiB):
@@ -519,6 +521,24 @@ int64_t qmat_attn_workspace_bytes(const qmat_attn_args *args);
  * workspace_bytes < 0, QMAT_E_WORKSPACE. */
 int qmat_attn(const qmat_attn_args *args, void *workspace, int64_t workspace_bytes,
               void *stream);
+
+/*
+ * qmat_embed — named rows of a packed matrix as rows of dtype: the first
+ *   operator of a decoder (its token embedding is such a matrix, [LC05 KV]),
+ *   and the way back from Q8_0 activations to values.
+ *     out[i][k] = T(dequant(blocks)[ids[i]][k]),  T = dtype,
+ *   computed in fp32 (exact for Q4_0, Q8_0 and Q6_K, one rounding for Q4_K)
+ *   and rounded to T, to nearest even.
+ *   fmt, blocks: W in any format, rows rows of K (16-byte aligned).
+ *   ids: DEVICE int32 [n] (4-byte aligned), each any number of times; an id
+ *        outside [0, rows) gives a row of zeros (padding of a batch). NULL:
+ *        row i is i, and n is at most rows (QMAT_E_SHAPE).
+ *   out: n rows, out_stride elements apart (>= K; 16-byte aligned, the stride
+ *        a whole multiple of 16 bytes); elements past K are left as they were.
+ *   n == 0 or K == 0 enqueues nothing; blocks may be NULL when rows is 0.
+ */
+int qmat_embed(int fmt, int dtype, const void *blocks, const int32_t *ids, void *out,
+               int64_t out_stride, int64_t n, int64_t rows, int64_t K, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,42 @@
+"""The entry points of a step on the CPU: refused arguments (through a
+sanitizer build of the C ABI with stub launchers), and the binding's own
+checks."""
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+from block_quantized_weight_qmat_amd import binding
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HC = os.path.join(ROOT, "tests", "host_check")
+CSRC = os.path.join(ROOT, "block_quantized_weight_qmat_amd", "csrc")
+
+needs_lib = pytest.mark.skipif(not os.path.exists(binding.library_path()), reason="libqmat.so not built")
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_step_abi_checks_under_sanitizers(tmp_path):
+    exe = str(tmp_path / "step_abi_drv")
+    r = subprocess.run(
+        ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+         f"-I{HC}", f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}", "-x", "c++", os.path.join(CSRC, "qmat_api.cpp"),
+         os.path.join(CSRC, "qmat_step_api.cpp"), os.path.join(HC, "launch_stub.cpp"),
+         os.path.join(HC, "step_launch_stub.cpp"), os.path.join(HC, "step_abi_driver.cpp"), "-o", exe],
+        capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "all cases ok" in r.stdout, r.stdout + r.stderr
+
+
+@needs_lib
+def test_embed_refuses_cpu_tensors_and_types():
+    t = torch.zeros(4, 34, dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        binding.embed("q8_0", t, 32)
+    with pytest.raises(TypeError):
+        binding.embed("q8_0", t.float(), 32)
+    with pytest.raises(KeyError):
+        binding.embed("q5_0", t, 32)
