@@ -36,6 +36,16 @@ class AttnArgs(ctypes.Structure):
                 [("scale", ctypes.c_float)])
 
 
+class NormArgs(ctypes.Structure):
+    """The C struct qmat_norm_args."""
+    _fields_ = ([("dtype", ctypes.c_int32)] +
+                [(n, ctypes.c_void_p) for n in ("x", "residual", "residual_out", "weight", "rows",
+                                                "q8")] +
+                [(n, ctypes.c_int64) for n in ("x_stride", "residual_stride", "residual_out_stride",
+                                               "rows_stride", "n", "K")] +
+                [("eps", ctypes.c_double)])
+
+
 class QmatError(RuntimeError):
     """A non-zero status returned by the C ABI."""
 
@@ -96,6 +106,8 @@ def load_library():
     lib.qmat_attn.restype = i32
     lib.qmat_embed.argtypes = [i32, i32, p, p, p, i64, i64, i64, i64, p]
     lib.qmat_embed.restype = i32
+    lib.qmat_norm.argtypes = [ctypes.POINTER(NormArgs), p]
+    lib.qmat_norm.restype = i32
     _lib = lib
     return lib
 
@@ -571,3 +583,60 @@ def embed(fmt, blocks: torch.Tensor, K: int, ids: torch.Tensor | None = None,
     _launch("qmat_embed", load_library().qmat_embed, device, f, dt, blocks.data_ptr(),
             None if ids is None else ids.data_ptr(), out.data_ptr(), stride, n, rows, K)
     return out
+
+
+def _same(t: torch.Tensor, name: str, x: torch.Tensor) -> int:
+    """Token stride of t, which has the shape, type and device of x."""
+    stride = _rows(t, name, x.dtype)
+    if t.shape != x.shape or t.device != x.device:
+        raise ValueError(f"{name} must have the shape and device of its counterpart")
+    return stride
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+             residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+             want: str = "q8", rows: torch.Tensor | None = None, q8: torch.Tensor | None = None):
+    """h = x + residual (x alone without one), y = h / sqrt(mean h^2 + eps) * weight, for
+    x [n, K] (fp32, fp16 or bf16; tokens any stride apart) and weight [K] (fp32).
+    want: "q8" for y as Q8_0 blocks (what gemm takes), "rows" for y in x's type
+    (gemv's x), "both". Returns (rows or None, q8 or None, h or None). h goes to
+    residual_out, which may be residual or x itself; rows may be x itself."""
+    if want not in ("q8", "rows", "both"):
+        raise ValueError(f'want must be "q8", "rows" or "both", not {want!r}')
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [n, K]")
+    dt, xs = _dtype(x.dtype), _rows(x, "x", x.dtype)
+    n, K = x.shape
+    device = x.device
+    if K % 32 != 0:
+        raise ValueError(f"{K} elements are not whole blocks of 32")
+    _flat(weight, "weight", torch.float32, device)
+    if weight.numel() != K:
+        raise ValueError("weight must hold K values")
+    rs = hs = ys = 0
+    rp = hp = yp = qp = None
+    if residual is not None:
+        rs, rp = _same(residual, "residual", x), residual.data_ptr()
+        if residual_out is None:
+            residual_out = torch.empty((n, K), dtype=x.dtype, device=device)
+        hs, hp = _same(residual_out, "residual_out", x), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if want == "q8":
+        rows = None
+    else:
+        if rows is None:
+            rows = torch.empty((n, K), dtype=x.dtype, device=device)
+        ys, yp = _same(rows, "rows", x), rows.data_ptr()
+    if want == "rows":
+        q8 = None
+    else:
+        if q8 is None:
+            q8 = torch.empty((n, K // 32 * 34), dtype=torch.uint8, device=device)
+        _flat(q8, "q8", torch.uint8, device)
+        if q8.numel() != n * (K // 32 * 34):
+            raise ValueError("q8 has the wrong size")
+        qp = q8.data_ptr()
+    a = NormArgs(dt, x.data_ptr(), rp, hp, weight.data_ptr(), yp, qp, xs, rs, hs, ys, n, K, eps)
+    _launch("qmat_norm", load_library().qmat_norm, device, ctypes.byref(a))
+    return rows, q8, residual_out

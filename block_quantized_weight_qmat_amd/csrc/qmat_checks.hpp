@@ -32,7 +32,7 @@ inline bool rows_ok(int64_t rows, int64_t row_elems, int64_t stride, int64_t byt
 }
 
 // finite: a NaN or an infinity fails its own subtraction
-inline bool finite(float v) { return v - v == 0.0f; }
+inline bool is_finite(double v) { return v - v == 0.0; }
 
 inline int hip_status(hipError_t e) { return e == hipSuccess ? QMAT_OK : QMAT_E_HIP; }
 

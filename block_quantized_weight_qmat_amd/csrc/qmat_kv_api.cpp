@@ -67,7 +67,7 @@ int check_attn(const qmat_attn_args& a) {
   const int64_t row = a.heads * a.head_dim, size = dtype_bytes(a.dtype);
   if (!rows_ok(a.n_tokens, row, a.q_stride, size) || !rows_ok(a.n_tokens, row, a.out_stride, size))
     return QMAT_E_SHAPE;
-  if (!finite(a.scale)) return QMAT_E_SHAPE;
+  if (!is_finite(a.scale)) return QMAT_E_SHAPE;
   return QMAT_OK;
 }
 

@@ -1,6 +1,6 @@
 // qmat_step_api.cpp — the C ABI of a step around the products and the cache
-// (include/qmat.h: qmat_embed): every argument is checked on the host before anything is
-// enqueued; embed.hip launches the kernels.
+// (include/qmat.h: qmat_embed, qmat_norm): every argument is checked on the
+// host before anything is enqueued; embed.hip and norm.hip launch the kernels.
 #include <hip/hip_runtime.h>
 
 #include "qmat.h"
@@ -10,6 +10,14 @@
 namespace {
 
 using namespace qmat;
+
+constexpr int64_t kMaxNormK = 1LL << 24;
+
+// Rows of activations: 16-byte aligned, as is their stride in bytes.
+int check_rows(const void* p, int64_t stride, int64_t size) {
+  if (const int rc = check_buf(p); rc != QMAT_OK) return rc;
+  return stride * size % 16 == 0 ? QMAT_OK : QMAT_E_ALIGN;
+}
 
 }  // namespace
 
@@ -29,10 +37,34 @@ int qmat_embed(int fmt, int dtype, const void* blocks, const int32_t* ids, void*
   int rc = QMAT_OK;
   if (rows > 0 && (rc = check_buf(blocks)) != QMAT_OK) return rc;
   if (!aligned(ids, 4)) return QMAT_E_ALIGN;
-  if ((rc = check_buf(out)) != QMAT_OK) return rc;
-  if (out_stride * size % 16 != 0) return QMAT_E_ALIGN;
+  if ((rc = check_rows(out, out_stride, size)) != QMAT_OK) return rc;
   return hip_status(launch_embed(fmt, dtype, blocks, ids, out, out_stride, n, rows, K,
                                  static_cast<hipStream_t>(stream)));
+}
+
+int qmat_norm(const qmat_norm_args* args, void* stream) {
+  if (args == nullptr) return QMAT_E_NULL;
+  const qmat_norm_args& a = *args;
+  if (!dtype_ok(a.dtype)) return QMAT_E_DTYPE;
+  if (a.n < 0 || a.n > kMaxDim || a.K < 0 || a.K > kMaxNormK || a.K % 32 != 0) return QMAT_E_SHAPE;
+  if (!is_finite(a.eps) || a.eps < 0) return QMAT_E_SHAPE;
+  const int64_t size = dtype_bytes(a.dtype);
+  const bool sum = a.residual != nullptr || a.residual_out != nullptr;
+  if (!rows_ok(a.n, a.K, a.x_stride, size) ||
+      (sum && (!rows_ok(a.n, a.K, a.residual_stride, size) ||
+               !rows_ok(a.n, a.K, a.residual_out_stride, size))) ||
+      (a.rows != nullptr && !rows_ok(a.n, a.K, a.rows_stride, size)))
+    return QMAT_E_SHAPE;
+  if (a.n == 0 || a.K == 0) return QMAT_OK;
+  if (a.rows == nullptr && a.q8 == nullptr) return QMAT_E_NULL;
+  int rc = check_rows(a.x, a.x_stride, size);
+  if (rc == QMAT_OK) rc = check_buf(a.weight);
+  if (rc == QMAT_OK && sum) rc = check_rows(a.residual, a.residual_stride, size);
+  if (rc == QMAT_OK && sum) rc = check_rows(a.residual_out, a.residual_out_stride, size);
+  if (rc == QMAT_OK && a.rows != nullptr) rc = check_rows(a.rows, a.rows_stride, size);
+  if (rc == QMAT_OK && !aligned(a.q8, 16)) rc = QMAT_E_ALIGN;
+  if (rc != QMAT_OK) return rc;
+  return hip_status(launch_norm(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

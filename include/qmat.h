@@ -1,7 +1,7 @@
 /*
  * qmat.h — C ABI of the block-quantized weight matmul for MI355X (gfx950).
  *
- * Ten operations, all enqueued asynchronously on a caller-supplied HIP
+ * Eleven operations, all enqueued asynchronously on a caller-supplied HIP
  * stream:
  *   qmat_quantize  fp32 matrix  -> packed weight (or activation) blocks
  *   qmat_gemv      packed W × fp32 x        -> fp32 y        (decode)
@@ -13,6 +13,7 @@
  *   qmat_kv_load   the named cache cells -> fp32 / fp16 / bf16 K and V rows
  *   qmat_attn      attention of new tokens over a paged Q4_0 / Q8_0 cache
  *   qmat_embed     named rows of a packed matrix -> fp32 / fp16 / bf16 rows
+ *   qmat_norm      residual sum and RMS norm -> rows and / or Q8_0 blocks
  * and qmat_prefill_noalloc, qmat_prefill without a caller workspace for
  * callers that cannot allocate device memory.
  *
@@ -131,7 +132,7 @@ typedef enum qmat_status {
 } qmat_status;
 
 /* Element type of the activations of qmat_kv_store, qmat_kv_load, qmat_attn,
- * qmat_embed. */
+ * qmat_embed, qmat_norm. */
 typedef enum qmat_dtype { QMAT_F32 = 0, QMAT_F16 = 1, QMAT_BF16 = 2 } qmat_dtype;
 
 /* Bytes of the static device workspace of qmat_prefill_noalloc (16 MiB):
@@ -539,6 +540,46 @@ int qmat_attn(const qmat_attn_args *args, void *workspace, int64_t workspace_byt
  */
 int qmat_embed(int fmt, int dtype, const void *blocks, const int32_t *ids, void *out,
                int64_t out_stride, int64_t n, int64_t rows, int64_t K, void *stream);
+
+/*
+ * qmat_norm — the residual sum and the RMS norm before a projection, in one
+ *   pass, with the result as the Q8_0 blocks that qmat_gemm takes, as rows
+ *   (qmat_gemv's fp32 x), or both. For each of n rows of K elements:
+ *     h = T(x + residual)  (x where there is no residual),  T = dtype,
+ *     y = f32(h * (1 / sqrt(sum_k h_k^2 / K + eps)) * weight),
+ *     residual_out = h,  rows = T(y),  q8 = qmat_quantize(QMAT_Q8_0, y).
+ *   x + residual is one fp32 sum. The sum of squares, the root and the
+ *   products are held in 64 bits and y is rounded to fp32 once, so that q8 holds
+ *   the bytes of the formula: a code next to a border would otherwise
+ *   depend on the order of the sum. (The 64-bit value is off by a few 2^-53 of
+ *   itself; where it lies that near to a rounding border of fp32, y may be the
+ *   neighbour.)
+ *   x, residual, residual_out, rows: n rows of dtype, their strides in
+ *     elements (>= K, whole multiples of 16 bytes). residual and residual_out
+ *     are both given or both NULL. residual_out may be residual or x itself,
+ *     and rows may be x itself, with the same stride; nothing else overlaps.
+ *     Elements of a row past K are left as they were.
+ *   weight: fp32 [K]. eps: finite, >= 0 (QMAT_E_SHAPE).
+ *   rows, q8: at least one of them (QMAT_E_NULL). q8: n rows of
+ *     qmat_row_bytes(QMAT_Q8_0, K) bytes, without gaps.
+ *   All pointers 16-byte aligned. K is a multiple of 32, at most 2^24. n == 0 or K == 0 enqueues
+ *   nothing. Rows with an infinity or a NaN give unspecified q8 bytes and the
+ *   formula's values in rows; they touch no other row.
+ */
+typedef struct qmat_norm_args {
+  int32_t dtype;
+  const void *x;
+  const void *residual; /* or NULL */
+  void *residual_out;   /* or NULL */
+  const float *weight;
+  void *rows;           /* or NULL */
+  void *q8;             /* or NULL */
+  int64_t x_stride, residual_stride, residual_out_stride, rows_stride;
+  int64_t n, K;
+  double eps;
+} qmat_norm_args;
+
+int qmat_norm(const qmat_norm_args *args, void *stream);
 
 #ifdef __cplusplus
 }

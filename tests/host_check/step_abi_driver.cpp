@@ -55,8 +55,73 @@ static void embed_cases() {
   EMBED(QMAT_OK, 1, 0, 0, NULL, S, A, 64, 3, 0, 64);  // every id outside: zeros
 }
 
+static qmat_norm_args norm_good() {
+  qmat_norm_args a = {};
+  a.dtype = QMAT_BF16;
+  a.eps = 1e-6;
+  a.x = a.residual = A;
+  a.residual_out = a.rows = a.q8 = A;
+  a.weight = (const float*)A;
+  a.x_stride = a.residual_stride = a.residual_out_stride = a.rows_stride = 64;
+  a.n = 3;
+  a.K = 64;
+  return a;
+}
+
+static void norm_cases() {
+#define NORM(field, value, want, launches)  \
+  do {                                      \
+    qmat_norm_args x = norm_good();         \
+    x.field = value;                        \
+    EXPECT(qmat_norm(&x, NULL), want, launches); \
+  } while (0)
+  EXPECT(qmat_norm(NULL, NULL), QMAT_E_NULL, 0);
+  NORM(eps, 0.0, QMAT_OK, 1);
+  NORM(dtype, 3, QMAT_E_DTYPE, 0);
+  NORM(dtype, -1, QMAT_E_DTYPE, 0);
+  NORM(n, -1, QMAT_E_SHAPE, 0);
+  NORM(n, big, QMAT_E_SHAPE, 0);
+  NORM(K, -32, QMAT_E_SHAPE, 0);
+  NORM(K, 48, QMAT_E_SHAPE, 0);
+  NORM(K, ((int64_t)1 << 24) + 32, QMAT_E_SHAPE, 0);
+  NORM(K, 96, QMAT_E_SHAPE, 0);  // strides shorter than a row
+  NORM(eps, -1e-9, QMAT_E_SHAPE, 0);
+  NORM(eps, NAN, QMAT_E_SHAPE, 0);
+  NORM(eps, INFINITY, QMAT_E_SHAPE, 0);
+  NORM(x_stride, 32, QMAT_E_SHAPE, 0);
+  NORM(residual_stride, 0, QMAT_E_SHAPE, 0);
+  NORM(residual_out_stride, 63, QMAT_E_SHAPE, 0);
+  NORM(rows_stride, -64, QMAT_E_SHAPE, 0);
+  NORM(x_stride, INT64_MAX, QMAT_E_SHAPE, 0);
+  NORM(x, NULL, QMAT_E_NULL, 0);
+  NORM(weight, NULL, QMAT_E_NULL, 0);
+  NORM(residual, NULL, QMAT_E_NULL, 0);
+  NORM(residual_out, NULL, QMAT_E_NULL, 0);
+  NORM(rows, NULL, QMAT_OK, 1);
+  NORM(q8, NULL, QMAT_OK, 1);
+  NORM(x, A + 8, QMAT_E_ALIGN, 0);
+  NORM(weight, (const float*)(A + 4), QMAT_E_ALIGN, 0);
+  NORM(residual, A + 2, QMAT_E_ALIGN, 0);
+  NORM(residual_out, A + 2, QMAT_E_ALIGN, 0);
+  NORM(rows, A + 8, QMAT_E_ALIGN, 0);
+  NORM(q8, A + 2, QMAT_E_ALIGN, 0);
+  NORM(x_stride, 68, QMAT_E_ALIGN, 0);
+  NORM(residual_stride, 65, QMAT_E_ALIGN, 0);
+  NORM(rows_stride, 66, QMAT_E_ALIGN, 0);
+  NORM(n, 0, QMAT_OK, 0);
+  NORM(K, 0, QMAT_OK, 0);
+  qmat_norm_args x = norm_good();
+  x.rows = x.q8 = NULL;
+  EXPECT(qmat_norm(&x, NULL), QMAT_E_NULL, 0);
+  x = norm_good();
+  x.residual = x.residual_out = NULL;  // their strides do not matter then
+  x.residual_stride = x.residual_out_stride = 0;
+  EXPECT(qmat_norm(&x, NULL), QMAT_OK, 1);
+}
+
 int main() {
   embed_cases();
+  norm_cases();
   if (failures) {
     fprintf(stderr, "%d failures\n", failures);
     return 1;

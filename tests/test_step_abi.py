@@ -40,3 +40,16 @@ def test_embed_refuses_cpu_tensors_and_types():
         binding.embed("q8_0", t.float(), 32)
     with pytest.raises(KeyError):
         binding.embed("q5_0", t, 32)
+
+
+@needs_lib
+def test_rms_norm_refuses():
+    x, w = torch.zeros(2, 64), torch.ones(64)
+    with pytest.raises(TypeError):
+        binding.rms_norm(x, w)
+    with pytest.raises(TypeError):
+        binding.rms_norm(x.double(), w)
+    with pytest.raises(ValueError):
+        binding.rms_norm(x, w, want="none")
+    with pytest.raises(ValueError):
+        binding.rms_norm(x[0], w)
