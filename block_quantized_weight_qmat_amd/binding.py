@@ -46,6 +46,17 @@ class NormArgs(ctypes.Structure):
                 [("eps", ctypes.c_double)])
 
 
+class RopeArgs(ctypes.Structure):
+    """The C struct qmat_rope_args."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("in_dtype", "out_dtype", "neighbours", "axes")] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out", "positions", "freq",
+                                                "axis", "q_norm", "k_norm")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride",
+                                               "k_out_stride", "pos_stride", "n", "heads",
+                                               "kv_heads", "head_dim", "rot_dim")] +
+                [("eps", ctypes.c_double)])
+
+
 class QmatError(RuntimeError):
     """A non-zero status returned by the C ABI."""
 
@@ -108,6 +119,8 @@ def load_library():
     lib.qmat_embed.restype = i32
     lib.qmat_norm.argtypes = [ctypes.POINTER(NormArgs), p]
     lib.qmat_norm.restype = i32
+    lib.qmat_rope.argtypes = [ctypes.POINTER(RopeArgs), p]
+    lib.qmat_rope.restype = i32
     _lib = lib
     return lib
 
@@ -640,3 +653,97 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     a = NormArgs(dt, x.data_ptr(), rp, hp, weight.data_ptr(), yp, qp, xs, rs, hs, ys, n, K, eps)
     _launch("qmat_norm", load_library().qmat_norm, device, ctypes.byref(a))
     return rows, q8, residual_out
+
+
+def rope_freq(rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """base^(-2i / rot_dim) for the pairs i < rot_dim / 2: rope's freq, fp64."""
+    if rot_dim < 0 or rot_dim % 2 != 0:
+        raise ValueError("rot_dim must be even")
+    return torch.tensor([float(base) ** (-2 * i / rot_dim) for i in range(rot_dim // 2)],
+                        dtype=torch.float64, device=device)
+
+
+def rope_axis(sections, cycle: bool = False, device="cuda") -> torch.Tensor:
+    """rope's axis for pairs shared out over axes: sections[a] pairs for axis a, one axis after
+    the other, or (cycle) in turn, an axis dropping out when its pairs are used up."""
+    left = [int(s) for s in sections]
+    if any(s < 0 for s in left):
+        raise ValueError("sections must not be negative")
+    if not cycle:
+        axis = [a for a, s in enumerate(left) for _ in range(s)]
+    else:
+        axis = [a for turn in range(max(left, default=0)) for a, s in enumerate(left) if turn < s]
+    return torch.tensor(axis, dtype=torch.int32, device=device)
+
+
+def _heads(t: torch.Tensor, name: str, like: torch.Tensor) -> int:
+    """Token stride of t [n, heads, head_dim], of like's type, tokens, head size and device."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [n, heads, head_dim]")
+    stride = _rows(t, name, like.dtype)
+    if t.device != like.device or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]:
+        raise ValueError(f"{name} must have the tokens, head size and device of q")
+    return stride
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, freq: torch.Tensor,
+         axis: torch.Tensor | None = None, neighbours: bool = False,
+         q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None,
+         eps: float = 1e-6, dtype: torch.dtype | None = None,
+         q_out: torch.Tensor | None = None,
+         k_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Rotary positions of q [n, heads, head_dim] and k [n, kv_heads, head_dim]
+    (or None) in one type, tokens any stride apart: pair i is turned by
+    positions[axis[i], t] * freq[i]. positions: int32 [n] or [axes, n]; freq: fp64
+    [pairs] (rope_freq); axis: int32 [pairs] (rope_axis; all 0 if None). Pairs
+    are (i, i + pairs), or neighbours (2i, 2i + 1); elements past 2 * pairs are
+    passed on. q_norm, k_norm (fp32 [head_dim]): an RMS norm of each head
+    before. Results in dtype (q's if None) go to q_out and k_out, which may be q
+    and k themselves."""
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D [n, heads, head_dim]")
+    it, qs, device = _dtype(q.dtype), _rows(q, "q", q.dtype), q.device
+    n, heads, head_dim = q.shape
+    if dtype is None:
+        dtype = q.dtype if q_out is None else q_out.dtype
+    ot = _dtype(dtype)
+    if q_out is None:
+        q_out = torch.empty((n, heads, head_dim), dtype=dtype, device=device)
+    if q_out.dtype != dtype:
+        raise TypeError(f"q_out must be {dtype}, got {q_out.dtype}")
+    if q_out.shape != q.shape or q_out.device != device:
+        raise ValueError("q_out must have the shape and device of q")
+    qos = _rows(q_out, "q_out", dtype)
+    ks = kos = kv_heads = 0
+    kp = kop = None
+    if k is not None:
+        ks, kp, kv_heads = _heads(k, "k", q), k.data_ptr(), k.shape[1]
+        if k_out is None:
+            k_out = torch.empty((n, kv_heads, head_dim), dtype=dtype, device=device)
+        kos, kop = _heads(k_out, "k_out", q_out), k_out.data_ptr()
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+    elif k_out is not None:
+        raise ValueError("k_out needs a k")
+    _flat(positions, "positions", torch.int32, device)
+    _flat(freq, "freq", torch.float64, device)
+    shape = positions.shape
+    if (len(shape) != 1 and len(shape) != 2) or shape[-1] != n:
+        raise ValueError("positions must be [n] or [axes, n]")
+    axes, pairs = (shape[0] if len(shape) == 2 else 1), freq.numel()
+    if axis is not None:
+        _flat(axis, "axis", torch.int32, device)
+        if axis.numel() != pairs:
+            raise ValueError("axis and freq must have one number for each pair")
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _flat(w, name, torch.float32, device)
+            if w.numel() != head_dim:
+                raise ValueError(f"{name} must hold head_dim values")
+    a = RopeArgs(it, ot, 1 if neighbours else 0, axes, q.data_ptr(), kp, q_out.data_ptr(), kop,
+                 positions.data_ptr(), freq.data_ptr(), None if axis is None else axis.data_ptr(),
+                 None if q_norm is None else q_norm.data_ptr(),
+                 None if k_norm is None else k_norm.data_ptr(), qs, ks, qos, kos, n, n, heads,
+                 kv_heads, head_dim, 2 * pairs, eps)
+    _launch("qmat_rope", load_library().qmat_rope, device, ctypes.byref(a))
+    return q_out, k_out

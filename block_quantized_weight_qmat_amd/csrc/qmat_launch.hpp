@@ -53,6 +53,9 @@ hipError_t launch_embed(int fmt, int dtype, const void* blocks, const int32_t* i
 // Residual sum and RMS norm (norm.hip).
 hipError_t launch_norm(const qmat_norm_args& a, hipStream_t stream);
 
+// Rotary positions of queries and keys (rope.hip).
+hipError_t launch_rope(const qmat_rope_args& a, hipStream_t stream);
+
 hipError_t launch_gemv(int fmt, const void* blocks, const float* x, float* y, int64_t M,
                        int64_t K, hipStream_t stream);
 

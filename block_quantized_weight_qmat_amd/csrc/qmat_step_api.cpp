@@ -1,6 +1,7 @@
 // qmat_step_api.cpp — the C ABI of a step around the products and the cache
-// (include/qmat.h: qmat_embed, qmat_norm): every argument is checked on the
-// host before anything is enqueued; embed.hip and norm.hip launch the kernels.
+// (include/qmat.h: qmat_embed, qmat_norm, qmat_rope): every argument is checked
+// on the host before anything is enqueued; embed.hip, norm.hip and rope.hip
+// launch the kernels.
 #include <hip/hip_runtime.h>
 
 #include "qmat.h"
@@ -12,6 +13,8 @@ namespace {
 using namespace qmat;
 
 constexpr int64_t kMaxNormK = 1LL << 24;
+constexpr int64_t kMaxRopeHeads = 1LL << 16;
+constexpr int64_t kMaxRopeRows = 1LL << 32;  // of all tokens and heads
 
 // Rows of activations: 16-byte aligned, as is their stride in bytes.
 int check_rows(const void* p, int64_t stride, int64_t size) {
@@ -65,6 +68,46 @@ int qmat_norm(const qmat_norm_args* args, void* stream) {
   if (rc == QMAT_OK && !aligned(a.q8, 16)) rc = QMAT_E_ALIGN;
   if (rc != QMAT_OK) return rc;
   return hip_status(launch_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+int qmat_rope(const qmat_rope_args* args, void* stream) {
+  if (args == nullptr) return QMAT_E_NULL;
+  const qmat_rope_args& a = *args;
+  if (!dtype_ok(a.in_dtype) || !dtype_ok(a.out_dtype)) return QMAT_E_DTYPE;
+  if (a.n < 0 || a.n > kMaxDim || a.heads < 0 || a.heads > kMaxRopeHeads || a.kv_heads < 0 ||
+      a.kv_heads > kMaxRopeHeads || a.heads + a.kv_heads > kMaxRopeHeads ||
+      a.n * (a.heads + a.kv_heads) > kMaxRopeRows)
+    return QMAT_E_SHAPE;
+  if (a.head_dim < 8 || a.head_dim > 512 || a.head_dim % 8 != 0 || a.rot_dim < 0 ||
+      a.rot_dim > a.head_dim || a.rot_dim % 8 != 0)
+    return QMAT_E_SHAPE;
+  if (a.axes < 1 || a.axes > 16 || !rows_ok(a.axes, a.n, a.pos_stride, 4) || !is_finite(a.eps) ||
+      a.eps < 0)
+    return QMAT_E_SHAPE;
+  struct {
+    const void *in, *out;
+    int64_t heads, in_stride, out_stride;
+  } const both[2] = {{a.q, a.q_out, a.heads, a.q_stride, a.q_out_stride},
+                     {a.k, a.k_out, a.kv_heads, a.k_stride, a.k_out_stride}};
+  const int64_t in = dtype_bytes(a.in_dtype), out = dtype_bytes(a.out_dtype);
+  for (const auto& x : both)
+    if (x.heads > 0 && (!rows_ok(a.n, x.heads * a.head_dim, x.in_stride, in) ||
+                        !rows_ok(a.n, x.heads * a.head_dim, x.out_stride, out)))
+      return QMAT_E_SHAPE;
+  if (a.n == 0 || a.heads + a.kv_heads == 0) return QMAT_OK;
+  int rc = QMAT_OK;
+  for (const auto& x : both) {
+    if (x.heads == 0) continue;
+    if ((rc = check_rows(x.in, x.in_stride, in)) != QMAT_OK) return rc;
+    if ((rc = check_rows(x.out, x.out_stride, out)) != QMAT_OK) return rc;
+  }
+  if (a.rot_dim > 0) {
+    if ((rc = check_buf(a.positions, 4)) != QMAT_OK) return rc;
+    if ((rc = check_buf(a.freq)) != QMAT_OK) return rc;
+    if (!aligned(a.axis, 4)) return QMAT_E_ALIGN;
+  }
+  if (!aligned(a.q_norm, 16) || !aligned(a.k_norm, 16)) return QMAT_E_ALIGN;
+  return hip_status(launch_rope(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

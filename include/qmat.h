@@ -1,7 +1,7 @@
 /*
  * qmat.h — C ABI of the block-quantized weight matmul for MI355X (gfx950).
  *
- * Eleven operations, all enqueued asynchronously on a caller-supplied HIP
+ * Twelve operations, all enqueued asynchronously on a caller-supplied HIP
  * stream:
  *   qmat_quantize  fp32 matrix  -> packed weight (or activation) blocks
  *   qmat_gemv      packed W × fp32 x        -> fp32 y        (decode)
@@ -14,6 +14,7 @@
  *   qmat_attn      attention of new tokens over a paged Q4_0 / Q8_0 cache
  *   qmat_embed     named rows of a packed matrix -> fp32 / fp16 / bf16 rows
  *   qmat_norm      residual sum and RMS norm -> rows and / or Q8_0 blocks
+ *   qmat_rope      rotary positions of queries and keys, of several axes
  * and qmat_prefill_noalloc, qmat_prefill without a caller workspace for
  * callers that cannot allocate device memory.
  *
@@ -132,7 +133,7 @@ typedef enum qmat_status {
 } qmat_status;
 
 /* Element type of the activations of qmat_kv_store, qmat_kv_load, qmat_attn,
- * qmat_embed, qmat_norm. */
+ * qmat_embed, qmat_norm, qmat_rope. */
 typedef enum qmat_dtype { QMAT_F32 = 0, QMAT_F16 = 1, QMAT_BF16 = 2 } qmat_dtype;
 
 /* Bytes of the static device workspace of qmat_prefill_noalloc (16 MiB):
@@ -580,6 +581,54 @@ typedef struct qmat_norm_args {
 } qmat_norm_args;
 
 int qmat_norm(const qmat_norm_args *args, void *stream);
+
+/*
+ * qmat_rope — rotary positions of queries and keys, between their projection
+ *   and qmat_kv_store / qmat_attn. Pair i of a head, i < rot_dim / 2, is
+ *   (x_i, x_{i + rot_dim/2}), or (x_2i, x_2i+1) where neighbours is set, and is
+ *   turned by theta = positions[axis[i]][t] * freq[i] for token t:
+ *     (a, b) -> (a cos theta - b sin theta, b cos theta + a sin theta).
+ *   Elements past rot_dim are passed on. With q_norm (k_norm), every head x of
+ *   q (k) is first normed: x / sqrt(sum x^2 / head_dim + eps) * q_norm.
+ *   Several axes (time, height, width of images and video): axis names the
+ *   axis of each pair, in any arrangement; a number outside [0, axes) leaves
+ *   its pair unturned.
+ *   Arithmetic: theta in 64 bits, reduced to less than half a turn, sine and
+ *   cosine in fp32: theta is off by at most 2^-51 of its size (2^-20 for the
+ *   largest positions with freq of 1) and its rest by 2^-23 of a turn. The
+ *   norm and the turn are fp32, rounded once to out_dtype; heads whose sum of squares
+ *   leaves fp32's range are not normed right.
+ *   q, k: [n] tokens, q_stride and k_stride elements apart, of heads and
+ *     kv_heads heads of head_dim elements of in_dtype. Either may have no
+ *     heads (and be NULL). q_out, k_out: the same of out_dtype; q_out may be q
+ *     itself (k_out k) with the same type and stride. Nothing else overlaps.
+ *   positions: DEVICE int32 [axes][n], pos_stride apart. freq: DEVICE fp64
+ *     [rot_dim / 2], radians for each position. axis: DEVICE int32
+ *     [rot_dim / 2], NULL: all 0. q_norm, k_norm: fp32 [head_dim] or NULL.
+ *   Limits (QMAT_E_SHAPE): head_dim a multiple of 8, 8 to 512; rot_dim a
+ *   multiple of 8, 0 to head_dim; heads + kv_heads at most 2^16; axes 1 to 16; n at most
+ *   2^31 - 1, n * (heads + kv_heads) at most 2^32; strides at least the heads' elements, pos_stride >= n; eps
+ *   finite, >= 0.
+ *   Alignment: q, k, q_out, k_out, freq, q_norm, k_norm 16 bytes, the strides of q, k,
+ *   q_out, k_out whole multiples of 16 bytes; positions and axis 4 bytes.
+ *   n == 0 or no heads enqueues nothing.
+ */
+typedef struct qmat_rope_args {
+  int32_t in_dtype, out_dtype;
+  int32_t neighbours; /* nonzero: pairs of neighbours, else of halves */
+  int32_t axes;
+  const void *q, *k;
+  void *q_out, *k_out;
+  const int32_t *positions;
+  const double *freq;
+  const int32_t *axis;          /* or NULL */
+  const float *q_norm, *k_norm; /* or NULL */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride, pos_stride;
+  int64_t n, heads, kv_heads, head_dim, rot_dim;
+  double eps;
+} qmat_rope_args;
+
+int qmat_rope(const qmat_rope_args *args, void *stream);
 
 #ifdef __cplusplus
 }

@@ -119,9 +119,100 @@ static void norm_cases() {
   EXPECT(qmat_norm(&x, NULL), QMAT_OK, 1);
 }
 
+static qmat_rope_args rope_good() {
+  qmat_rope_args a = {};
+  a.in_dtype = QMAT_F32;
+  a.out_dtype = QMAT_F16;
+  a.axes = 3;
+  a.q = a.k = A;
+  a.q_out = a.k_out = A;
+  a.positions = a.axis = S;
+  a.freq = (const double*)A;
+  a.q_norm = a.k_norm = (const float*)A;
+  a.q_stride = a.k_stride = a.q_out_stride = a.k_out_stride = 8 * 128;
+  a.pos_stride = 5;
+  a.n = 5;
+  a.heads = 8;
+  a.kv_heads = 2;
+  a.head_dim = a.rot_dim = 128;
+  a.eps = 1e-6;
+  return a;
+}
+
+static void rope_cases() {
+#define ROPE(field, value, want, launches)  \
+  do {                                      \
+    qmat_rope_args x = rope_good();         \
+    x.field = value;                        \
+    EXPECT(qmat_rope(&x, NULL), want, launches); \
+  } while (0)
+  EXPECT(qmat_rope(NULL, NULL), QMAT_E_NULL, 0);
+  ROPE(neighbours, 1, QMAT_OK, 1);
+  ROPE(in_dtype, 3, QMAT_E_DTYPE, 0);
+  ROPE(out_dtype, -1, QMAT_E_DTYPE, 0);
+  ROPE(n, -1, QMAT_E_SHAPE, 0);
+  ROPE(n, big, QMAT_E_SHAPE, 0);
+  ROPE(heads, -1, QMAT_E_SHAPE, 0);
+  ROPE(heads, 1 << 16, QMAT_E_SHAPE, 0);
+  ROPE(kv_heads, -1, QMAT_E_SHAPE, 0);
+  ROPE(kv_heads, INT64_MAX, QMAT_E_SHAPE, 0);
+  ROPE(head_dim, 0, QMAT_E_SHAPE, 0);
+  ROPE(head_dim, 100, QMAT_E_SHAPE, 0);
+  ROPE(head_dim, 520, QMAT_E_SHAPE, 0);
+  ROPE(head_dim, 120, QMAT_E_SHAPE, 0);  // more turned elements than there are
+  ROPE(rot_dim, -8, QMAT_E_SHAPE, 0);
+  ROPE(rot_dim, 100, QMAT_E_SHAPE, 0);
+  ROPE(rot_dim, 136, QMAT_E_SHAPE, 0);
+  ROPE(axes, 0, QMAT_E_SHAPE, 0);
+  ROPE(axes, 17, QMAT_E_SHAPE, 0);
+  ROPE(pos_stride, 4, QMAT_E_SHAPE, 0);
+  ROPE(pos_stride, INT64_MAX, QMAT_E_SHAPE, 0);
+  ROPE(eps, -1.0, QMAT_E_SHAPE, 0);
+  ROPE(eps, NAN, QMAT_E_SHAPE, 0);
+  ROPE(q_stride, 1023, QMAT_E_SHAPE, 0);
+  ROPE(k_stride, 255, QMAT_E_SHAPE, 0);
+  ROPE(q_out_stride, 0, QMAT_E_SHAPE, 0);
+  ROPE(k_out_stride, INT64_MAX, QMAT_E_SHAPE, 0);
+  ROPE(q, NULL, QMAT_E_NULL, 0);
+  ROPE(k, NULL, QMAT_E_NULL, 0);
+  ROPE(q_out, NULL, QMAT_E_NULL, 0);
+  ROPE(k_out, NULL, QMAT_E_NULL, 0);
+  ROPE(positions, NULL, QMAT_E_NULL, 0);
+  ROPE(freq, NULL, QMAT_E_NULL, 0);
+  ROPE(axis, NULL, QMAT_OK, 1);
+  ROPE(q_norm, NULL, QMAT_OK, 1);
+  ROPE(k_norm, NULL, QMAT_OK, 1);
+  ROPE(q, A + 8, QMAT_E_ALIGN, 0);
+  ROPE(k_out, A + 2, QMAT_E_ALIGN, 0);
+  ROPE(q_stride, 1026, QMAT_E_ALIGN, 0);
+  ROPE(q_out_stride, 1028, QMAT_E_ALIGN, 0);
+  ROPE(positions, (int32_t*)(A + 2), QMAT_E_ALIGN, 0);
+  ROPE(axis, (int32_t*)(A + 1), QMAT_E_ALIGN, 0);
+  ROPE(freq, (const double*)(A + 8), QMAT_E_ALIGN, 0);
+  ROPE(k_norm, (const float*)(A + 4), QMAT_E_ALIGN, 0);
+  ROPE(n, 0, QMAT_OK, 0);
+  qmat_rope_args x = rope_good();
+  x.kv_heads = 0;  // no keys: nothing of them is looked at
+  x.k = NULL;
+  x.k_out = NULL;
+  x.k_stride = x.k_out_stride = 0;
+  EXPECT(qmat_rope(&x, NULL), QMAT_OK, 1);
+  x.heads = 0;
+  EXPECT(qmat_rope(&x, NULL), QMAT_OK, 0);
+  x = rope_good();
+  x.rot_dim = 0;  // norms alone
+  x.positions = x.axis = NULL;
+  x.freq = NULL;
+  EXPECT(qmat_rope(&x, NULL), QMAT_OK, 1);
+  x = rope_good();  // tokens x heads
+  x.n = x.pos_stride = (int64_t)1 << 30;
+  EXPECT(qmat_rope(&x, NULL), QMAT_E_SHAPE, 0);
+}
+
 int main() {
   embed_cases();
   norm_cases();
+  rope_cases();
   if (failures) {
     fprintf(stderr, "%d failures\n", failures);
     return 1;

@@ -16,4 +16,8 @@ hipError_t launch_norm(const qmat_norm_args&, hipStream_t) {
   ++g_launches;
   return hipSuccess;
 }
+hipError_t launch_rope(const qmat_rope_args&, hipStream_t) {
+  ++g_launches;
+  return hipSuccess;
+}
 }  // namespace qmat

@@ -53,3 +53,27 @@ def test_rms_norm_refuses():
         binding.rms_norm(x, w, want="none")
     with pytest.raises(ValueError):
         binding.rms_norm(x[0], w)
+
+
+def test_rope_tables():
+    """The frequencies in 64 bits, and pairs shared out over axes one after the other or in turn."""
+    f = binding.rope_freq(8, base=10000.0, device="cpu")
+    assert f.dtype == torch.float64 and f.tolist() == [1.0, 10000.0 ** -0.25, 10000.0 ** -0.5, 10000.0 ** -0.75]
+    assert binding.rope_axis([1, 2, 3], device="cpu").tolist() == [0, 1, 1, 2, 2, 2]
+    assert binding.rope_axis([3, 2, 1], cycle=True, device="cpu").tolist() == [0, 1, 2, 0, 1, 0]
+    assert binding.rope_axis([], device="cpu").numel() == 0
+    with pytest.raises(ValueError):
+        binding.rope_freq(7, device="cpu")
+    with pytest.raises(ValueError):
+        binding.rope_axis([2, -1], device="cpu")
+
+
+@needs_lib
+def test_rope_refuses():
+    q, pos, freq = torch.zeros(3, 2, 16), torch.zeros(3, dtype=torch.int32), torch.ones(8, dtype=torch.float64)
+    with pytest.raises(TypeError):
+        binding.rope(q, None, pos, freq)
+    with pytest.raises(TypeError):
+        binding.rope(q.double(), None, pos, freq)
+    with pytest.raises(ValueError):
+        binding.rope(q[0], None, pos, freq)
