@@ -57,6 +57,15 @@ class RopeArgs(ctypes.Structure):
                 [("eps", ctypes.c_double)])
 
 
+class PageArgs(ctypes.Structure):
+    """The C struct qmat_page_args."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("kv_len", "keep", "add", "page_table", "free_pages",
+                                                "free_count", "q_start", "slots", "positions",
+                                                "token_seq", "status")] +
+                [(n, ctypes.c_int64) for n in ("n_seqs", "max_tokens", "pages", "page_size",
+                                               "pages_per_seq")])
+
+
 class QmatError(RuntimeError):
     """A non-zero status returned by the C ABI."""
 
@@ -121,6 +130,10 @@ def load_library():
     lib.qmat_norm.restype = i32
     lib.qmat_rope.argtypes = [ctypes.POINTER(RopeArgs), p]
     lib.qmat_rope.restype = i32
+    lib.qmat_page_workspace_bytes.argtypes = [ctypes.POINTER(PageArgs)]
+    lib.qmat_page_workspace_bytes.restype = i64
+    lib.qmat_page_step.argtypes = [ctypes.POINTER(PageArgs), p, i64, p]
+    lib.qmat_page_step.restype = i32
     _lib = lib
     return lib
 
@@ -747,3 +760,67 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, freq:
                  kv_heads, head_dim, 2 * pairs, eps)
     _launch("qmat_rope", load_library().qmat_rope, device, ctypes.byref(a))
     return q_out, k_out
+
+
+def _ints(t: torch.Tensor | None, name: str, n: int, device: torch.device) -> torch.Tensor:
+    """t, n int32 numbers on device; allocated when None."""
+    if t is None:
+        return torch.empty(n, dtype=torch.int32, device=device)
+    _flat(t, name, torch.int32, device)
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} numbers")
+    return t
+
+
+def page_step(kv_len: torch.Tensor, add: torch.Tensor, page_table: torch.Tensor,
+              free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, max_tokens: int,
+              keep: torch.Tensor | None = None, q_start: torch.Tensor | None = None,
+              slots: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+              token_seq: torch.Tensor | None = None, status: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None) -> tuple[torch.Tensor, ...]:
+    """One step's changes of lengths: sequence b keeps the first keep[b] of its kv_len[b] cells (all
+    if keep is None) and adds add[b]; pages it lacks come from the end of the stack
+    free_pages[:free_count], pages it no longer needs go back there. kv_len [seqs],
+    page_table [seqs, pages_per_seq], free_pages [pages of the cache] and free_count [1] (all int32)
+    are updated in place. Returns (q_start [seqs + 1], slots, positions,
+    token_seq [max_tokens each], status [seqs]): what kv_store, rope, attn and lora take;
+    rows behind the last token have slot -1, position 0, sequence -1. status is 0
+    where it was done, 1 where the table row or max_tokens, 2 where the
+    pages do not suffice: such a sequence is left as it was and has no tokens."""
+    device = kv_len.device
+    _gpu(kv_len, "kv_len", torch.int32)
+    n_seqs = kv_len.numel()
+    _ints(add, "add", n_seqs, device)
+    if keep is not None:
+        _ints(keep, "keep", n_seqs, device)
+    _flat(page_table, "page_table", torch.int32, device)
+    if page_table.dim() != 2 or page_table.shape[0] != n_seqs:
+        raise ValueError("page_table must be 2-D [seqs, pages_per_seq]")
+    _flat(free_pages, "free_pages", torch.int32, device)
+    _ints(free_count, "free_count", 1, device)
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    q_start = _ints(q_start, "q_start", n_seqs + 1, device)
+    slots = _ints(slots, "slots", max_tokens, device)
+    positions = _ints(positions, "positions", max_tokens, device)
+    token_seq = _ints(token_seq, "token_seq", max_tokens, device)
+    status = _ints(status, "status", n_seqs, device)
+    a = PageArgs(kv_len.data_ptr(), None if keep is None else keep.data_ptr(), add.data_ptr(),
+                 page_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                 q_start.data_ptr(), slots.data_ptr(), positions.data_ptr(), token_seq.data_ptr(),
+                 status.data_ptr(), n_seqs, max_tokens, free_pages.numel(), page_size,
+                 page_table.shape[1])
+    lib = load_library()
+    ref = ctypes.byref(a)
+    if workspace is None:
+        need = lib.qmat_page_workspace_bytes(ref)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _flat(workspace, "workspace", torch.uint8, device)
+    if workspace is None:
+        _launch("qmat_page_step", lib.qmat_page_step, device, ref, None, 0)
+    else:
+        _launch("qmat_page_step", lib.qmat_page_step, device, ref, workspace.data_ptr(),
+                workspace.numel())
+    return q_start, slots, positions, token_seq, status

@@ -25,7 +25,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["quantize.hip", "gemv.hip", "decode.hip", "gemm.hip", "kv.hip", "attn.hip", "attn_prompt.hip",
-           "embed.hip", "norm.hip", "rope.hip",
+           "embed.hip", "norm.hip", "rope.hip", "pages.hip",
            "qmat_api.cpp", "qmat_kv_api.cpp", "qmat_step_api.cpp"]
 MICRO_SOURCES = ["micro.hip"]
 

@@ -56,6 +56,11 @@ hipError_t launch_norm(const qmat_norm_args& a, hipStream_t stream);
 // Rotary positions of queries and keys (rope.hip).
 hipError_t launch_rope(const qmat_rope_args& a, hipStream_t stream);
 
+// Page table, slots and positions of a step (pages.hip): workspace of
+// page_workspace_bytes() bytes.
+int64_t page_workspace_bytes(const qmat_page_args& a);
+hipError_t launch_page_step(const qmat_page_args& a, void* workspace, hipStream_t stream);
+
 hipError_t launch_gemv(int fmt, const void* blocks, const float* x, float* y, int64_t M,
                        int64_t K, hipStream_t stream);
 

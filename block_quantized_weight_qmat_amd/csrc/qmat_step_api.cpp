@@ -1,7 +1,7 @@
 // qmat_step_api.cpp — the C ABI of a step around the products and the cache
-// (include/qmat.h: qmat_embed, qmat_norm, qmat_rope): every argument is checked
-// on the host before anything is enqueued; embed.hip, norm.hip and rope.hip
-// launch the kernels.
+// (include/qmat.h: qmat_embed, qmat_norm, qmat_rope, qmat_page_step): every
+// argument is checked on the host before anything is enqueued; embed.hip,
+// norm.hip, rope.hip and pages.hip launch the kernels.
 #include <hip/hip_runtime.h>
 
 #include "qmat.h"
@@ -15,11 +15,32 @@ using namespace qmat;
 constexpr int64_t kMaxNormK = 1LL << 24;
 constexpr int64_t kMaxRopeHeads = 1LL << 16;
 constexpr int64_t kMaxRopeRows = 1LL << 32;  // of all tokens and heads
+constexpr int64_t kMaxTokens = 1LL << 24;    // also sequences
+constexpr int64_t kMaxCells = 1LL << 30;     // of one sequence
 
 // Rows of activations: 16-byte aligned, as is their stride in bytes.
 int check_rows(const void* p, int64_t stride, int64_t size) {
   if (const int rc = check_buf(p); rc != QMAT_OK) return rc;
   return stride * size % 16 == 0 ? QMAT_OK : QMAT_E_ALIGN;
+}
+
+// The sizes of qmat_page_step.
+int check_pages(const qmat_page_args& a) {
+  if (a.n_seqs < 0 || a.n_seqs > kMaxTokens || a.max_tokens < 0 || a.max_tokens > kMaxTokens)
+    return QMAT_E_SHAPE;
+  if (a.page_size <= 0 || a.page_size > kMaxCells || (a.page_size & (a.page_size - 1)) != 0 ||
+      a.pages < 0 || a.pages > kMaxDim / a.page_size || a.pages_per_seq < 0 ||
+      a.pages_per_seq > kMaxCells / a.page_size)
+    return QMAT_E_SHAPE;
+  return QMAT_OK;
+}
+
+// A workspace of workspace_bytes where need bytes are wanted.
+int check_workspace(const void* workspace, int64_t workspace_bytes, int64_t need) {
+  if (workspace_bytes < 0) return QMAT_E_SHAPE;
+  if (need == 0) return QMAT_OK;
+  if (workspace == nullptr || workspace_bytes < need) return QMAT_E_WORKSPACE;
+  return aligned(workspace, 16) ? QMAT_OK : QMAT_E_ALIGN;
 }
 
 }  // namespace
@@ -108,6 +129,41 @@ int qmat_rope(const qmat_rope_args* args, void* stream) {
   }
   if (!aligned(a.q_norm, 16) || !aligned(a.k_norm, 16)) return QMAT_E_ALIGN;
   return hip_status(launch_rope(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qmat_page_workspace_bytes(const qmat_page_args* args) {
+  if (args == nullptr || check_pages(*args) != QMAT_OK) return -1;
+  return page_workspace_bytes(*args);
+}
+
+int qmat_page_step(const qmat_page_args* args, void* workspace, int64_t workspace_bytes,
+                   void* stream) {
+  if (args == nullptr) return QMAT_E_NULL;
+  const qmat_page_args& a = *args;
+  int rc = check_pages(a);
+  if (rc != QMAT_OK) return rc;
+  const bool seqs = a.n_seqs > 0;
+  struct {
+    const int32_t* p;
+    bool needed;
+  } const all[] = {{a.free_count, true},
+                   {a.q_start, true},
+                   {a.kv_len, seqs},
+                   {a.add, seqs},
+                   {a.status, seqs},
+                   {a.page_table, seqs && a.pages_per_seq > 0},
+                   {a.free_pages, a.pages > 0},
+                   {a.slots, a.max_tokens > 0},
+                   {a.keep, false},
+                   {a.positions, false},
+                   {a.token_seq, false}};
+  for (const auto& x : all) {
+    if (x.p == nullptr && x.needed) return QMAT_E_NULL;
+    if (!aligned(x.p, 4)) return QMAT_E_ALIGN;
+  }
+  rc = check_workspace(workspace, workspace_bytes, page_workspace_bytes(a));
+  if (rc != QMAT_OK) return rc;
+  return hip_status(launch_page_step(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

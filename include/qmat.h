@@ -1,7 +1,7 @@
 /*
  * qmat.h — C ABI of the block-quantized weight matmul for MI355X (gfx950).
  *
- * Twelve operations, all enqueued asynchronously on a caller-supplied HIP
+ * Thirteen operations, all enqueued asynchronously on a caller-supplied HIP
  * stream:
  *   qmat_quantize  fp32 matrix  -> packed weight (or activation) blocks
  *   qmat_gemv      packed W × fp32 x        -> fp32 y        (decode)
@@ -15,6 +15,7 @@
  *   qmat_embed     named rows of a packed matrix -> fp32 / fp16 / bf16 rows
  *   qmat_norm      residual sum and RMS norm -> rows and / or Q8_0 blocks
  *   qmat_rope      rotary positions of queries and keys, of several axes
+ *   qmat_page_step page tables, slots and positions from request lengths
  * and qmat_prefill_noalloc, qmat_prefill without a caller workspace for
  * callers that cannot allocate device memory.
  *
@@ -126,9 +127,8 @@ typedef enum qmat_status {
   QMAT_E_ALIGN = 5, /* a pointer is not 16-byte aligned                   */
   QMAT_E_SCRATCH = 6, /* qmat_prefill_noalloc: the activation workspace it
                         needs exceeds its static scratch                   */
-  QMAT_E_WORKSPACE = 7, /* qmat_gemm_ws, qmat_attn: workspace NULL or smaller
-                           than qmat_gemm_workspace_bytes() /
-                           qmat_attn_workspace_bytes()                     */
+  QMAT_E_WORKSPACE = 7, /* workspace NULL or smaller than the call's
+                           *_workspace_bytes()                             */
   QMAT_E_DTYPE = 8      /* unknown element type                            */
 } qmat_status;
 
@@ -629,6 +629,78 @@ typedef struct qmat_rope_args {
 } qmat_rope_args;
 
 int qmat_rope(const qmat_rope_args *args, void *stream);
+
+/*
+ * qmat_page_step — the page table, the slots and the positions of a step,
+ *   built on the device from the requests' lengths: what qmat_kv_store,
+ *   qmat_rope, qmat_attn and qmat_lora take. Sequence b holds kv_len[b] cells
+ *   in the first ceil(kv_len[b] / page_size) pages of its row of page_table.
+ *   A step keeps the first keep[b] of them (all, where keep is NULL) and adds
+ *   add[b] cells:
+ *     kept = min(keep[b], kv_len[b]), goal = kept + add[b],
+ *     old = ceil(kv_len[b] / page_size), new = ceil(goal / page_size).
+ *   Its pages from new on go back to the free stack (old > new), or new - old
+ *   pages come from it. add = 0 and keep = 0 ends a sequence; keep = accepted
+ *   and add = drafted takes back turned-down tokens and adds the next ones.
+ *
+ *   The free stack: free_pages[0 .. free_count - 1], page numbers, the next one
+ *   last. All pages given back in a call are pushed first, as if from the last
+ *   one to the first in the order of (sequence, page), and may be taken in the
+ *   same call; pages are taken from the end in that order. So a step whose
+ *   tokens are taken back leaves the stack as it was.
+ *
+ *   A sequence that does not fit is left as it was and has no tokens in this
+ *   step: status[b] = 1 where goal exceeds its table row, or where the tokens
+ *   that sequences 0..b ask for exceed max_tokens (and it adds any); else
+ *   status[b] = 2 where the pages that sequences 0..b ask for (those of status 1
+ *   excepted) exceed the free ones (and it needs any): whoever comes first is
+ *   served first, and a large one that waits is not overtaken by later ones
+ *   that need pages. status[b] = 0: done.
+ *
+ *   Outputs: kv_len[b] = goal (in place); the pages taken in page_table;
+ *   free_pages and free_count[0] updated; q_start[n_seqs + 1], the prefix sum of the
+ *   tokens added; for token t of sequence b, at position p: slots[t] =
+ *   page_table[b][p / page_size] * page_size + p % page_size, positions[t] = p,
+ *   token_seq[t] = b. Rows behind the last token get slot -1 (which
+ *   qmat_kv_store skips), position 0 and sequence -1.
+ *
+ *   All pointers are DEVICE pointers, 4-byte aligned (keep, positions and token_seq
+ *   may be NULL; slots may be when max_tokens is 0, page_table when pages_per_seq is 0,
+ *   free_pages when pages is 0, the arrays of sequences when n_seqs is 0). free_pages
+ *   has room for pages numbers.
+ *   Values outside their range do no harm: kv_len[b] counts as cut to [0,
+ *   pages_per_seq * page_size], keep[b] and add[b] as at least 0, free_count[0] as
+ *   cut to [0, pages]; what is pushed past pages is dropped; a page number
+ *   outside [0, pages) gives slot -1.
+ *   Limits (QMAT_E_SHAPE): page_size a power of two; pages * page_size <=
+ *   2^31 - 1; pages_per_seq * page_size <= 2^30; n_seqs, max_tokens <= 2^24.
+ *   Without sequences the rows are those behind the last token.
+ *   Many sequences or tokens take two kernels, and the workspace holds what the
+ *   second needs of the first;
+ *   calls that share one must not overlap in time, and neither may calls that
+ *   share any of the updated arrays.
+ */
+typedef struct qmat_page_args {
+  int32_t *kv_len;       /* [n_seqs], updated               */
+  const int32_t *keep;   /* [n_seqs] or NULL                */
+  const int32_t *add;    /* [n_seqs]                        */
+  int32_t *page_table;   /* [n_seqs][pages_per_seq], updated */
+  int32_t *free_pages;   /* [pages], updated                */
+  int32_t *free_count;   /* [1], updated                    */
+  int32_t *q_start;      /* [n_seqs + 1]                    */
+  int32_t *slots;        /* [max_tokens]                    */
+  int32_t *positions;    /* [max_tokens] or NULL            */
+  int32_t *token_seq;    /* [max_tokens] or NULL            */
+  int32_t *status;       /* [n_seqs]                        */
+  int64_t n_seqs, max_tokens, pages, page_size, pages_per_seq;
+} qmat_page_args;
+
+/* Bytes of device workspace for these sizes (0: none); -1 for sizes that
+ * qmat_page_step rejects. */
+int64_t qmat_page_workspace_bytes(const qmat_page_args *args);
+
+int qmat_page_step(const qmat_page_args *args, void *workspace, int64_t workspace_bytes,
+                   void *stream);
 
 #ifdef __cplusplus
 }

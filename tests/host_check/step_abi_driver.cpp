@@ -209,10 +209,85 @@ static void rope_cases() {
   EXPECT(qmat_rope(&x, NULL), QMAT_E_SHAPE, 0);
 }
 
+static qmat_page_args pages_good() {
+  qmat_page_args a = {};
+  a.kv_len = a.page_table = a.free_pages = a.free_count = a.q_start = S;
+  a.keep = a.add = S;
+  a.slots = a.positions = a.token_seq = a.status = S;
+  a.n_seqs = 4;
+  a.max_tokens = 10;
+  a.pages = 100;
+  a.page_size = 16;
+  a.pages_per_seq = 8;
+  return a;
+}
+
+static void page_cases() {
+#define PAGES(field, value, want, launches)  \
+  do {                                       \
+    qmat_page_args x = pages_good();         \
+    x.field = value;                         \
+    EXPECT(qmat_page_step(&x, NULL, 0, NULL), want, launches); \
+    if (want == QMAT_E_SHAPE && qmat_page_workspace_bytes(&x) != -1) ++failures; \
+  } while (0)
+  EXPECT(qmat_page_step(NULL, NULL, 0, NULL), QMAT_E_NULL, 0);
+  if (qmat_page_workspace_bytes(NULL) != -1) ++failures;
+  int32_t* const odd = (int32_t*)(A + 2);
+  PAGES(pages, 99, QMAT_OK, 1);
+  PAGES(n_seqs, -1, QMAT_E_SHAPE, 0);
+  PAGES(n_seqs, ((int64_t)1 << 24) + 1, QMAT_E_SHAPE, 0);
+  PAGES(max_tokens, -1, QMAT_E_SHAPE, 0);
+  PAGES(max_tokens, ((int64_t)1 << 24) + 1, QMAT_E_SHAPE, 0);
+  PAGES(page_size, 0, QMAT_E_SHAPE, 0);
+  PAGES(page_size, 24, QMAT_E_SHAPE, 0);
+  PAGES(page_size, big, QMAT_E_SHAPE, 0);
+  PAGES(page_size, -16, QMAT_E_SHAPE, 0);
+  PAGES(pages, -1, QMAT_E_SHAPE, 0);
+  PAGES(pages, big / 16, QMAT_E_SHAPE, 0);  // cells past 31 bits
+  PAGES(pages_per_seq, -1, QMAT_E_SHAPE, 0);
+  PAGES(pages_per_seq, ((int64_t)1 << 26) + 1, QMAT_E_SHAPE, 0);
+  PAGES(kv_len, NULL, QMAT_E_NULL, 0);
+  PAGES(add, NULL, QMAT_E_NULL, 0);
+  PAGES(free_count, NULL, QMAT_E_NULL, 0);
+  PAGES(q_start, NULL, QMAT_E_NULL, 0);
+  PAGES(status, NULL, QMAT_E_NULL, 0);
+  PAGES(page_table, NULL, QMAT_E_NULL, 0);
+  PAGES(free_pages, NULL, QMAT_E_NULL, 0);
+  PAGES(slots, NULL, QMAT_E_NULL, 0);
+  PAGES(keep, NULL, QMAT_OK, 1);
+  PAGES(positions, NULL, QMAT_OK, 1);
+  PAGES(token_seq, NULL, QMAT_OK, 1);
+  PAGES(kv_len, odd, QMAT_E_ALIGN, 0);
+  PAGES(keep, odd, QMAT_E_ALIGN, 0);
+  PAGES(page_table, odd, QMAT_E_ALIGN, 0);
+  PAGES(free_pages, odd, QMAT_E_ALIGN, 0);
+  PAGES(slots, odd, QMAT_E_ALIGN, 0);
+  PAGES(token_seq, odd, QMAT_E_ALIGN, 0);
+  PAGES(n_seqs, 0, QMAT_OK, 1);
+  qmat_page_args x = pages_good();  // no sequences
+  x.n_seqs = 0;
+  x.kv_len = x.page_table = x.status = NULL;
+  x.add = x.keep = NULL;
+  EXPECT(qmat_page_step(&x, NULL, 0, NULL), QMAT_OK, 1);
+  x = pages_good();  // no rows, no pages, no table
+  x.max_tokens = x.pages = x.pages_per_seq = 0;
+  x.slots = x.positions = x.token_seq = x.free_pages = x.page_table = NULL;
+  EXPECT(qmat_page_step(&x, NULL, 0, NULL), QMAT_OK, 1);
+  x = pages_good();
+  x.max_tokens = 2000;  // the stub wants 4096 bytes
+  if (qmat_page_workspace_bytes(&x) != 4096) ++failures;
+  EXPECT(qmat_page_step(&x, NULL, 4096, NULL), QMAT_E_WORKSPACE, 0);
+  EXPECT(qmat_page_step(&x, A, 4095, NULL), QMAT_E_WORKSPACE, 0);
+  EXPECT(qmat_page_step(&x, A, -1, NULL), QMAT_E_SHAPE, 0);
+  EXPECT(qmat_page_step(&x, A + 8, 4096, NULL), QMAT_E_ALIGN, 0);
+  EXPECT(qmat_page_step(&x, A, 4096, NULL), QMAT_OK, 1);
+}
+
 int main() {
   embed_cases();
   norm_cases();
   rope_cases();
+  page_cases();
   if (failures) {
     fprintf(stderr, "%d failures\n", failures);
     return 1;

@@ -77,3 +77,20 @@ def test_rope_refuses():
         binding.rope(q.double(), None, pos, freq)
     with pytest.raises(ValueError):
         binding.rope(q[0], None, pos, freq)
+
+
+@needs_lib
+def test_page_step_refuses():
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        binding.page_step(i, i, i.view(2, 1), i, i[:1], 16, 4)
+    with pytest.raises(TypeError):
+        binding.page_step(i.long(), i, i.view(2, 1), i, i[:1], 16, 4)
+
+
+def test_structs_have_the_headers_sizes():
+    """Fields of 8 bytes follow each other without gaps; the 32-bit ones come first."""
+    import ctypes
+    assert ctypes.sizeof(binding.NormArgs) == 8 + 6 * 8 + 6 * 8 + 8
+    assert ctypes.sizeof(binding.RopeArgs) == 4 * 4 + 9 * 8 + 10 * 8 + 8
+    assert ctypes.sizeof(binding.PageArgs) == 11 * 8 + 5 * 8
