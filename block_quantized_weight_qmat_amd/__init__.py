@@ -10,6 +10,7 @@ from __future__ import annotations
 __all__ = ["quantize", "gemv", "gemv_batch", "gemv_jobs", "gemm", "gemm_ws", "gemm_workspace_bytes", "prefill", "prefill_noalloc", "kv_write",
            "kv_store", "kv_load", "attn", "attn_args", "attn_workspace_bytes", "embed", "rms_norm",
            "rope", "rope_freq", "rope_axis", "page_step",
+           "lora",
            "block_elems", "block_bytes", "row_bytes", "noalloc_scratch_bytes",
            "Q4_0", "Q8_0", "Q4_K", "Q6_K", "FORMATS", "QmatError", "library_path"]
 

@@ -66,6 +66,15 @@ class PageArgs(ctypes.Structure):
                                                "pages_per_seq")])
 
 
+class LoraArgs(ctypes.Structure):
+    """The C struct qmat_lora_args."""
+    _fields_ = ([("dtype", ctypes.c_int32)] +
+                [(n, ctypes.c_void_p) for n in ("x_q8", "a", "b", "scale", "ranks", "adapter",
+                                                "q_start", "base", "y")] +
+                [(n, ctypes.c_int64) for n in ("base_stride", "y_stride", "n_tokens", "n_seqs",
+                                               "n_adapters", "rank", "M", "K", "max_q")])
+
+
 class QmatError(RuntimeError):
     """A non-zero status returned by the C ABI."""
 
@@ -134,6 +143,10 @@ def load_library():
     lib.qmat_page_workspace_bytes.restype = i64
     lib.qmat_page_step.argtypes = [ctypes.POINTER(PageArgs), p, i64, p]
     lib.qmat_page_step.restype = i32
+    lib.qmat_lora_workspace_bytes.argtypes = [ctypes.POINTER(LoraArgs)]
+    lib.qmat_lora_workspace_bytes.restype = i64
+    lib.qmat_lora.argtypes = [ctypes.POINTER(LoraArgs), p, i64, p]
+    lib.qmat_lora.restype = i32
     _lib = lib
     return lib
 
@@ -824,3 +837,59 @@ def page_step(kv_len: torch.Tensor, add: torch.Tensor, page_table: torch.Tensor,
         _launch("qmat_page_step", lib.qmat_page_step, device, ref, workspace.data_ptr(),
                 workspace.numel())
     return q_start, slots, positions, token_seq, status
+
+
+def lora(x_q8: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: torch.Tensor,
+         q_start: torch.Tensor, y: torch.Tensor, base: torch.Tensor | None = None,
+         scale: torch.Tensor | None = None, ranks: torch.Tensor | None = None,
+         max_q: int | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = base + scale * b (a x) with every request's own adapter: x_q8 the Q8_0
+    rows that gemm takes (uint8 [tokens, row_bytes]), a [adapters, rank, K] and
+    b [adapters, M, rank] (fp16 or bf16), y and base fp32 [tokens, M], rows any stride
+    apart (base is y, gemm's product, if None). adapter [seqs] and q_start
+    [seqs + 1] (int32): tokens q_start[i] .. q_start[i + 1] - 1 have adapter[i];
+    one outside the adapters: base alone. scale [adapters] (fp32; 1 if None),
+    ranks [adapters] (int32; rank if None). max_q: the most tokens of a sequence
+    (all tokens if None; give 1 for decode). A workspace of
+    qmat_lora_workspace_bytes() is allocated when none is given."""
+    device = y.device
+    dt = _dtype(a.dtype)
+    if dt == 0:
+        raise TypeError("adapters are torch.float16 or torch.bfloat16")
+    ys = _rows(y, "y", torch.float32)
+    bs, bp = (ys, y.data_ptr()) if base is None else (_same(base, "base", y), base.data_ptr())
+    _flat(a, "a", a.dtype, device)
+    _flat(b, "b", a.dtype, device)
+    _flat(x_q8, "x_q8", torch.uint8, device)
+    _flat(adapter, "adapter", torch.int32, device)
+    _flat(q_start, "q_start", torch.int32, device)
+    if y.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("y must be [tokens, M], a [adapters, rank, K], b [adapters, M, rank]")
+    (n, M), (adapters, rank, K), seqs = y.shape, a.shape, adapter.numel()
+    if K % 32 != 0 or x_q8.numel() != n * (K // 32 * 34):
+        raise ValueError("x_q8 must hold a Q8_0 row of K elements for each token")
+    if b.shape != (adapters, M, rank) or q_start.numel() != seqs + 1:
+        raise ValueError("a, b, y or adapter, q_start do not match")
+    for t, name, dtype in ((scale, "scale", torch.float32), (ranks, "ranks", torch.int32)):
+        if t is not None:
+            _flat(t, name, dtype, device)
+            if t.numel() != adapters:
+                raise ValueError(f"{name} must hold a number for each adapter")
+    args = LoraArgs(dt, x_q8.data_ptr(), a.data_ptr(), b.data_ptr(),
+                    None if scale is None else scale.data_ptr(),
+                    None if ranks is None else ranks.data_ptr(), adapter.data_ptr(),
+                    q_start.data_ptr(), bp, y.data_ptr(), bs, ys, n, seqs, adapters, rank, M, K,
+                    n if max_q is None else max_q)
+    lib = load_library()
+    ref = ctypes.byref(args)
+    if workspace is None:
+        need = lib.qmat_lora_workspace_bytes(ref)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _flat(workspace, "workspace", torch.uint8, device)
+    if workspace is None:
+        _launch("qmat_lora", lib.qmat_lora, device, ref, None, 0)
+    else:
+        _launch("qmat_lora", lib.qmat_lora, device, ref, workspace.data_ptr(), workspace.numel())
+    return y

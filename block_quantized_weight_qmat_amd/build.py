@@ -26,7 +26,7 @@ ARCH = "gfx950"
 
 SOURCES = ["quantize.hip", "gemv.hip", "decode.hip", "gemm.hip", "kv.hip", "attn.hip", "attn_prompt.hip",
            "embed.hip", "norm.hip", "rope.hip", "pages.hip",
-           "qmat_api.cpp", "qmat_kv_api.cpp", "qmat_step_api.cpp"]
+           "lora.hip", "qmat_api.cpp", "qmat_kv_api.cpp", "qmat_step_api.cpp"]
 MICRO_SOURCES = ["micro.hip"]
 
 CFLAGS = [

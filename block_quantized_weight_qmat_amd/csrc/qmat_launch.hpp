@@ -61,6 +61,11 @@ hipError_t launch_rope(const qmat_rope_args& a, hipStream_t stream);
 int64_t page_workspace_bytes(const qmat_page_args& a);
 hipError_t launch_page_step(const qmat_page_args& a, void* workspace, hipStream_t stream);
 
+// Low-rank adapters added to a shared product (lora.hip): workspace of
+// lora_workspace_bytes() bytes.
+int64_t lora_workspace_bytes(const qmat_lora_args& a);
+hipError_t launch_lora(const qmat_lora_args& a, void* workspace, hipStream_t stream);
+
 hipError_t launch_gemv(int fmt, const void* blocks, const float* x, float* y, int64_t M,
                        int64_t K, hipStream_t stream);
 

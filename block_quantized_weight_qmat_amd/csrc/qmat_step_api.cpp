@@ -1,7 +1,8 @@
 // qmat_step_api.cpp — the C ABI of a step around the products and the cache
-// (include/qmat.h: qmat_embed, qmat_norm, qmat_rope, qmat_page_step): every
-// argument is checked on the host before anything is enqueued; embed.hip,
-// norm.hip, rope.hip and pages.hip launch the kernels.
+// (include/qmat.h: qmat_embed, qmat_norm, qmat_rope, qmat_page_step,
+// qmat_lora): every argument is checked on the host before anything is
+// enqueued; embed.hip, norm.hip, rope.hip, pages.hip and lora.hip launch the
+// kernels.
 #include <hip/hip_runtime.h>
 
 #include "qmat.h"
@@ -12,7 +13,7 @@ namespace {
 
 using namespace qmat;
 
-constexpr int64_t kMaxNormK = 1LL << 24;
+constexpr int64_t kMaxK = 1LL << 24;
 constexpr int64_t kMaxRopeHeads = 1LL << 16;
 constexpr int64_t kMaxRopeRows = 1LL << 32;  // of all tokens and heads
 constexpr int64_t kMaxTokens = 1LL << 24;    // also sequences
@@ -22,6 +23,24 @@ constexpr int64_t kMaxCells = 1LL << 30;     // of one sequence
 int check_rows(const void* p, int64_t stride, int64_t size) {
   if (const int rc = check_buf(p); rc != QMAT_OK) return rc;
   return stride * size % 16 == 0 ? QMAT_OK : QMAT_E_ALIGN;
+}
+
+constexpr int64_t kMaxLoraTokens = 1LL << 20;
+constexpr int64_t kMaxLoraRows = 1LL << 23;
+constexpr int64_t kMaxLoraRank = 256;
+
+// The host values of qmat_lora.
+int check_lora(const qmat_lora_args& a) {
+  if (a.dtype != QMAT_F16 && a.dtype != QMAT_BF16) return QMAT_E_DTYPE;
+  if (a.n_tokens < 0 || a.n_tokens > kMaxLoraTokens || a.n_seqs < 0 || a.n_seqs > kMaxTokens ||
+      a.n_adapters < 0 || a.n_adapters > kMaxTokens || a.M < 0 || a.M > kMaxLoraRows || a.max_q < 0)
+    return QMAT_E_SHAPE;
+  if (a.K < 0 || a.K > kMaxK || a.K % 32 != 0 || a.rank < 8 || a.rank > kMaxLoraRank ||
+      a.rank % 8 != 0)
+    return QMAT_E_SHAPE;
+  if (!rows_ok(a.n_tokens, a.M, a.base_stride, 4) || !rows_ok(a.n_tokens, a.M, a.y_stride, 4))
+    return QMAT_E_SHAPE;
+  return QMAT_OK;
 }
 
 // The sizes of qmat_page_step.
@@ -70,7 +89,7 @@ int qmat_norm(const qmat_norm_args* args, void* stream) {
   if (args == nullptr) return QMAT_E_NULL;
   const qmat_norm_args& a = *args;
   if (!dtype_ok(a.dtype)) return QMAT_E_DTYPE;
-  if (a.n < 0 || a.n > kMaxDim || a.K < 0 || a.K > kMaxNormK || a.K % 32 != 0) return QMAT_E_SHAPE;
+  if (a.n < 0 || a.n > kMaxDim || a.K < 0 || a.K > kMaxK || a.K % 32 != 0) return QMAT_E_SHAPE;
   if (!is_finite(a.eps) || a.eps < 0) return QMAT_E_SHAPE;
   const int64_t size = dtype_bytes(a.dtype);
   const bool sum = a.residual != nullptr || a.residual_out != nullptr;
@@ -164,6 +183,40 @@ int qmat_page_step(const qmat_page_args* args, void* workspace, int64_t workspac
   rc = check_workspace(workspace, workspace_bytes, page_workspace_bytes(a));
   if (rc != QMAT_OK) return rc;
   return hip_status(launch_page_step(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qmat_lora_workspace_bytes(const qmat_lora_args* args) {
+  if (args == nullptr || check_lora(*args) != QMAT_OK) return -1;
+  return lora_workspace_bytes(*args);
+}
+
+int qmat_lora(const qmat_lora_args* args, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (args == nullptr) return QMAT_E_NULL;
+  const qmat_lora_args& a = *args;
+  int rc = check_lora(a);
+  if (rc != QMAT_OK) return rc;
+  if (a.n_tokens == 0 || a.M == 0) return QMAT_OK;
+  const bool any = a.n_adapters > 0;
+  struct {
+    const void* p;
+    uintptr_t to;
+    bool needed;
+  } const all[] = {{a.y, 16, true},
+                   {a.base, 16, true},
+                   {a.x_q8, 16, any && a.K > 0},
+                   {a.a, 16, any && a.K > 0},
+                   {a.b, 16, any},
+                   {a.adapter, 4, a.n_seqs > 0},
+                   {a.q_start, 4, a.n_seqs > 0},
+                   {a.scale, 4, false},
+                   {a.ranks, 4, false}};
+  for (const auto& x : all) {
+    if (x.p == nullptr && x.needed) return QMAT_E_NULL;
+    if (!aligned(x.p, x.to)) return QMAT_E_ALIGN;
+  }
+  rc = check_workspace(workspace, workspace_bytes, lora_workspace_bytes(a));
+  if (rc != QMAT_OK) return rc;
+  return hip_status(launch_lora(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

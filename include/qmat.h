@@ -1,7 +1,7 @@
 /*
  * qmat.h — C ABI of the block-quantized weight matmul for MI355X (gfx950).
  *
- * Thirteen operations, all enqueued asynchronously on a caller-supplied HIP
+ * Fourteen operations, all enqueued asynchronously on a caller-supplied HIP
  * stream:
  *   qmat_quantize  fp32 matrix  -> packed weight (or activation) blocks
  *   qmat_gemv      packed W × fp32 x        -> fp32 y        (decode)
@@ -16,6 +16,7 @@
  *   qmat_norm      residual sum and RMS norm -> rows and / or Q8_0 blocks
  *   qmat_rope      rotary positions of queries and keys, of several axes
  *   qmat_page_step page tables, slots and positions from request lengths
+ *   qmat_lora      requests' low-rank adapters added to a shared product
  * and qmat_prefill_noalloc, qmat_prefill without a caller workspace for
  * callers that cannot allocate device memory.
  *
@@ -133,7 +134,7 @@ typedef enum qmat_status {
 } qmat_status;
 
 /* Element type of the activations of qmat_kv_store, qmat_kv_load, qmat_attn,
- * qmat_embed, qmat_norm, qmat_rope. */
+ * qmat_embed, qmat_norm, qmat_rope; of the adapters of qmat_lora (not fp32). */
 typedef enum qmat_dtype { QMAT_F32 = 0, QMAT_F16 = 1, QMAT_BF16 = 2 } qmat_dtype;
 
 /* Bytes of the static device workspace of qmat_prefill_noalloc (16 MiB):
@@ -701,6 +702,63 @@ int64_t qmat_page_workspace_bytes(const qmat_page_args *args);
 
 int qmat_page_step(const qmat_page_args *args, void *workspace, int64_t workspace_bytes,
                    void *stream);
+
+/*
+ * qmat_lora — the low-rank adapters of many requests, added to the product of
+ *   all of them with a shared weight matrix (qmat_gemm's Y):
+ *     y[t][m] = base[t][m] + s_a * sum_{r < R_a} b[a][m][r] *
+ *               (sum_k a[a][r][k] dequant(x_q8)[t][k]),
+ *   a = adapter[b] for the tokens q_start[b] .. q_start[b+1] - 1 of sequence b,
+ *   s_a = scale[a] (1 where scale is NULL), R_a = ranks[a] (rank where NULL, cut to
+ *   [0, rank]); rows of a and columns of b from R_a on have no effect. Tokens
+ *   of an adapter outside [0, n_adapters) or of rank 0 and tokens of no
+ *   sequence get base.
+ *   x_q8: the Q8_0 rows [n_tokens][K] that qmat_gemm takes.
+ *   a: [n_adapters][rank][K], b: [n_adapters][M][rank], of dtype (QMAT_F16 or
+ *     QMAT_BF16). scale: fp32, ranks: int32, both DEVICE [n_adapters].
+ *   adapter: DEVICE int32 [n_seqs]; q_start: DEVICE int32 [n_seqs + 1], not
+ *     decreasing. Values outside [0, n_tokens] name no token.
+ *   y, base: fp32 rows [n_tokens][M], strides in elements (>= M). base may be
+ *     y itself with the same stride: then only tokens with an adapter are touched.
+ *   Arithmetic: products of a code and an element of a are exact, a block's
+ *   sum is scaled and added in fp32; the second product is fp32. Other
+ *   requests' adapters and activations have no effect on a token, whatever
+ *   their values (infinities and NaN included).
+ *   Limits (QMAT_E_SHAPE): K a multiple of 32, up to 2^24; rank a multiple of
+ *   8, 8 to 256; n_tokens up to 2^20, M up to 2^23, n_seqs and n_adapters up to
+ *   2^24; max_q >= 0.
+ *   max_q: no sequence has more tokens. An estimate: it chooses how the work is
+ *   divided (1 for decode), and with it the order of a sum's last bits.
+ *   Alignment: x_q8, a, b, y, base 16 bytes; scale, ranks, adapter, q_start 4.
+ *   x_q8, a and b may be NULL when there are no adapters or K is 0 (b: no
+ *   adapters), adapter and q_start when there are no sequences. n_tokens == 0
+ *   or M == 0 enqueues nothing.
+ */
+typedef struct qmat_lora_args {
+  int32_t dtype;
+  const void *x_q8;
+  const void *a, *b;
+  const float *scale;     /* or NULL */
+  const int32_t *ranks;   /* or NULL */
+  const int32_t *adapter;
+  const int32_t *q_start;
+  const float *base;
+  float *y;
+  int64_t base_stride, y_stride;
+  int64_t n_tokens, n_seqs, n_adapters, rank, M, K, max_q;
+} qmat_lora_args;
+
+/* Bytes of device workspace that qmat_lora needs for these host values; -1
+ * for values that it rejects. */
+int64_t qmat_lora_workspace_bytes(const qmat_lora_args *args);
+
+/* Errors of the four calls with a struct: QMAT_E_NULL for args NULL,
+ * QMAT_E_DTYPE, QMAT_E_SHAPE; nothing to do: QMAT_OK; QMAT_E_NULL and
+ * QMAT_E_ALIGN for the buffers; then QMAT_E_SHAPE for workspace_bytes < 0,
+ * QMAT_E_WORKSPACE, QMAT_E_ALIGN for a workspace that is not 16-byte aligned.
+ * The structs are HOST memory, read during the call only. */
+int qmat_lora(const qmat_lora_args *args, void *workspace, int64_t workspace_bytes,
+              void *stream);
 
 #ifdef __cplusplus
 }

@@ -5,6 +5,9 @@
 #include <math.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
+#include "lora_plan.hpp"
 #include "qmat.h"
 
 extern int g_launches;
@@ -283,11 +286,130 @@ static void page_cases() {
   EXPECT(qmat_page_step(&x, A, 4096, NULL), QMAT_OK, 1);
 }
 
+static qmat_lora_args lora_good() {
+  qmat_lora_args a = {};
+  a.dtype = QMAT_BF16;
+  a.x_q8 = a.a = a.b = A;
+  a.scale = a.base = (const float*)A;
+  a.y = (float*)A;
+  a.ranks = a.adapter = a.q_start = S;
+  a.base_stride = a.y_stride = 100;
+  a.n_tokens = 5;
+  a.n_seqs = 3;
+  a.n_adapters = 2;
+  a.rank = 16;
+  a.M = 100;
+  a.K = 256;
+  a.max_q = 3;
+  return a;
+}
+
+static int lora(const qmat_lora_args& a) {
+  const int64_t n = qmat_lora_workspace_bytes(&a);
+  return qmat_lora(&a, A, n < 0 ? 0 : n, NULL);
+}
+
+static void lora_cases() {
+#define LORA(field, value, want, launches)  \
+  do {                                      \
+    qmat_lora_args x = lora_good();         \
+    x.field = value;                        \
+    EXPECT(lora(x), want, launches);        \
+    if (want == QMAT_E_SHAPE && qmat_lora_workspace_bytes(&x) != -1) ++failures; \
+  } while (0)
+  EXPECT(qmat_lora(NULL, NULL, 0, NULL), QMAT_E_NULL, 0);
+  if (qmat_lora_workspace_bytes(NULL) != -1) ++failures;
+  LORA(max_q, 0, QMAT_OK, 1);
+  LORA(max_q, INT64_MAX, QMAT_OK, 1);
+  LORA(dtype, QMAT_F16, QMAT_OK, 1);
+  LORA(dtype, QMAT_F32, QMAT_E_DTYPE, 0);
+  LORA(dtype, 3, QMAT_E_DTYPE, 0);
+  LORA(n_tokens, -1, QMAT_E_SHAPE, 0);
+  LORA(n_tokens, ((int64_t)1 << 20) + 1, QMAT_E_SHAPE, 0);
+  LORA(n_seqs, -1, QMAT_E_SHAPE, 0);
+  LORA(n_seqs, ((int64_t)1 << 24) + 1, QMAT_E_SHAPE, 0);
+  LORA(n_adapters, -1, QMAT_E_SHAPE, 0);
+  LORA(n_adapters, ((int64_t)1 << 24) + 1, QMAT_E_SHAPE, 0);
+  LORA(rank, 0, QMAT_E_SHAPE, 0);
+  LORA(rank, 12, QMAT_E_SHAPE, 0);
+  LORA(rank, 264, QMAT_E_SHAPE, 0);
+  LORA(M, -1, QMAT_E_SHAPE, 0);
+  LORA(M, 101, QMAT_E_SHAPE, 0);  // strides shorter than a row
+  LORA(M, ((int64_t)1 << 23) + 1, QMAT_E_SHAPE, 0);
+  LORA(K, -32, QMAT_E_SHAPE, 0);
+  LORA(K, 40, QMAT_E_SHAPE, 0);
+  LORA(K, ((int64_t)1 << 24) + 32, QMAT_E_SHAPE, 0);
+  LORA(max_q, -1, QMAT_E_SHAPE, 0);
+  LORA(y_stride, 99, QMAT_E_SHAPE, 0);
+  LORA(base_stride, 0, QMAT_E_SHAPE, 0);
+  LORA(y_stride, INT64_MAX, QMAT_E_SHAPE, 0);
+  LORA(x_q8, NULL, QMAT_E_NULL, 0);
+  LORA(a, NULL, QMAT_E_NULL, 0);
+  LORA(b, NULL, QMAT_E_NULL, 0);
+  LORA(y, NULL, QMAT_E_NULL, 0);
+  LORA(base, NULL, QMAT_E_NULL, 0);
+  LORA(adapter, NULL, QMAT_E_NULL, 0);
+  LORA(q_start, NULL, QMAT_E_NULL, 0);
+  LORA(scale, NULL, QMAT_OK, 1);
+  LORA(ranks, NULL, QMAT_OK, 1);
+  LORA(x_q8, A + 2, QMAT_E_ALIGN, 0);
+  LORA(a, A + 8, QMAT_E_ALIGN, 0);
+  LORA(b, A + 4, QMAT_E_ALIGN, 0);
+  LORA(y, (float*)(A + 4), QMAT_E_ALIGN, 0);
+  LORA(base, (float*)(A + 8), QMAT_E_ALIGN, 0);
+  LORA(scale, (float*)(A + 2), QMAT_E_ALIGN, 0);
+  LORA(q_start, (int32_t*)(A + 2), QMAT_E_ALIGN, 0);
+  LORA(n_tokens, 0, QMAT_OK, 0);
+  LORA(M, 0, QMAT_OK, 0);
+  qmat_lora_args x = lora_good();
+  x.n_adapters = x.n_seqs = 0;  // a copy of base
+  x.x_q8 = x.a = x.b = x.scale = NULL;
+  x.ranks = x.adapter = x.q_start = NULL;
+  EXPECT(lora(x), QMAT_OK, 1);
+  x = lora_good();
+  x.K = 0;
+  x.x_q8 = x.a = NULL;
+  if (qmat_lora_workspace_bytes(&x) != 0) ++failures;
+  EXPECT(qmat_lora(&x, NULL, 0, NULL), QMAT_OK, 1);
+  x = lora_good();
+  const int64_t n = qmat_lora_workspace_bytes(&x);
+  if (n <= 0) ++failures;
+  EXPECT(qmat_lora(&x, NULL, n, NULL), QMAT_E_WORKSPACE, 0);
+  EXPECT(qmat_lora(&x, A, n - 1, NULL), QMAT_E_WORKSPACE, 0);
+  EXPECT(qmat_lora(&x, A, -1, NULL), QMAT_E_SHAPE, 0);
+  EXPECT(qmat_lora(&x, A + 4, n, NULL), QMAT_E_ALIGN, 0);
+  // every plan is within the launches' limits
+  const int64_t sizes[] = {1, 2, 15, 16, 17, 33, 1000, 4097, (int64_t)1 << 20};
+  for (int64_t tokens : sizes)
+    for (int64_t q : sizes)
+      for (int64_t rank : {8, 16, 24, 40, 64, 128, 136, 256})
+        for (int64_t K : {0, 32, 4096, 11008, 1 << 24})
+          for (int64_t adapters : {0, 1, 3, 1 << 24}) {
+            x.n_tokens = tokens;
+            x.max_q = q;
+            x.rank = rank;
+            x.K = K;
+            x.n_adapters = adapters;
+            const qmat::LoraPlan p = qmat::lora_plan(x);
+            const int64_t waves = p.tiles * p.slots * p.groups * p.parts;
+            if (waves * 64 >= (int64_t)1 << 32 || p.slots < 1 || p.slots > 16 ||
+                p.tiles * 16 * p.token_tiles < tokens || p.groups * 16 * p.rank_tiles < rank ||
+                p.z_stride < rank || p.z_stride > 256 || p.parts > K / 32 || (K > 0 && p.parts < 1) ||
+                p.up_rows % 64 != 0 || (((int64_t)1 << 23) + p.up_rows - 1) / p.up_rows > 65535 ||
+                qmat_lora_workspace_bytes(&x) != p.parts * tokens * p.z_stride * 4) {
+              fprintf(stderr, "FAIL plan: %lld tokens, max_q %lld, rank %lld, K %lld\n", (long long)tokens,
+                      (long long)q, (long long)rank, (long long)K);
+              ++failures;
+            }
+          }
+}
+
 int main() {
   embed_cases();
   norm_cases();
   rope_cases();
   page_cases();
+  lora_cases();
   if (failures) {
     fprintf(stderr, "%d failures\n", failures);
     return 1;

@@ -94,3 +94,15 @@ def test_structs_have_the_headers_sizes():
     assert ctypes.sizeof(binding.NormArgs) == 8 + 6 * 8 + 6 * 8 + 8
     assert ctypes.sizeof(binding.RopeArgs) == 4 * 4 + 9 * 8 + 10 * 8 + 8
     assert ctypes.sizeof(binding.PageArgs) == 11 * 8 + 5 * 8
+    assert ctypes.sizeof(binding.LoraArgs) == 8 + 9 * 8 + 9 * 8
+
+
+@needs_lib
+def test_lora_refuses():
+    t = torch.zeros
+    i = t(2, dtype=torch.int32)
+    args = (t(2, 34, dtype=torch.uint8), t(1, 8, 32).half(), t(1, 4, 8).half(), i, t(3, dtype=torch.int32), t(2, 4))
+    with pytest.raises(TypeError):
+        binding.lora(*args)
+    with pytest.raises(TypeError):
+        binding.lora(args[0], args[1].float(), *args[2:])
