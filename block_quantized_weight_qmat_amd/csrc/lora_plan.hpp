@@ -11,39 +11,49 @@ namespace qmat {
 constexpr int64_t kLoraMaxRank = 256;
 
 struct LoraPlan {
-  int64_t tiles;        // of 16 * token_tiles tokens
-  int64_t slots;        // waves that share a tile's adapters
-  int64_t groups;       // of 16 * rank_tiles ranks
-  int64_t parts;        // of K
+  bool few;             // one kernel, a token at a time
+  int64_t few_rows;     // its rows of b of a workgroup
+  int64_t tiles;        // of up to 16 * token_tiles tokens
   int64_t z_stride;     // numbers of z for each token: whole tiles of ranks
-  int64_t up_rows;      // rows of b of a workgroup (many tokens)
+  int64_t up_rows;      // rows of b of a workgroup
+  int32_t up_ranks;     // of z in LDS: whole tiles of 32
+  int32_t groups;       // of 16 * rank_tiles ranks
+  int32_t parts;        // of K
   int32_t token_tiles, rank_tiles;
-  bool few;             // few tokens of a sequence: one row of b a thread
 
-  int64_t bytes(const qmat_lora_args& a) const { return parts * a.n_tokens * z_stride * 4; }
+  int64_t bytes(const qmat_lora_args& a) const { return few ? 0 : parts * a.n_tokens * z_stride * 4; }
 };
+
+// Tiles of up to tile tokens, each of one sequence or of none: the aligned runs
+// of tile tokens, and one more for every cut between sequences (and before the
+// first and behind the last).
+inline int64_t lora_tiles(const qmat_lora_args& a, int64_t tile) {
+  return (a.n_tokens + tile - 1) / tile + (a.n_seqs > 0 ? a.n_seqs + 1 : 0);
+}
 
 inline LoraPlan lora_plan(const qmat_lora_args& a) {
   LoraPlan p{};
-  p.few = a.max_q <= 4;
-  p.token_tiles = p.few ? 1 : 2;
-  p.z_stride = (a.rank + 15) / 16 * 16;
+  const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  const auto cut = [](int64_t v, int64_t lo, int64_t hi) { return (int32_t)(v > hi ? hi > lo ? hi : lo : v < lo ? lo : v); };
+  p.few = a.max_q <= 4 && a.rank * a.K <= 1 << 18;
+  if (p.few) {
+    // a workgroup for each CU, and whole threads of rows
+    const int64_t splits = up(256, a.n_tokens > 0 ? a.n_tokens : 1);
+    p.few_rows = up(up(a.M, splits), 1024) * 1024;
+    return p;
+  }
+  p.token_tiles = a.max_q <= 16 ? 1 : 2;
+  p.z_stride = up(a.rank, 16) * 16;
   const int64_t rank_tiles = p.z_stride / 16;
   p.rank_tiles = rank_tiles >= 3 ? 4 : (int32_t)rank_tiles;
-  p.groups = (rank_tiles + p.rank_tiles - 1) / p.rank_tiles;
-  const int64_t tile = 16 * p.token_tiles;
-  p.tiles = (a.n_tokens + tile - 1) / tile;
-  // as many adapters as a tile of sequences of max_q tokens can have, up to 16
-  const int64_t most = a.max_q < 1 ? tile : tile / a.max_q + 1;
-  p.slots = most > 16 ? 16 : most;
-  if (p.slots > a.n_adapters) p.slots = a.n_adapters > 0 ? a.n_adapters : 1;
-  // K is divided until there are 16 waves for each CU, or 4 blocks of a wave
-  const int64_t blocks = a.K / 32, waves = p.tiles * p.slots * p.groups;
-  int64_t parts = waves > 0 ? 4096 / waves : 1;
-  if (parts > blocks / 4) parts = blocks / 4;
-  if (parts > 64) parts = 64;
-  p.parts = blocks == 0 ? 0 : parts < 1 ? 1 : parts;
-  p.up_rows = 256;
+  p.groups = (int32_t)up(rank_tiles, p.rank_tiles);
+  p.tiles = lora_tiles(a, 16 * p.token_tiles);
+  // K is divided until there are two workgroups for each CU, or two blocks for
+  // each wave
+  const int64_t blocks = a.K / 32, wgs = p.tiles * p.groups;
+  p.parts = blocks == 0 ? 0 : cut(wgs > 0 ? 512 / wgs : 1, 1, blocks / 16);
+  p.up_ranks = (int32_t)up(a.rank, 32) * 32;
+  p.up_rows = 512;
   return p;
 }
 

@@ -25,20 +25,23 @@ int check_rows(const void* p, int64_t stride, int64_t size) {
   return stride * size % 16 == 0 ? QMAT_OK : QMAT_E_ALIGN;
 }
 
-constexpr int64_t kMaxLoraTokens = 1LL << 20;
+constexpr int64_t kMaxLoraTokens = 1LL << 20;  // also sequences
 constexpr int64_t kMaxLoraRows = 1LL << 23;
 constexpr int64_t kMaxLoraRank = 256;
+constexpr int64_t kMaxLoraK = 1LL << 20;
+constexpr int64_t kMaxLoraStride = 1LL << 24;
 
 // The host values of qmat_lora.
 int check_lora(const qmat_lora_args& a) {
   if (a.dtype != QMAT_F16 && a.dtype != QMAT_BF16) return QMAT_E_DTYPE;
-  if (a.n_tokens < 0 || a.n_tokens > kMaxLoraTokens || a.n_seqs < 0 || a.n_seqs > kMaxTokens ||
+  if (a.n_tokens < 0 || a.n_tokens > kMaxLoraTokens || a.n_seqs < 0 || a.n_seqs > kMaxLoraTokens ||
       a.n_adapters < 0 || a.n_adapters > kMaxTokens || a.M < 0 || a.M > kMaxLoraRows || a.max_q < 0)
     return QMAT_E_SHAPE;
-  if (a.K < 0 || a.K > kMaxK || a.K % 32 != 0 || a.rank < 8 || a.rank > kMaxLoraRank ||
+  if (a.K < 0 || a.K > kMaxLoraK || a.K % 32 != 0 || a.rank < 8 || a.rank > kMaxLoraRank ||
       a.rank % 8 != 0)
     return QMAT_E_SHAPE;
-  if (!rows_ok(a.n_tokens, a.M, a.base_stride, 4) || !rows_ok(a.n_tokens, a.M, a.y_stride, 4))
+  if (a.base_stride < a.M || a.base_stride > kMaxLoraStride || a.y_stride < a.M ||
+      a.y_stride > kMaxLoraStride)
     return QMAT_E_SHAPE;
   return QMAT_OK;
 }

@@ -724,9 +724,9 @@ int qmat_page_step(const qmat_page_args *args, void *workspace, int64_t workspac
  *   sum is scaled and added in fp32; the second product is fp32. Other
  *   requests' adapters and activations have no effect on a token, whatever
  *   their values (infinities and NaN included).
- *   Limits (QMAT_E_SHAPE): K a multiple of 32, up to 2^24; rank a multiple of
- *   8, 8 to 256; n_tokens up to 2^20, M up to 2^23, n_seqs and n_adapters up to
- *   2^24; max_q >= 0.
+ *   Limits (QMAT_E_SHAPE): K a multiple of 32, up to 2^20; rank a multiple of
+ *   8, 8 to 256; n_tokens and n_seqs up to 2^20, M up to 2^23, n_adapters and
+ *   the strides up to 2^24; max_q >= 0.
  *   max_q: no sequence has more tokens. An estimate: it chooses how the work is
  *   divided (1 for decode), and with it the order of a sum's last bits.
  *   Alignment: x_q8, a, b, y, base 16 bytes; scale, ranks, adapter, q_start 4.

@@ -327,7 +327,7 @@ static void lora_cases() {
   LORA(n_tokens, -1, QMAT_E_SHAPE, 0);
   LORA(n_tokens, ((int64_t)1 << 20) + 1, QMAT_E_SHAPE, 0);
   LORA(n_seqs, -1, QMAT_E_SHAPE, 0);
-  LORA(n_seqs, ((int64_t)1 << 24) + 1, QMAT_E_SHAPE, 0);
+  LORA(n_seqs, ((int64_t)1 << 20) + 1, QMAT_E_SHAPE, 0);
   LORA(n_adapters, -1, QMAT_E_SHAPE, 0);
   LORA(n_adapters, ((int64_t)1 << 24) + 1, QMAT_E_SHAPE, 0);
   LORA(rank, 0, QMAT_E_SHAPE, 0);
@@ -338,11 +338,12 @@ static void lora_cases() {
   LORA(M, ((int64_t)1 << 23) + 1, QMAT_E_SHAPE, 0);
   LORA(K, -32, QMAT_E_SHAPE, 0);
   LORA(K, 40, QMAT_E_SHAPE, 0);
-  LORA(K, ((int64_t)1 << 24) + 32, QMAT_E_SHAPE, 0);
+  LORA(K, ((int64_t)1 << 20) + 32, QMAT_E_SHAPE, 0);
   LORA(max_q, -1, QMAT_E_SHAPE, 0);
   LORA(y_stride, 99, QMAT_E_SHAPE, 0);
   LORA(base_stride, 0, QMAT_E_SHAPE, 0);
-  LORA(y_stride, INT64_MAX, QMAT_E_SHAPE, 0);
+  LORA(y_stride, ((int64_t)1 << 24) + 1, QMAT_E_SHAPE, 0);
+  LORA(base_stride, INT64_MAX, QMAT_E_SHAPE, 0);
   LORA(x_q8, NULL, QMAT_E_NULL, 0);
   LORA(a, NULL, QMAT_E_NULL, 0);
   LORA(b, NULL, QMAT_E_NULL, 0);
@@ -372,6 +373,7 @@ static void lora_cases() {
   if (qmat_lora_workspace_bytes(&x) != 0) ++failures;
   EXPECT(qmat_lora(&x, NULL, 0, NULL), QMAT_OK, 1);
   x = lora_good();
+  x.max_q = 30;
   const int64_t n = qmat_lora_workspace_bytes(&x);
   if (n <= 0) ++failures;
   EXPECT(qmat_lora(&x, NULL, n, NULL), QMAT_E_WORKSPACE, 0);
@@ -383,20 +385,23 @@ static void lora_cases() {
   for (int64_t tokens : sizes)
     for (int64_t q : sizes)
       for (int64_t rank : {8, 16, 24, 40, 64, 128, 136, 256})
-        for (int64_t K : {0, 32, 4096, 11008, 1 << 24})
-          for (int64_t adapters : {0, 1, 3, 1 << 24}) {
+        for (int64_t K : {0, 32, 4096, 11008, 1 << 20})
+          for (int64_t seqs : {0, 1, 3, 1 << 20}) {
             x.n_tokens = tokens;
             x.max_q = q;
             x.rank = rank;
             x.K = K;
-            x.n_adapters = adapters;
+            x.n_seqs = seqs;
             const qmat::LoraPlan p = qmat::lora_plan(x);
-            const int64_t waves = p.tiles * p.slots * p.groups * p.parts;
-            if (waves * 64 >= (int64_t)1 << 32 || p.slots < 1 || p.slots > 16 ||
-                p.tiles * 16 * p.token_tiles < tokens || p.groups * 16 * p.rank_tiles < rank ||
-                p.z_stride < rank || p.z_stride > 256 || p.parts > K / 32 || (K > 0 && p.parts < 1) ||
-                p.up_rows % 64 != 0 || (((int64_t)1 << 23) + p.up_rows - 1) / p.up_rows > 65535 ||
-                qmat_lora_workspace_bytes(&x) != p.parts * tokens * p.z_stride * 4) {
+            const int64_t rows = p.few ? p.few_rows : p.up_rows;
+            const bool tiles = p.few || (p.tiles * 16 * p.token_tiles >= tokens && p.groups * 16 * p.rank_tiles >= rank &&
+                                         p.z_stride >= rank && p.z_stride <= 256 && p.parts <= K / 32 &&
+                                         (K == 0 || p.parts >= 1));
+            // threads of a launch in 32 bits, rows of workgroups in 16
+            if (!tiles || p.tiles * p.parts * 512 >= (int64_t)1 << 32 || tokens * 1024 >= (int64_t)1 << 32 ||
+                p.tiles * 512 >= (int64_t)1 << 32 || rows < 64 || rows % 64 != 0 ||
+                (((int64_t)1 << 23) + rows - 1) / rows > 65535 ||
+                qmat_lora_workspace_bytes(&x) != (p.few ? 0 : p.parts * tokens * p.z_stride * 4)) {
               fprintf(stderr, "FAIL plan: %lld tokens, max_q %lld, rank %lld, K %lld\n", (long long)tokens,
                       (long long)q, (long long)rank, (long long)K);
               ++failures;
