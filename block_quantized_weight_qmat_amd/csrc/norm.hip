@@ -147,10 +147,10 @@ __device__ __forceinline__ void put(const qmat_norm_args& a, int64_t row, int p,
 // kRows rows of up to kThreads * kUnits * 8 elements a workgroup, kThreads
 // threads each.
 template <typename T, int kThreads, int kRows, int kUnits>
-__global__ __launch_bounds__(kThreads* kRows) void norm_kernel(qmat_norm_args a) {
+__global__ __launch_bounds__(kThreads* kRows) void norm_kernel(qmat_norm_args a, int64_t row0) {
   static_assert(kRows == 1 || kThreads == kWave, "rows of a workgroup share no barrier");
   __shared__ double part[kThreads / kWave];
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kThreads;
+  const int64_t row = row0 + (int64_t)blockIdx.x * kRows + threadIdx.x / kThreads;
   if (kRows > 1 && row >= a.n) return;  // a whole wave
   const int t = threadIdx.x % kThreads, pieces = (int)(a.K / 8);
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
@@ -194,9 +194,9 @@ __global__ __launch_bounds__(kThreads* kRows) void norm_kernel(qmat_norm_args a)
 constexpr int kLongThreads = 1024;
 
 template <typename T>
-__global__ __launch_bounds__(kLongThreads) void norm_long_kernel(qmat_norm_args a) {
+__global__ __launch_bounds__(kLongThreads) void norm_long_kernel(qmat_norm_args a, int64_t row0) {
   __shared__ double part[kLongThreads / kWave];
-  const int64_t row = blockIdx.x;
+  const int64_t row = row0 + blockIdx.x;
   const int pieces = (int)(a.K / 8);
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   const T* res = static_cast<const T*>(a.residual) + row * a.residual_stride;
@@ -226,11 +226,16 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(qmat_norm_args 
   }
 }
 
+// Rows of a launch: a launch's threads are counted in 32 bits.
+constexpr int64_t kMaxRows = 1 << 21;
+
 template <typename T, int kThreads, int kRows, int kUnits>
 void launch_rows(const qmat_norm_args& a, hipStream_t stream) {
-  hipLaunchKernelGGL((norm_kernel<T, kThreads, kRows, kUnits>),
-                     dim3((unsigned)((a.n + kRows - 1) / kRows)), dim3(kThreads * kRows), 0, stream,
-                     a);
+  for (int64_t row = 0; row < a.n; row += kMaxRows) {
+    const int64_t n = a.n - row < kMaxRows ? a.n - row : kMaxRows;
+    hipLaunchKernelGGL((norm_kernel<T, kThreads, kRows, kUnits>), dim3((unsigned)((n + kRows - 1) / kRows)),
+                       dim3(kThreads * kRows), 0, stream, a, row);
+  }
 }
 
 template <typename T>
@@ -248,7 +253,9 @@ void launch_as(const qmat_norm_args& a, hipStream_t stream) {
   else if (a.K <= 16384)
     launch_rows<T, 1024, 1, 2>(a, stream);
   else
-    hipLaunchKernelGGL((norm_long_kernel<T>), dim3((unsigned)a.n), dim3(kLongThreads), 0, stream, a);
+    for (int64_t row = 0; row < a.n; row += kMaxRows)
+      hipLaunchKernelGGL((norm_long_kernel<T>), dim3((unsigned)(a.n - row < kMaxRows ? a.n - row : kMaxRows)),
+                         dim3(kLongThreads), 0, stream, a, row);
 }
 
 }  // namespace

@@ -29,14 +29,32 @@ __device__ __forceinline__ void turn(int32_t pos, double freq, float* s, float* 
   sincospif((float)(2.0 * (turns - rint(turns))), s, c);
 }
 
+template <int kCtrl>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(
+                 float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, true));
+}
+
+// The sum over 1 << log2_lanes neighbouring lanes, in each of them.
+__device__ __forceinline__ float group_sum(float v, int log2_lanes) {
+  if (log2_lanes > 0) v = dpp_add<0xB1>(v);   // neighbours
+  if (log2_lanes > 1) v = dpp_add<0x4E>(v);   // pairs of a quad
+  if (log2_lanes > 2) v = dpp_add<0x141>(v);  // quads, mirrored in 8 lanes
+  if (log2_lanes > 3) v = dpp_add<0x140>(v);  // eights, mirrored in 16
+  if (log2_lanes > 4) v += shfl_xor_f(v, 16);
+  if (log2_lanes > 5) v += shfl_xor_f(v, 32);
+  return v;
+}
+
 // log2_lanes: lanes of a head; parts: groups of lanes that share a token.
 template <typename In, typename Out>
-__global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int log2_lanes, int parts) {
-  const int lanes = 1 << log2_lanes;
-  const int u = threadIdx.x & (lanes - 1);
-  const int64_t group = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> log2_lanes;
-  const int64_t token = group / parts;
-  const int part = (int)(group - token * parts);
+__global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_t token0,
+                                                        int log2_lanes, int parts) {
+  const int u = threadIdx.x & ((1 << log2_lanes) - 1);
+  const uint32_t group = (blockIdx.x * kThreads + threadIdx.x) >> log2_lanes;
+  const uint32_t nth = group / (uint32_t)parts;
+  const int64_t token = token0 + nth;
+  const int part = (int)(group - nth * parts);
   const int D = (int)a.head_dim, pairs = (int)a.rot_dim / 2;
   // a wave's lanes stay together for the norm's sums: those without work load nothing
   const bool live = token < a.n && 8 * u < D;
@@ -44,6 +62,17 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int lo
   const bool turned = 8 * u < 2 * pairs;
   const int e0 = turned && !a.neighbours ? 4 * u : 8 * u;
   const int e1 = turned && !a.neighbours ? pairs + 4 * u : 8 * u + 4;
+  const int heads = (int)(a.heads + a.kv_heads), q_heads = (int)a.heads;
+  const In* const q = static_cast<const In*>(a.q) + token * a.q_stride;
+  const In* const k = static_cast<const In*>(a.k) + token * a.k_stride;
+  const auto load = [&](int h, float* v) {
+    if (!live || h >= heads) return;
+    const In* x = h < q_heads ? q + h * D : k + (h - q_heads) * D;
+    load_f32<In, 4>(x + e0, v);
+    load_f32<In, 4>(x + e1, v + 4);
+  };
+  float next[8] = {};
+  load(part, next);  // on its way during the angles; then always one head ahead
   float sn[4], cs[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -55,31 +84,30 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int lo
         turn(a.positions[ax * a.pos_stride + token], a.freq[4 * u + i], &sn[i], &cs[i]);
     }
   }
-  const int heads = (int)(a.heads + a.kv_heads);
+  const float mean = 1.0f / (float)D, eps = (float)a.eps;
+  const float* weight = nullptr;
+  float w[8];
   for (int h = part; h < heads; h += parts) {
-    const bool is_k = h >= (int)a.heads;
-    const int hh = is_k ? h - (int)a.heads : h;
-    const float* weight = is_k ? a.k_norm : a.q_norm;
-    float v[8] = {};
-    if (live) {
-      const In* x = static_cast<const In*>(is_k ? a.k : a.q) +
-                    token * (is_k ? a.k_stride : a.q_stride) + hh * a.head_dim;
-      load_f32<In, 4>(x + e0, v);
-      load_f32<In, 4>(x + e1, v + 4);
+    const bool is_k = h >= q_heads;
+    if (const float* now = is_k ? a.k_norm : a.q_norm; now != weight) {  // twice at most
+      weight = now;
+      if (live && weight != nullptr) {
+        load_f32<float, 4>(weight + e0, w);
+        load_f32<float, 4>(weight + e1, w + 4);
+      }
     }
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = next[e];
+    load(h + parts, next);
     if (weight != nullptr) {
       float s = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) s = fmaf(v[e], v[e], s);
-      for (int m = 1; m < lanes; m <<= 1) s += shfl_xor_f(s, m);
-      const float r = 1.0f / sqrtf(s / (float)D + (float)a.eps);
-      if (live) {
-        float w[8];
-        load_f32<float, 4>(weight + e0, w);
-        load_f32<float, 4>(weight + e1, w + 4);
+      s = group_sum(s, log2_lanes);
+      const float r = rsqrtf(s * mean + eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
-      }
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
     }
     if (!live) continue;
     if (turned) {
@@ -88,37 +116,49 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int lo
         // pair i: elements i and 4 + i (halves), or 2i and 2i + 1 of the eight
         const float x = a.neighbours ? v[2 * i] : v[i];
         const float y = a.neighbours ? v[2 * i + 1] : v[4 + i];
-        const float p = x * cs[i] - y * sn[i], q = y * cs[i] + x * sn[i];
+        const float p = x * cs[i] - y * sn[i], t = y * cs[i] + x * sn[i];
         if (a.neighbours) {
           v[2 * i] = p;
-          v[2 * i + 1] = q;
+          v[2 * i + 1] = t;
         } else {
           v[i] = p;
-          v[4 + i] = q;
+          v[4 + i] = t;
         }
       }
     }
-    Out* out = static_cast<Out*>(is_k ? a.k_out : a.q_out) +
-               token * (is_k ? a.k_out_stride : a.q_out_stride) + hh * a.head_dim;
+    Out* out = is_k ? static_cast<Out*>(a.k_out) + token * a.k_out_stride + (h - q_heads) * D
+                    : static_cast<Out*>(a.q_out) + token * a.q_out_stride + h * D;
     store_f32<Out, 4>(out + e0, v);
     store_f32<Out, 4>(out + e1, v + 4);
   }
 }
 
-// Lanes that fill the GPU: 256 CUs with four waves for each of their SIMDs.
-constexpr int64_t kFill = 256 * 4 * 4 * kWave;
+// How many groups of lanes share a token's heads: enough for eight waves on each
+// SIMD (8191 x 40 heads of 128, bf16, on 3 axes: 49 us with four, 43 with eight, 50
+// with twelve), but four heads for each group, which share its angles (1024 tokens: 13.0 us
+// with one or two, 10.0 with four, 11.5 with eight), as long as that leaves a wave
+// for each SIMD (128 tokens: 4.7 us with one head, 5.0 with four).
+constexpr int64_t kSimds = 256 * 4;
+constexpr int64_t kPerSimd = 8;
+constexpr int64_t kShared = 4;
+constexpr int64_t kMaxLanes = 1LL << 31;  // of a launch: their number has 32 bits
 
 template <typename In, typename Out>
 void launch_as(const qmat_rope_args& a, hipStream_t stream) {
   int log2_lanes = 0;
   while ((8 << log2_lanes) < a.head_dim) ++log2_lanes;
   const int64_t heads = a.heads + a.kv_heads;
-  int64_t parts = (kFill >> log2_lanes) / a.n;
+  const int64_t one = (kSimds * kWave >> log2_lanes) / a.n;  // for a wave on each SIMD
+  const int64_t most_shared = (heads + kShared - 1) / kShared;
+  int64_t parts = (kPerSimd * kSimds * kWave >> log2_lanes) / a.n;
+  if (parts > most_shared) parts = one > most_shared ? one : most_shared;
   parts = parts < 1 ? 1 : parts > heads ? heads : parts;
-  const int64_t per = kThreads >> log2_lanes;
-  const int64_t wgs = (a.n * parts + per - 1) / per;
-  hipLaunchKernelGGL((rope_kernel<In, Out>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, a,
-                     log2_lanes, (int)parts);
+  const int64_t per = kThreads >> log2_lanes, most = (kMaxLanes >> log2_lanes) / parts;
+  for (int64_t t = 0; t < a.n; t += most) {
+    const int64_t n = a.n - t < most ? a.n - t : most;
+    hipLaunchKernelGGL((rope_kernel<In, Out>), dim3((unsigned)((n * parts + per - 1) / per)), dim3(kThreads), 0,
+                       stream, a, t, log2_lanes, (int)parts);
+  }
 }
 
 template <typename In>

@@ -139,3 +139,16 @@ def test_nothing_to_do(lib):
     x = torch.zeros((0, 64), device="cuda")
     rows, q8, h = lib.rms_norm(x, torch.ones(64, device="cuda"), residual=x, want="both")
     assert rows.shape == (0, 64) and q8.shape == (0, 68) and h.shape == (0, 64)
+
+
+def test_more_rows_than_a_launch(lib):
+    """Rows past the 2^21 of one launch, and past 2^32 bytes of each buffer, get what the same rows alone get."""
+    import torch
+    n, K = (1 << 21) + 70001, 1024
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(n, K, device="cuda", generator=g, dtype=torch.float16)
+    w = torch.rand(K, device="cuda", generator=g)
+    rows, q8, _ = lib.rms_norm(x, w, want="both")
+    for at in (0, (1 << 21) - 3, n - 5):
+        part = lib.rms_norm(x[at:at + 5].clone(), w, want="both")
+        assert torch.equal(rows[at:at + 5], part[0]) and torch.equal(q8[at:at + 5], part[1])
