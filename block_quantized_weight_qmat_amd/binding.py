@@ -412,6 +412,8 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     shape, stride = t.shape, t.stride()
+    if len(shape) == 2 and stride[1] == 1 and shape[0] > 1:
+        return stride[0]
     row = 1
     for d in range(len(shape) - 1, 0, -1):
         if shape[d] != 1 and stride[d] != row:
@@ -607,20 +609,21 @@ def embed(fmt, blocks: torch.Tensor, K: int, ids: torch.Tensor | None = None,
     outside the matrix gives zeros."""
     f = _fmt(fmt)
     _gpu(blocks, "blocks", torch.uint8)
-    rb = row_bytes(f, K)
-    if blocks.dim() != 2 or blocks.shape[1] != rb:
+    if blocks.dim() != 2 or blocks.shape[1] != row_bytes(f, K):
         raise ValueError("blocks must be 2-D [rows, row_bytes(fmt, K)]")
-    device, rows = blocks.device, blocks.shape[0]
+    device, rows, dt = blocks.device, blocks.shape[0], _dtype(dtype)
+    n, ip = rows, None
     if ids is not None:
         _flat(ids, "ids", torch.int32, device)
-    n = rows if ids is None else ids.numel()
+        n, ip = ids.numel(), ids.data_ptr()
     if out is None:
-        out = torch.empty((n, K), dtype=dtype, device=device)
-    dt, stride = _dtype(dtype), _rows(out, "out", dtype)
-    if out.device != device or out.shape[0] != n or out.numel() != n * K:
-        raise ValueError("out must hold n rows of K elements, on the device of blocks")
-    _launch("qmat_embed", load_library().qmat_embed, device, f, dt, blocks.data_ptr(),
-            None if ids is None else ids.data_ptr(), out.data_ptr(), stride, n, rows, K)
+        out, stride = torch.empty((n, K), dtype=dtype, device=device), K
+    else:
+        stride = _rows(out, "out", dtype)
+        if out.device != device or out.shape[0] != n or out.numel() != n * K:
+            raise ValueError("out must hold n rows of K elements, on the device of blocks")
+    _launch("qmat_embed", load_library().qmat_embed, device, f, dt, blocks.data_ptr(), ip,
+            out.data_ptr(), stride, n, rows, K)
     return out
 
 
@@ -652,29 +655,35 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     _flat(weight, "weight", torch.float32, device)
     if weight.numel() != K:
         raise ValueError("weight must hold K values")
-    rs = hs = ys = 0
+    rs = hs = ys = K
     rp = hp = yp = qp = None
     if residual is not None:
         rs, rp = _same(residual, "residual", x), residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty((n, K), dtype=x.dtype, device=device)
-        hs, hp = _same(residual_out, "residual_out", x), residual_out.data_ptr()
+            residual_out = x.new_empty((n, K))
+        else:
+            hs = _same(residual_out, "residual_out", x)
+        hp = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if want == "q8":
         rows = None
     else:
         if rows is None:
-            rows = torch.empty((n, K), dtype=x.dtype, device=device)
-        ys, yp = _same(rows, "rows", x), rows.data_ptr()
+            rows = x.new_empty((n, K))
+        else:
+            ys = _same(rows, "rows", x)
+        yp = rows.data_ptr()
     if want == "rows":
         q8 = None
     else:
+        size = K // 32 * 34
         if q8 is None:
-            q8 = torch.empty((n, K // 32 * 34), dtype=torch.uint8, device=device)
-        _flat(q8, "q8", torch.uint8, device)
-        if q8.numel() != n * (K // 32 * 34):
-            raise ValueError("q8 has the wrong size")
+            q8 = torch.empty((n, size), dtype=torch.uint8, device=device)
+        else:
+            _flat(q8, "q8", torch.uint8, device)
+            if q8.numel() != n * size:
+                raise ValueError("q8 has the wrong size")
         qp = q8.data_ptr()
     a = NormArgs(dt, x.data_ptr(), rp, hp, weight.data_ptr(), yp, qp, xs, rs, hs, ys, n, K, eps)
     _launch("qmat_norm", load_library().qmat_norm, device, ctypes.byref(a))
@@ -734,21 +743,24 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, freq:
         dtype = q.dtype if q_out is None else q_out.dtype
     ot = _dtype(dtype)
     if q_out is None:
-        q_out = torch.empty((n, heads, head_dim), dtype=dtype, device=device)
-    if q_out.dtype != dtype:
-        raise TypeError(f"q_out must be {dtype}, got {q_out.dtype}")
-    if q_out.shape != q.shape or q_out.device != device:
-        raise ValueError("q_out must have the shape and device of q")
-    qos = _rows(q_out, "q_out", dtype)
+        q_out, qos = torch.empty((n, heads, head_dim), dtype=dtype, device=device), heads * head_dim
+    else:
+        if q_out.dtype != dtype:
+            raise TypeError(f"q_out must be {dtype}, got {q_out.dtype}")
+        if q_out.shape != q.shape or q_out.device != device:
+            raise ValueError("q_out must have the shape and device of q")
+        qos = _rows(q_out, "q_out", dtype)
     ks = kos = kv_heads = 0
     kp = kop = None
     if k is not None:
         ks, kp, kv_heads = _heads(k, "k", q), k.data_ptr(), k.shape[1]
         if k_out is None:
-            k_out = torch.empty((n, kv_heads, head_dim), dtype=dtype, device=device)
-        kos, kop = _heads(k_out, "k_out", q_out), k_out.data_ptr()
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must have the shape of k")
+            k_out, kos = q_out.new_empty((n, kv_heads, head_dim)), kv_heads * head_dim
+        else:
+            kos = _heads(k_out, "k_out", q_out)
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have the shape of k")
+        kop = k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out needs a k")
     _flat(positions, "positions", torch.int32, device)
@@ -813,11 +825,20 @@ def page_step(kv_len: torch.Tensor, add: torch.Tensor, page_table: torch.Tensor,
     _ints(free_count, "free_count", 1, device)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    q_start = _ints(q_start, "q_start", n_seqs + 1, device)
-    slots = _ints(slots, "slots", max_tokens, device)
-    positions = _ints(positions, "positions", max_tokens, device)
-    token_seq = _ints(token_seq, "token_seq", max_tokens, device)
-    status = _ints(status, "status", n_seqs, device)
+    if q_start is None and slots is None and positions is None and token_seq is None and \
+            status is None:
+        # one allocation; what kv_store takes starts at 16 bytes
+        wide = (max_tokens + 3) // 4 * 4
+        rest = wide - max_tokens
+        buf = torch.empty(3 * wide + 2 * n_seqs + 1, dtype=torch.int32, device=device)
+        slots, _, positions, _, token_seq, _, q_start, status = buf.split(
+            (max_tokens, rest, max_tokens, rest, max_tokens, rest, n_seqs + 1, n_seqs))
+    else:
+        q_start = _ints(q_start, "q_start", n_seqs + 1, device)
+        slots = _ints(slots, "slots", max_tokens, device)
+        positions = _ints(positions, "positions", max_tokens, device)
+        token_seq = _ints(token_seq, "token_seq", max_tokens, device)
+        status = _ints(status, "status", n_seqs, device)
     a = PageArgs(kv_len.data_ptr(), None if keep is None else keep.data_ptr(), add.data_ptr(),
                  page_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
                  q_start.data_ptr(), slots.data_ptr(), positions.data_ptr(), token_seq.data_ptr(),

@@ -239,22 +239,29 @@ __global__ __launch_bounds__(kRowThreads) void page_rows_kernel(qmat_page_args a
 }
 
 constexpr int kManyThreads = 1024;
+constexpr int kFewThreads = 256;
+constexpr int kEach = 4;  // tokens' rows of a thread, where one kernel does it all
 
-// Where one kernel does it all: a thread for each sequence, four rows for each thread.
-bool alone(const qmat_page_args& a) {
-  return a.n_seqs <= kManyThreads && a.max_tokens <= 4 * kManyThreads;
+// A thread for each sequence and kEach rows for each thread.
+bool alone(const qmat_page_args& a, int64_t threads) {
+  return a.n_seqs <= threads && a.max_tokens <= kEach * threads;
 }
 
 }  // namespace
 
 int64_t page_workspace_bytes(const qmat_page_args& a) {
-  return alone(a) ? 0 : (int64_t)sizeof(Step) + a.n_seqs * (int64_t)sizeof(Seq);
+  return alone(a, kManyThreads) ? 0 : (int64_t)sizeof(Step) + a.n_seqs * (int64_t)sizeof(Seq);
 }
 
 hipError_t launch_page_step(const qmat_page_args& a, void* workspace, hipStream_t stream) {
   int shift = 0;
   while ((1LL << shift) < a.page_size) ++shift;
-  if (alone(a)) {
+  if (alone(a, kFewThreads)) {
+    hipLaunchKernelGGL((page_step_kernel<kFewThreads, true>), dim3(1), dim3(kFewThreads), 0, stream, a,
+                       shift, nullptr, nullptr);
+    return hipGetLastError();
+  }
+  if (alone(a, kManyThreads)) {
     hipLaunchKernelGGL((page_step_kernel<kManyThreads, true>), dim3(1), dim3(kManyThreads), 0,
                        stream, a, shift, nullptr, nullptr);
     return hipGetLastError();
