@@ -50,6 +50,23 @@ __device__ __forceinline__ float quad_max(float v) {
   return fmaxf(v, __builtin_bit_cast(float, o));
 }
 
+template <int kCtrl>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(
+                 float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, true));
+}
+
+// The sum over 1 << log2_lanes neighbouring lanes, in each of them.
+__device__ __forceinline__ float group_sum(float v, int log2_lanes) {
+  if (log2_lanes > 0) v = dpp_add<0xB1>(v);   // neighbours
+  if (log2_lanes > 1) v = dpp_add<0x4E>(v);   // pairs of a quad
+  if (log2_lanes > 2) v = dpp_add<0x141>(v);  // quads, mirrored in 8 lanes
+  if (log2_lanes > 3) v = dpp_add<0x140>(v);  // eights, mirrored in 16
+  if (log2_lanes > 4) v += shfl_xor_f(v, 16);
+  if (log2_lanes > 5) v += shfl_xor_f(v, 32);
+  return v;
+}
+
 // Row and block column of block i of rows of nb blocks; 32-bit division
 // wherever the counts fit.
 __device__ __forceinline__ void split_index(int64_t i, int64_t total, int nb, int64_t* row,

@@ -442,25 +442,55 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(qmat_lora_args a, L
 
 // --------------------------------------------------- both, for a token at a time
 
+// Eight products, exact in fp32, and their sum.
+__device__ __forceinline__ float dot8x8(half8_t a, half8_t b) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    s = __builtin_amdgcn_fdot2(half2_t{a[i], a[i + 1]}, half2_t{b[i], b[i + 1]}, s, false);
+  return s;
+}
+__device__ __forceinline__ float dot8x8(bf16x8 a, bf16x8 b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    s = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a[i], a[i + 1]}, bf16x2{b[i], b[i + 1]}, s, false);
+  return s;
+}
+
 constexpr int kFewThreads = 1024;
 constexpr int kFewWaves = kFewThreads / kWave;
 // A few tokens of each sequence and small adapters: one launch and no
 // workspace. A workgroup has one token and plan.few_rows rows of b; it computes
 // all of z for itself (a wave has a rank's row of a, side by side), since a pass
-// over a in the L2 is shorter than a second kernel, and then has a row of b for each
-// thread at a time, the next of which (16 ranks of it) is on its way meanwhile.
+// over a in the L2 is shorter than a second kernel. Then a wave has 64 rows of b at a time:
+// eight ranks for each lane, a row for as many lanes as that takes, so that loads
+// are side by side; a lane keeps its part of z in registers, the lanes of a
+// row add up their sums, and each lane keeps one row's. Two loads are always on their
+// way, the first two during the products with a.
 template <typename T>
 __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(qmat_lora_args a, LoraPlan plan) {
   typedef typename Vec8<T>::type vec8;
   __shared__ __attribute__((aligned(16))) float zs[kLoraMaxRank];
-  const int lane = threadIdx.x & 63;
+  extern __shared__ __attribute__((aligned(16))) uint8_t xs[];  // codes as T, then block scales
+  const int lane = threadIdx.x & 63, K = (int)a.K;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
-  const int64_t m0 = (int64_t)blockIdx.y * plan.few_rows + threadIdx.x;
-  const int64_t end = (int64_t)(blockIdx.y + 1) * plan.few_rows;
-  const int64_t m_end = end < a.M ? end : a.M;
+  const int first = (int)(blockIdx.y * plan.few_rows);
+  const int m_end = (int)(first + plan.few_rows < a.M ? first + plan.few_rows : a.M);
   const float* base = a.base + t * a.base_stride;
   float* y = a.y + t * a.y_stride;
+  // the token's codes, which every rank's row meets, as T: once, eight a thread
+  const uint8_t* const x = static_cast<const uint8_t*>(a.x_q8) + t * (K / 32 * 34);
+  float* const scales = reinterpret_cast<float*>(xs + 2 * K);
+#pragma nounroll
+  for (int k = 8 * threadIdx.x; k < K; k += 8 * kFewThreads) {
+    const uint8_t* blk = x + (k >> 5) * 34;
+    const u32x2_a2 q = *reinterpret_cast<const u32x2_a2*>(blk + 2 + (k & 31));
+    *reinterpret_cast<vec8*>(xs + 2 * k) = codes<T>(q.x, q.y);
+    if ((k & 31) == 0) scales[k >> 5] = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(blk));
+  }
   // the sequence is t most often: its adapter is read beside its start
   Adapter ad{-1, 0, 0.0f};
   if (a.n_seqs > 0) {
@@ -476,61 +506,65 @@ __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(qmat_lora_args a,
   }
   if (ad.id < 0) {  // the workgroup together
     if (a.base != a.y)
-      for (int64_t m = m0; m < m_end; m += kFewThreads) y[m] = base[m];
+      for (int m = first + threadIdx.x; m < m_end; m += kFewThreads) y[m] = base[m];
     return;
   }
-  const T* brow = static_cast<const T*>(a.b) + (int64_t)ad.id * a.M * a.rank;
-  const int second = a.rank < 16 ? 0 : 8;  // the ranks read ahead: 0.. and these
-  struct Row {
-    vec8 w[2];
-    float base;
-  };
-  const auto load_row = [&](int64_t m) {  // past the last: the last
-    m = m < m_end ? m : m_end - 1;
-    return Row{{*reinterpret_cast<const vec8*>(brow + m * a.rank), *reinterpret_cast<const vec8*>(brow + m * a.rank + second)},
-               base[m]};
-  };
-  Row next = load_row(m0);
-  // z: a rank's row for each wave, eight elements for each lane at a time
   const int rank = ad.rank;
-  const uint8_t* x = static_cast<const uint8_t*>(a.x_q8) + t * (a.K / 32 * 34);
+  // rows m0 + 64 / (1 << log2) i + lane >> log2 for i = 0, 1, ..; past the last: the last
+  const int sub = lane & ((1 << plan.few_log2) - 1), r0 = 8 * sub, per = kWave >> plan.few_log2;
+  const T* const brow = static_cast<const T*>(a.b) + (int64_t)ad.id * a.M * a.rank + (r0 < a.rank ? r0 : 0);
+  const int m0 = first + kWave * wave;
+  const auto load_row = [&](int i) {
+    // a wave's next 64 rows lie behind the other waves'
+    const int m = m0 + (i >> plan.few_log2) * kFewThreads + (i & ((1 << plan.few_log2) - 1)) * per + (lane >> plan.few_log2);
+    return *reinterpret_cast<const u32x4*>(brow + (uint32_t)(m < m_end ? m : m_end - 1) * a.rank);
+  };
+  u32x4 w0 = load_row(0), w1 = load_row(1);
+  // z: a rank's row for each wave, eight elements for each lane at a time
+  __syncthreads();
   for (int r = wave; r < rank; r += kFewWaves) {
-    const T* row = static_cast<const T*>(a.a) + (ad.id * a.rank + r) * a.K;
+    const T* row = static_cast<const T*>(a.a) + (ad.id * a.rank + r) * K;
     float sum = 0.0f;
 #pragma unroll 4
-    for (int k = 8 * lane; k < (int)a.K; k += 8 * kWave) {
+    for (int k = 8 * lane; k < K; k += 8 * kWave) {
       const vec8 w = *reinterpret_cast<const vec8*>(row + k);
-      const uint8_t* blk = x + (int64_t)(k >> 5) * 34;
-      const float d = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(blk));
-      const u32x2_a2 q = *reinterpret_cast<const u32x2_a2*>(blk + 2 + (k & 31));
-      float part = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        part = fmaf((float)w[e], (float)(int8_t)(q[e >> 2] >> (8 * (e & 3))), part);
-      sum = fmaf(d, part, sum);
+      sum = fmaf(scales[k >> 5], dot8x8(w, *reinterpret_cast<const vec8*>(xs + 2 * k)), sum);
     }
 #pragma unroll
     for (int m = 1; m < kWave; m <<= 1) sum += shfl_xor_f(sum, m);
     if (lane == 0) zs[r] = sum;
   }
-  // up to the next eight ranks: 0
-  if (threadIdx.x < 8 && rank + threadIdx.x < kLoraMaxRank) zs[rank + threadIdx.x] = 0.0f;
   __syncthreads();
-  const auto dot8 = [&](const vec8& w, int r8, float sum) {
+  float zr[8];
+  u32x4 keep;  // ranks that are there
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(r8 + e < rank ? (float)w[e] : 0.0f, zs[r8 + e], sum);
-    return sum;
-  };
+  for (int e = 0; e < 8; e += 2) {
+    const bool in0 = r0 + e < rank, in1 = r0 + e + 1 < rank;
+    zr[e] = in0 ? zs[r0 + e] : 0.0f;
+    zr[e + 1] = in1 ? zs[r0 + e + 1] : 0.0f;
+    keep[e / 2] = (in0 ? 0xFFFFu : 0u) | (in1 ? 0xFFFF0000u : 0u);
+  }
+  // the lane's own row of 64: of its group's, the one that its place in a row counts
+  const int own = sub * per + (lane >> plan.few_log2);
+  int i = 0;
 #pragma nounroll
-  for (int64_t m = m0; m < m_end; m += kFewThreads) {
-    const Row row = next;
-    next = load_row(m + kFewThreads);
-    float sum = dot8(row.w[0], 0, 0.0f);
-    if (rank > 8) sum = dot8(row.w[1], 8, sum);
+  for (int m = m0; m < m_end; m += kFewThreads) {
+    const int mine = m + own < m_end ? m + own : m_end - 1;
+    const float v = base[mine];
+    float sum = 0.0f;
 #pragma nounroll
-    for (int r8 = 16; r8 < rank; r8 += 8)
-      sum = dot8(*reinterpret_cast<const vec8*>(brow + m * a.rank + r8), r8, sum);
-    y[m] = fmaf(ad.scale, sum, row.base);
+    for (int j = 0; j < 1 << plan.few_log2; ++j, ++i) {
+      const u32x4 wk = w0 & keep;
+      w0 = w1;
+      w1 = load_row(i + 2);
+      const vec8 w = __builtin_bit_cast(vec8, wk);
+      float s = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = fmaf((float)w[e], zr[e], s);
+      s = group_sum(s, plan.few_log2);
+      sum = j == sub ? s : sum;
+    }
+    if (m + own < m_end) y[mine] = fmaf(ad.scale, sum, v);
   }
 }
 
@@ -556,7 +590,7 @@ void launch_as(const qmat_lora_args& a, const LoraPlan& p, float* z, hipStream_t
   if (p.few) {
     hipLaunchKernelGGL((lora_few_kernel<T>),
                        dim3((unsigned)a.n_tokens, (unsigned)((a.M + p.few_rows - 1) / p.few_rows)),
-                       dim3(kFewThreads), 0, stream, a, p);
+                       dim3(kFewThreads), 2 * a.K + a.K / 8, stream, a, p);
     return;
   }
   p.token_tiles == 1 ? launch_both<T, 1>(a, p, z, stream) : launch_both<T, 2>(a, p, z, stream);

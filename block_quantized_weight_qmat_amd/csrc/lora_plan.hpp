@@ -12,6 +12,7 @@ constexpr int64_t kLoraMaxRank = 256;
 
 struct LoraPlan {
   bool few;             // one kernel, a token at a time
+  int32_t few_log2;     // log2 of its lanes of a row of b: eight ranks each
   int64_t few_rows;     // its rows of b of a workgroup
   int64_t tiles;        // of up to 16 * token_tiles tokens
   int64_t z_stride;     // numbers of z for each token: whole tiles of ranks
@@ -35,8 +36,17 @@ inline LoraPlan lora_plan(const qmat_lora_args& a) {
   LoraPlan p{};
   const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   const auto cut = [](int64_t v, int64_t lo, int64_t hi) { return (int32_t)(v > hi ? hi > lo ? hi : lo : v < lo ? lo : v); };
-  p.few = a.max_q <= 4 && a.rank * a.K <= 1 << 18;
+  // A token at a time reads an adapter's a once more for every 256th of all rows of b, but
+  // is one short launch; tiles read it once for 32 tokens of a sequence, but a
+  // decode batch has one token in each. (4096 x 4096 unless said; us, a token at a time against
+  // tiles.) Rank 16, 64 / 256 sequences of 1 token: 8 / 10 against 20 / 37, 16 of 4, 8 and 16:
+  // 7, 9, 10 against 11, 11, 12, 64 of 8: 21 against 19; rank 64, 1 token: 9 against 11,
+  // 64: 14 against 15; 11008 x 4096, rank 64, 1 token: 22 against 13, 64: 24 against 29.
+  const int64_t elems = a.rank * a.K;
+  p.few = a.K <= 1 << 14 && (a.max_q <= 4 ? elems <= 1 << 18 || (elems <= 1 << 20 && a.n_tokens >= 32)
+                                          : a.n_tokens * elems <= 1 << 24);
   if (p.few) {
+    while (8 << p.few_log2 < a.rank) ++p.few_log2;
     // a workgroup for each CU, and whole threads of rows
     const int64_t splits = up(256, a.n_tokens > 0 ? a.n_tokens : 1);
     p.few_rows = up(up(a.M, splits), 1024) * 1024;

@@ -29,23 +29,6 @@ __device__ __forceinline__ void turn(int32_t pos, double freq, float* s, float* 
   sincospif((float)(2.0 * (turns - rint(turns))), s, c);
 }
 
-template <int kCtrl>
-__device__ __forceinline__ float dpp_add(float v) {
-  return v + __builtin_bit_cast(
-                 float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, true));
-}
-
-// The sum over 1 << log2_lanes neighbouring lanes, in each of them.
-__device__ __forceinline__ float group_sum(float v, int log2_lanes) {
-  if (log2_lanes > 0) v = dpp_add<0xB1>(v);   // neighbours
-  if (log2_lanes > 1) v = dpp_add<0x4E>(v);   // pairs of a quad
-  if (log2_lanes > 2) v = dpp_add<0x141>(v);  // quads, mirrored in 8 lanes
-  if (log2_lanes > 3) v = dpp_add<0x140>(v);  // eights, mirrored in 16
-  if (log2_lanes > 4) v += shfl_xor_f(v, 16);
-  if (log2_lanes > 5) v += shfl_xor_f(v, 32);
-  return v;
-}
-
 // log2_lanes: lanes of a head; parts: groups of lanes that share a token.
 template <typename In, typename Out>
 __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_t token0,

@@ -374,6 +374,7 @@ static void lora_cases() {
   EXPECT(qmat_lora(&x, NULL, 0, NULL), QMAT_OK, 1);
   x = lora_good();
   x.max_q = 30;
+  x.n_tokens = 5000;
   const int64_t n = qmat_lora_workspace_bytes(&x);
   if (n <= 0) ++failures;
   EXPECT(qmat_lora(&x, NULL, n, NULL), QMAT_E_WORKSPACE, 0);

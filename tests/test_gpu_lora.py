@@ -15,6 +15,10 @@ import oracle
 
 pytestmark = pytest.mark.gpu
 
+# Rows of this many elements are too long for the kernel that takes a token at a time, so the one
+# for tiles of tokens takes them however few tokens there are; 513 blocks are no whole chunks.
+LONG = 16416
+
 
 @pytest.fixture(scope="module")
 def lib():
@@ -103,6 +107,29 @@ def test_sizes(lib, rank, K, M, max_q, dtype):
     Case([1, 3, 1, 30, 2], [0, 2, 1, 0, 2], 3, rank, K, M, dtype, seed=rank + M).check(lib, max_q=max_q)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("max_q", [1, 17])
+@pytest.mark.parametrize("rank,M", [(8, 1), (16, 257), (24, 100), (32, 31), (40, 64), (64, 600), (72, 33), (136, 20), (256, 130)])
+def test_sizes_in_tiles(lib, rank, M, max_q, dtype):
+    """Tiles of 16 and of 32 tokens; sequences that start and end inside one."""
+    Case([1, 3, 41, 2, 17], [0, 2, 1, 0, 2], 3, rank, LONG, M, dtype, seed=rank + M, tail=2).check(lib, max_q=max_q)
+
+
+@pytest.mark.parametrize("K", [32 * 8 * 64 + 32 * n for n in (1, 2, 7, 8, 9, 63)])
+def test_ends_of_rows(lib, K):
+    """Chunks of eight blocks of which the last holds 1 to 8; the last row's end is the buffer's."""
+    c = Case([20, 13], [1, 0], 2, 16, K, 40)
+    first = c.check(lib)
+    assert first.shape == (33, 40)
+    Case([1, 1], [1, 0], 2, 64, K, 40, "f16").check(lib)
+
+
+@pytest.mark.parametrize("lens,rank,K", [([700, 1, 300, 5], 24, 1056), ([4096], 8, 512), ([1] * 500, 64, 11008), ([1000, 64, 1, 1, 1, 999], 64, 1024)])
+def test_many_tokens(lib, lens, rank, K):
+    r = np.random.default_rng(len(lens))
+    Case(lens, r.integers(-1, 4, len(lens)).tolist(), 4, rank, K, 72, seed=rank, tail=1).check(lib)
+
+
 @pytest.mark.parametrize("seqs", [1, 2, 15, 16, 17, 64, 200])
 def test_decode(lib, seqs):
     r = np.random.default_rng(seqs)
@@ -114,6 +141,7 @@ def test_all_adapters_different(lib, max_q):
     """As many adapters as tokens, in one tile and over several; none of them shares a column."""
     Case([1] * 70, list(range(70)), 70, 8, 256, 70).check(lib, max_q=max_q)
     Case([1] * 70, list(range(69, -1, -1)), 70, 24, 96, 36, "f16").check(lib, max_q=max_q)
+    Case([1] * 70, list(range(70)), 70, 8, LONG, 36).check(lib, max_q=max_q)
 
 
 @pytest.mark.parametrize("lens", [[33], [1, 100, 1], [0, 17, 0, 0, 15, 32, 0], [509, 3, 64, 127], [0, 0]])
@@ -123,10 +151,11 @@ def test_prompts(lib, lens, dtype):
     Case(lens, r.integers(0, 3, len(lens)).tolist(), 3, 32, 1056, 132, dtype, tail=3).check(lib)
 
 
+@pytest.mark.parametrize("K", [160, LONG])
 @pytest.mark.parametrize("max_q", [1, 64])
-def test_ranks_and_strangers(lib, max_q):
+def test_ranks_and_strangers(lib, max_q, K):
     """Smaller ranks, rank 0, numbers outside the range, adapters that are not there, tokens of no sequence."""
-    c = Case([2, 1, 20, 5, 1, 1, 3], [0, 1, 2, 3, -1, 4, 5], 5, 48, 224, 65, ranks=[48, 5, 17, 0, 1000], tail=4, lead=3)
+    c = Case([2, 1, 20, 5, 1, 1, 3], [0, 1, 2, 3, -1, 4, 5], 5, 48, K, 65, ranks=[48, 5, 17, 0, 1000], tail=4, lead=3)
     c.check(lib, max_q=max_q)
     c.ranks = [-4, 1, 33, 16, 8]
     c.check(lib, max_q=max_q, in_place=True, pad=3)
@@ -135,12 +164,13 @@ def test_ranks_and_strangers(lib, max_q):
     c.check(lib, max_q=max_q, pad=4)
 
 
+@pytest.mark.parametrize("K", [160, LONG])
 @pytest.mark.parametrize("max_q", [1, 64])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-def test_others_stay_clean(lib, dtype, max_q):
+def test_others_stay_clean(lib, dtype, max_q, K):
     """NaN and infinities of another adapter, of another token, past a rank and of base stay where they are."""
     import torch
-    c = Case([1, 1, 6, 9, 3], [0, 1, 2, 0, -1], 3, 32, 160, 50, dtype, ranks=[20, 32, 32])
+    c = Case([1, 1, 6, 9, 3], [0, 1, 2, 0, -1], 3, 32, K, 50, dtype, ranks=[20, 32, 32])
     want = c.run(lib, max_q=max_q).cpu()
     c.a[0, 20:] = float("nan")
     c.b[0, :, 20:] = float("inf")
@@ -158,33 +188,36 @@ def test_others_stay_clean(lib, dtype, max_q):
     assert torch.equal(got[18][keep], want[18][keep]) and torch.isnan(got[18, 2]).item()
 
 
+@pytest.mark.parametrize("K", [160, LONG])
 @pytest.mark.parametrize("max_q", [1, 64])
-def test_row_strides(lib, max_q):
+def test_row_strides(lib, max_q, K):
     """Slices of a wider product, 16-byte rows or not; rows behind the last token of any sequence stay."""
     for M, pad in ((64, 64), (64, 1), (63, 1), (30, 2)):
-        Case([5, 1, 12], [1, 0, 1], 2, 16, 128, M, tail=2).check(lib, max_q=max_q, in_place=True, pad=pad)
-        Case([5, 1, 12], [1, 0, 1], 2, 16, 128, M, tail=2).check(lib, max_q=max_q, pad=pad)
+        Case([5, 1, 12], [1, 0, 1], 2, 16, K, M, tail=2).check(lib, max_q=max_q, in_place=True, pad=pad)
+        Case([5, 1, 12], [1, 0, 1], 2, 16, K, M, tail=2).check(lib, max_q=max_q, pad=pad)
 
 
+@pytest.mark.parametrize("K", [160, LONG])
 @pytest.mark.parametrize("max_q", [1, 64])
-def test_nothing(lib, max_q):
+def test_nothing(lib, max_q, K):
     """No adapters, no sequences, no elements, no rows, no tokens."""
     import torch
-    Case([3, 1], [0, -1], 0, 8, 64, 20).check(lib, max_q=max_q)
-    Case([], [], 2, 8, 64, 20, tail=5).check(lib, max_q=max_q)
+    Case([3, 1], [0, -1], 0, 8, K, 20).check(lib, max_q=max_q)
+    Case([], [], 2, 8, K, 20, tail=5).check(lib, max_q=max_q)
     Case([3, 1], [0, 1], 2, 8, 0, 20).check(lib, max_q=max_q)
-    assert Case([3, 1], [0, 1], 2, 8, 64, 0).run(lib, max_q=max_q).shape == (4, 0)
-    c = Case([0], [0], 1, 8, 64, 20)
+    assert Case([3, 1], [0, 1], 2, 8, K, 0).run(lib, max_q=max_q).shape == (4, 0)
+    c = Case([0], [0], 1, 8, K, 20)
     assert c.n == 0 and c.run(lib, max_q=max_q).shape == (0, 20)
 
 
+@pytest.mark.parametrize("K", [160, LONG])
 @pytest.mark.parametrize("max_q", [1, 64])
-def test_bad_starts(lib, max_q):
+def test_bad_starts(lib, max_q, K):
     """Starts that decrease or lie outside the tokens harm no memory, and no token of a sound sequence behind."""
-    c = Case([4, 4, 4], [0, 1, 0], 2, 16, 64, 40)
+    c = Case([4, 4, 4], [0, 1, 0], 2, 16, K, 40)
     c.starts = [-7, 4, 8, 2 ** 31 - 1]
     got = c.run(lib, max_q=max_q)
-    sound = Case([4, 4, 4], [0, 1, 0], 2, 16, 64, 40).run(lib, max_q=max_q)
+    sound = Case([4, 4, 4], [0, 1, 0], 2, 16, K, 40).run(lib, max_q=max_q)
     import torch
     assert torch.equal(got, sound)
     c.starts = [9, 3, -1, 0]
@@ -213,11 +246,12 @@ def test_same_bits_again(lib):
     import ctypes
     import torch
     from block_quantized_weight_qmat_amd import binding
-    for lens, max_q in (([1] * 40, 1), ([100, 7, 30], 100)):
+    for lens, max_q in (([1] * 40, 1), ([100, 7, 300], 300)):
         c = Case(lens, [i % 3 for i in range(len(lens))], 3, 64, 2048, 200)
         first = c.run(lib, max_q=max_q)
         args = binding.LoraArgs(2, None, None, None, None, None, None, None, None, None, 200, 200, c.n, len(lens), 3, 64, 200, 2048, max_q)
         need = binding.load_library().qmat_lora_workspace_bytes(ctypes.byref(args))
+        assert (need > 0) == (max_q > 1)
         ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN
         assert torch.equal(c.run(lib, max_q=max_q, workspace=ws), first)
         ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
