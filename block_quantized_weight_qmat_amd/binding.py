@@ -827,12 +827,10 @@ def page_step(kv_len: torch.Tensor, add: torch.Tensor, page_table: torch.Tensor,
         raise ValueError("max_tokens must not be negative")
     if q_start is None and slots is None and positions is None and token_seq is None and \
             status is None:
-        # one allocation; what kv_store takes starts at 16 bytes
-        wide = (max_tokens + 3) // 4 * 4
-        rest = wide - max_tokens
-        buf = torch.empty(3 * wide + 2 * n_seqs + 1, dtype=torch.int32, device=device)
-        slots, _, positions, _, token_seq, _, q_start, status = buf.split(
-            (max_tokens, rest, max_tokens, rest, max_tokens, rest, n_seqs + 1, n_seqs))
+        # one allocation, slots in front: kv_store takes them at 16 bytes
+        buf = torch.empty(3 * max_tokens + 2 * n_seqs + 1, dtype=torch.int32, device=device)
+        slots, positions, token_seq, q_start, status = buf.split_with_sizes(
+            (max_tokens, max_tokens, max_tokens, n_seqs + 1, n_seqs))
     else:
         q_start = _ints(q_start, "q_start", n_seqs + 1, device)
         slots = _ints(slots, "slots", max_tokens, device)
