@@ -312,6 +312,7 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(qmat_lora_args 
 
 // ------------------------------------------------------------- y = base + s b z
 
+constexpr int kMaxGridY = 65535;
 constexpr int kUpMT = 2;  // tiles of 16 rows of b that a wave has at a time
 constexpr int kUpThreads = 512;
 constexpr int kUpRows = 16 * kUpMT * (kUpThreads / kWave);  // of a workgroup at a time
@@ -360,7 +361,9 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(qmat_lora_args a, L
   extern __shared__ __attribute__((aligned(16))) __bf16 zs[];  // [3][token][pitch]
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
   const int wide = plan.up_ranks, pitch = wide + 8, plane = 16 * kTT * pitch, M = (int)a.M;
-  const Tile tile = tile_of<16 * kTT>(a, blockIdx.x);
+  // neighbouring workgroups: parts of M, so that (of eight) one XCD reads one part of b
+  const int m_first = (int)(blockIdx.x * plan.up_rows);
+  const Tile tile = tile_of<16 * kTT>(a, (int)(blockIdx.z * kMaxGridY + blockIdx.y));
   const bool has = tile.adapter.id >= 0;
   if (tile.t0 >= tile.t1 || (!has && a.base == a.y)) return;  // the workgroup together
   // a lane has row m0 + 16 mt + col of tokens 16 tt + 4 g + e: offsets from token
@@ -375,9 +378,9 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(qmat_lora_args a, L
   };
   const T* const b = static_cast<const T*>(a.b) + (int64_t)(has ? tile.adapter.id : 0) * M * a.rank;
   const int rank = has ? tile.adapter.rank : 0;
-  const int m_end = (int)((blockIdx.y + 1) * plan.up_rows < M ? (blockIdx.y + 1) * plan.up_rows : M);
+  const int m_end = m_first + plan.up_rows < M ? (int)(m_first + plan.up_rows) : M;
   bool first = true;
-  for (int m0 = (int)(blockIdx.y * plan.up_rows) + 16 * kUpMT * wave; first || m0 < m_end; m0 += kUpRows) {
+  for (int m0 = m_first + 16 * kUpMT * wave; first || m0 < m_end; m0 += kUpRows) {
     f32x4 v[kTT][kUpMT] = {};
 #pragma unroll
     for (int tt = 0; tt < kTT; ++tt)
@@ -410,10 +413,13 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(qmat_lora_args a, L
 #pragma unroll
       for (int mt = 0; mt < kUpMT; ++mt) {  // rows and ranks past the last: the last
         const int m = m0 + 16 * mt + col;
-        vec8 x = *reinterpret_cast<const vec8*>(b + (uint32_t)(m < M ? m : M - 1) * a.rank + (r < a.rank ? r : a.rank - 8));
+        u32x4 x = *reinterpret_cast<const u32x4*>(b + (uint32_t)(m < M ? m : M - 1) * a.rank + (r < a.rank ? r : a.rank - 8));
+        if (r0 + 32 > rank) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = r + e < rank ? x[e] : (T)0.0f;
-        split(x, part[mt]);
+          for (int e = 0; e < 8; e += 2)
+            x[e / 2] &= (r + e < rank ? 0xFFFFu : 0u) | (r + e + 1 < rank ? 0xFFFF0000u : 0u);
+        }
+        split(__builtin_bit_cast(vec8, x), part[mt]);
       }
 #pragma unroll
       for (int tt = 0; tt < kTT; ++tt)
@@ -461,6 +467,7 @@ __device__ __forceinline__ float dot8x8(bf16x8 a, bf16x8 b) {
 
 constexpr int kFewThreads = 1024;
 constexpr int kFewWaves = kFewThreads / kWave;
+
 // A few tokens of each sequence and small adapters: one launch and no
 // workspace. A workgroup has one token and plan.few_rows rows of b; it computes
 // all of z for itself (a wave has a rank's row of a, side by side), since a pass
@@ -485,7 +492,7 @@ __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(qmat_lora_args a,
   const uint8_t* const x = static_cast<const uint8_t*>(a.x_q8) + t * (K / 32 * 34);
   float* const scales = reinterpret_cast<float*>(xs + 2 * K);
 #pragma nounroll
-  for (int k = 8 * threadIdx.x; k < K; k += 8 * kFewThreads) {
+  for (int k = 8 * threadIdx.x; k < K && a.n_adapters > 0; k += 8 * kFewThreads) {
     const uint8_t* blk = x + (k >> 5) * 34;
     const u32x2_a2 q = *reinterpret_cast<const u32x2_a2*>(blk + 2 + (k & 31));
     *reinterpret_cast<vec8*>(xs + 2 * k) = codes<T>(q.x, q.y);
@@ -580,9 +587,10 @@ void launch_both(const qmat_lora_args& a, const LoraPlan& p, float* z, hipStream
     p.rank_tiles == 1   ? launch_down<T, 1, kTT>(a, p, z, stream)
     : p.rank_tiles == 2 ? launch_down<T, 2, kTT>(a, p, z, stream)
                         : launch_down<T, 4, kTT>(a, p, z, stream);
-  hipLaunchKernelGGL((lora_up_kernel<T, kTT>),
-                     dim3((unsigned)p.tiles, (unsigned)((a.M + p.up_rows - 1) / p.up_rows)), dim3(kUpThreads),
-                     3 * 16 * kTT * (p.up_ranks + 8) * 2, stream, a, p, z);
+  const int64_t rows = p.tiles < kMaxGridY ? p.tiles : kMaxGridY;
+  const dim3 grid((unsigned)((a.M + p.up_rows - 1) / p.up_rows), (unsigned)rows, (unsigned)((p.tiles + rows - 1) / rows));
+  hipLaunchKernelGGL((lora_up_kernel<T, kTT>), grid, dim3(kUpThreads), 3 * 16 * kTT * (p.up_ranks + 8) * 2, stream,
+                     a, p, z);
 }
 
 template <typename T>

@@ -41,7 +41,7 @@ int check_lora(const qmat_lora_args& a) {
       a.rank % 8 != 0)
     return QMAT_E_SHAPE;
   if (a.base_stride < a.M || a.base_stride > kMaxLoraStride || a.y_stride < a.M ||
-      a.y_stride > kMaxLoraStride)
+      a.y_stride > kMaxLoraStride || (a.n_tokens > 0 && a.base == a.y && a.base_stride != a.y_stride))
     return QMAT_E_SHAPE;
   return QMAT_OK;
 }
@@ -101,6 +101,11 @@ int qmat_norm(const qmat_norm_args* args, void* stream) {
                !rows_ok(a.n, a.K, a.residual_out_stride, size))) ||
       (a.rows != nullptr && !rows_ok(a.n, a.K, a.rows_stride, size)))
     return QMAT_E_SHAPE;
+  // in place: row upon row
+  if (a.n > 0 && sum && ((a.residual_out == a.residual && a.residual_out_stride != a.residual_stride) ||
+              (a.residual_out == a.x && a.residual_out_stride != a.x_stride)))
+    return QMAT_E_SHAPE;
+  if (a.n > 0 && a.rows != nullptr && a.rows == a.x && a.rows_stride != a.x_stride) return QMAT_E_SHAPE;
   if (a.n == 0 || a.K == 0) return QMAT_OK;
   if (a.rows == nullptr && a.q8 == nullptr) return QMAT_E_NULL;
   int rc = check_rows(a.x, a.x_stride, size);
@@ -135,7 +140,8 @@ int qmat_rope(const qmat_rope_args* args, void* stream) {
   const int64_t in = dtype_bytes(a.in_dtype), out = dtype_bytes(a.out_dtype);
   for (const auto& x : both)
     if (x.heads > 0 && (!rows_ok(a.n, x.heads * a.head_dim, x.in_stride, in) ||
-                        !rows_ok(a.n, x.heads * a.head_dim, x.out_stride, out)))
+                        !rows_ok(a.n, x.heads * a.head_dim, x.out_stride, out) ||
+                        (a.n > 0 && x.in == x.out && (a.in_dtype != a.out_dtype || x.in_stride != x.out_stride))))
       return QMAT_E_SHAPE;
   if (a.n == 0 || a.heads + a.kv_heads == 0) return QMAT_OK;
   int rc = QMAT_OK;

@@ -559,7 +559,8 @@ int qmat_embed(int fmt, int dtype, const void *blocks, const int32_t *ids, void 
  *   x, residual, residual_out, rows: n rows of dtype, their strides in
  *     elements (>= K, whole multiples of 16 bytes). residual and residual_out
  *     are both given or both NULL. residual_out may be residual or x itself,
- *     and rows may be x itself, with the same stride; nothing else overlaps.
+ *     and rows may be x itself, with the same stride (QMAT_E_SHAPE for another);
+ *     nothing else overlaps.
  *     Elements of a row past K are left as they were.
  *   weight: fp32 [K]. eps: finite, >= 0 (QMAT_E_SHAPE).
  *   rows, q8: at least one of them (QMAT_E_NULL). q8: n rows of
@@ -602,7 +603,8 @@ int qmat_norm(const qmat_norm_args *args, void *stream);
  *   q, k: [n] tokens, q_stride and k_stride elements apart, of heads and
  *     kv_heads heads of head_dim elements of in_dtype. Either may have no
  *     heads (and be NULL). q_out, k_out: the same of out_dtype; q_out may be q
- *     itself (k_out k) with the same type and stride. Nothing else overlaps.
+ *     itself (k_out k) with the same type and stride (QMAT_E_SHAPE for others).
+ *     Nothing else overlaps.
  *   positions: DEVICE int32 [axes][n], pos_stride apart. freq: DEVICE fp64
  *     [rot_dim / 2], radians for each position. axis: DEVICE int32
  *     [rot_dim / 2], NULL: all 0. q_norm, k_norm: fp32 [head_dim] or NULL.
@@ -719,11 +721,14 @@ int qmat_page_step(const qmat_page_args *args, void *workspace, int64_t workspac
  *   adapter: DEVICE int32 [n_seqs]; q_start: DEVICE int32 [n_seqs + 1], not
  *     decreasing. Values outside [0, n_tokens] name no token.
  *   y, base: fp32 rows [n_tokens][M], strides in elements (>= M). base may be
- *     y itself with the same stride: then only tokens with an adapter are touched.
+ *     y itself with the same stride (QMAT_E_SHAPE for another): then only tokens
+ *     with an adapter are touched.
  *   Arithmetic: products of a code and an element of a are exact, a block's
- *   sum is scaled and added in fp32; the second product is fp32. Other
- *   requests' adapters and activations have no effect on a token, whatever
- *   their values (infinities and NaN included).
+ *   sum is scaled and added in fp32; the second product takes that sum to
+ *   2^-27 of itself and adds up in fp32. Elements below their type's normal range may
+ *   count as zero. A token whose adapter (within its rank) or activations hold an infinity or a
+ *   NaN has no finite result in some or all elements; other
+ *   requests' adapters and activations have no effect on it.
  *   Limits (QMAT_E_SHAPE): K a multiple of 32, up to 2^20; rank a multiple of
  *   8, 8 to 256; n_tokens and n_seqs up to 2^20, M up to 2^23, n_adapters and
  *   the strides up to 2^24; max_q >= 0.

@@ -63,7 +63,9 @@ static qmat_norm_args norm_good() {
   a.dtype = QMAT_BF16;
   a.eps = 1e-6;
   a.x = a.residual = A;
-  a.residual_out = a.rows = a.q8 = A;
+  a.residual_out = A + 0x1000;
+  a.rows = A + 0x2000;
+  a.q8 = A + 0x3000;
   a.weight = (const float*)A;
   a.x_stride = a.residual_stride = a.residual_out_stride = a.rows_stride = 64;
   a.n = 3;
@@ -113,7 +115,20 @@ static void norm_cases() {
   NORM(rows_stride, 66, QMAT_E_ALIGN, 0);
   NORM(n, 0, QMAT_OK, 0);
   NORM(K, 0, QMAT_OK, 0);
-  qmat_norm_args x = norm_good();
+  qmat_norm_args x = norm_good();  // in place: with the same stride alone
+  x.residual_out = A;
+  EXPECT(qmat_norm(&x, NULL), QMAT_OK, 1);
+  x.residual_out_stride = 128;
+  EXPECT(qmat_norm(&x, NULL), QMAT_E_SHAPE, 0);
+  x.x = A + 0x4000;
+  EXPECT(qmat_norm(&x, NULL), QMAT_E_SHAPE, 0);
+  x.residual = A + 0x5000;
+  EXPECT(qmat_norm(&x, NULL), QMAT_OK, 1);
+  x.rows = A + 0x4000;
+  EXPECT(qmat_norm(&x, NULL), QMAT_OK, 1);
+  x.rows_stride = 72;
+  EXPECT(qmat_norm(&x, NULL), QMAT_E_SHAPE, 0);
+  x = norm_good();
   x.rows = x.q8 = NULL;
   EXPECT(qmat_norm(&x, NULL), QMAT_E_NULL, 0);
   x = norm_good();
@@ -128,7 +143,8 @@ static qmat_rope_args rope_good() {
   a.out_dtype = QMAT_F16;
   a.axes = 3;
   a.q = a.k = A;
-  a.q_out = a.k_out = A;
+  a.q_out = A + 0x10000;
+  a.k_out = A + 0x20000;
   a.positions = a.axis = S;
   a.freq = (const double*)A;
   a.q_norm = a.k_norm = (const float*)A;
@@ -194,7 +210,15 @@ static void rope_cases() {
   ROPE(freq, (const double*)(A + 8), QMAT_E_ALIGN, 0);
   ROPE(k_norm, (const float*)(A + 4), QMAT_E_ALIGN, 0);
   ROPE(n, 0, QMAT_OK, 0);
+  ROPE(q_out, A, QMAT_E_SHAPE, 0);  // in place, of another type
+  ROPE(k_out, A, QMAT_E_SHAPE, 0);
   qmat_rope_args x = rope_good();
+  x.out_dtype = x.in_dtype;
+  x.q_out = x.k_out = A;
+  EXPECT(qmat_rope(&x, NULL), QMAT_OK, 1);
+  x.k_out_stride = 2048;
+  EXPECT(qmat_rope(&x, NULL), QMAT_E_SHAPE, 0);
+  x = rope_good();
   x.kv_heads = 0;  // no keys: nothing of them is looked at
   x.k = NULL;
   x.k_out = NULL;
@@ -291,7 +315,7 @@ static qmat_lora_args lora_good() {
   a.dtype = QMAT_BF16;
   a.x_q8 = a.a = a.b = A;
   a.scale = a.base = (const float*)A;
-  a.y = (float*)A;
+  a.y = (float*)(A + 0x10000);
   a.ranks = a.adapter = a.q_start = S;
   a.base_stride = a.y_stride = 100;
   a.n_tokens = 5;
@@ -363,6 +387,11 @@ static void lora_cases() {
   LORA(n_tokens, 0, QMAT_OK, 0);
   LORA(M, 0, QMAT_OK, 0);
   qmat_lora_args x = lora_good();
+  x.y = (float*)A;  // in place: with the same stride alone
+  EXPECT(lora(x), QMAT_OK, 1);
+  x.y_stride = 104;
+  EXPECT(lora(x), QMAT_E_SHAPE, 0);
+  x = lora_good();
   x.n_adapters = x.n_seqs = 0;  // a copy of base
   x.x_q8 = x.a = x.b = x.scale = NULL;
   x.ranks = x.adapter = x.q_start = NULL;

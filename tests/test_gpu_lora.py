@@ -211,6 +211,33 @@ def test_nothing(lib, max_q, K):
 
 
 @pytest.mark.parametrize("K", [160, LONG])
+def test_null_where_nothing_is_read(lib, K):
+    """Through the C ABI: without adapters their buffers and the activations may be NULL; base is copied."""
+    import ctypes
+    import torch
+    from block_quantized_weight_qmat_amd import binding
+    base, y = torch.randn(40, 24, device="cuda"), torch.zeros(40, 24, device="cuda")
+    adapter, starts = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.tensor([0, 30, 40], dtype=torch.int32, device="cuda")
+    for seqs in (2, 0):
+        y.zero_()
+        args = binding.LoraArgs(1, None, None, None, None, None, adapter.data_ptr() if seqs else None, starts.data_ptr() if seqs else None,
+                                base.data_ptr(), y.data_ptr(), 24, 24, 40, seqs, 0, 16, 24, K, 30)
+        n = binding.load_library().qmat_lora_workspace_bytes(ctypes.byref(args))
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+        assert binding.load_library().qmat_lora(ctypes.byref(args), ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(y, base)
+
+
+@pytest.mark.parametrize("K", [160, LONG])
+def test_many_empty_sequences(lib, K):
+    """More sequences than one probe of 64 lanes tells apart, and than a grid's rows; all but a few without tokens."""
+    lens = [0] * 70001
+    for i, n in ((0, 2), (63, 40), (64, 1), (4095, 5), (4096, 33), (69999, 7), (70000, 1)):
+        lens[i] = n
+    Case(lens, [i % 3 for i in range(len(lens))], 3, 16, K, 20, tail=3).check(lib, max_q=40)
+
+
+@pytest.mark.parametrize("K", [160, LONG])
 @pytest.mark.parametrize("max_q", [1, 64])
 def test_bad_starts(lib, max_q, K):
     """Starts that decrease or lie outside the tokens harm no memory, and no token of a sound sequence behind."""
