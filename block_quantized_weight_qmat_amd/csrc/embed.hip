@@ -100,7 +100,8 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t h, float s, float do
   }
 }
 
-template <int kFmt, typename T>
+// kStream: results are written past the caches.
+template <int kFmt, bool kStream, typename T>
 __global__ __launch_bounds__(kThreads) void embed_kernel(const uint8_t* __restrict__ blocks,
                                                          const int32_t* __restrict__ ids,
                                                          T* __restrict__ out, int64_t out_stride,
@@ -123,20 +124,36 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const uint8_t* __restri
       unpack<kFmt>(p.w1, p.h1, p.s1, p.down, e1, v + 4);
     }
     T* dst = out + row * out_stride + 32 * group;
-    put16<false>(dst + e0, v);
-    if constexpr (kWide) put16<false>(dst + e1, v + 4);
+    put16<kStream>(dst + e0, v);
+    if constexpr (kWide) put16<kStream>(dst + e1, v + 4);
   }
 }
 
 constexpr int64_t kMaxGrid = 1 << 22;
 
+// 16-bit results above half of the last-level cache's 256 MB, most of which is gone
+// before somebody reads it, are written past the caches: 70000 rows of 1024, Q6_K to bf16, 66 us
+// through them, 45 past them; 20000 of 4096, Q4_0: 68 and 43. Smaller ones stay for their
+// reader (16384 rows of 1024 with a copy of the result behind: 24.6 us, 26.0 past them).
+constexpr int64_t kStreamBytes = 128 << 20;
+
+template <int kFmt, bool kStream, typename T>
+void launch_to(const void* blocks, const int32_t* ids, void* out, int64_t out_stride, int64_t n,
+               int64_t rows, int64_t K, hipStream_t stream) {
+  const int64_t wgs = (n * (K / 32) + kThreads / 4 - 1) / (kThreads / 4);
+  hipLaunchKernelGGL((embed_kernel<kFmt, kStream, T>), dim3((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid)),
+                     dim3(kThreads), 0, stream, static_cast<const uint8_t*>(blocks), ids,
+                     static_cast<T*>(out), out_stride, n, rows, (int)(K / 32));
+}
+
 template <int kFmt, typename T>
 void launch_as(const void* blocks, const int32_t* ids, void* out, int64_t out_stride, int64_t n,
                int64_t rows, int64_t K, hipStream_t stream) {
-  const int64_t wgs = (n * (K / 32) + kThreads / 4 - 1) / (kThreads / 4);
-  hipLaunchKernelGGL((embed_kernel<kFmt, T>), dim3((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid)),
-                     dim3(kThreads), 0, stream, static_cast<const uint8_t*>(blocks), ids,
-                     static_cast<T*>(out), out_stride, n, rows, (int)(K / 32));
+  if constexpr (sizeof(T) == 2) {
+    if (n * K * (int64_t)sizeof(T) > kStreamBytes)
+      return launch_to<kFmt, true, T>(blocks, ids, out, out_stride, n, rows, K, stream);
+  }
+  launch_to<kFmt, false, T>(blocks, ids, out, out_stride, n, rows, K, stream);
 }
 
 template <int kFmt>

@@ -106,3 +106,17 @@ def test_nothing_to_do(lib):
     assert lib.embed("q8_0", t, 32, torch.zeros(0, dtype=torch.int32, device="cuda")).shape == (0, 32)
     got = lib.embed("q8_0", t[:0], 32, torch.zeros(3, dtype=torch.int32, device="cuda"), dtype=torch.float16)
     assert got.shape == (3, 32) and not got.any().item()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_large_results(lib, dtype):
+    """Results that are written past the caches are those of smaller calls."""
+    import torch
+    fmt, K, n = "q6_k", 1024, 70001  # 143 MB
+    packed, _ = table(fmt, 50, K, 8)
+    dev = torch.from_numpy(packed).cuda()
+    ids = torch.randint(-1, 51, (n,), dtype=torch.int32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    got = lib.embed(fmt, dev, K, ids, dtype=torch_type(dtype))
+    for at in range(0, n, 20000):
+        part = ids[at:at + 20000].clone()
+        assert torch.equal(got[at:at + 20000], lib.embed(fmt, dev, K, part, dtype=torch_type(dtype)))
