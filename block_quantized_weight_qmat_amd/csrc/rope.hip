@@ -4,16 +4,20 @@
 //   theta = positions[axis[i]][t] freq[i],  (a, b) -> (a cos - b sin, b cos + a sin)
 //
 // A copy with eight multiplications for four elements: bound by HBM bandwidth
-// where there are many tokens, by one chain of loads where there are few. What
-// could bound it instead are the angles: in 64 bits (fp32 knows an angle of
-// 10^6 to 0.03, fp64 to 2^-34), a few dozen instructions for each pair.
+// where there are many tokens, by one chain of loads where there are few. 8191
+// tokens of 40 heads of 128, bf16, on 3 axes: 32 us, 5.2 TB/s, a large copy's rate;
+// 64 tokens: 3.8 us, most of it the fetch of the code, of the axes, of the positions.
+// What could bound it instead are the angles: in 64 bits (fp32 knows an angle of
+// 10^6 to 0.03, fp64 to 2^-34), about a hundred instructions each.
 //
 // Work split: a lane has eight elements of a head, four pairs (elements i..i+3
 // and i+rot/2.., or eight neighbours), and goes through several heads of one
-// token, so that an angle's sine and cosine are computed once for all of them.
-// A head takes the lanes of the next power of two (16 for 128 elements), a
+// token. A head takes the lanes of the next power of two (16 for 128 elements), a
 // workgroup 256 lanes; how many groups of lanes share a token's heads follows
-// from how many are needed to fill the GPU.
+// from how many are needed to fill the GPU. A workgroup computes the sines and
+// cosines of its tokens once, a thread for each, and shares them in LDS: where each lane
+// had its own four, all waves began with 5 us of arithmetic without a load on its
+// way (8191 tokens 43 us, 1024 10.0 instead of 7.9).
 #include "kv_device.hpp"
 #include "qmat_launch.hpp"
 
@@ -21,6 +25,7 @@ namespace qmat {
 namespace {
 
 constexpr int kThreads = 256;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // Sine and cosine of pos * freq (radians): whole turns are taken off in 64
 // bits, the rest (at most half a turn) is exact to 2^-25 in fp32.
@@ -33,6 +38,9 @@ __device__ __forceinline__ void turn(int32_t pos, double freq, float* s, float* 
 template <typename In, typename Out>
 __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_t token0,
                                                         int log2_lanes, int parts) {
+  // cosines and sines of the workgroup's tokens: with one part a token for each group of
+  // lanes, with more at most half as many and one, never more than its groups
+  __shared__ __attribute__((aligned(16))) f32x2 turns[4 * kThreads];
   const int u = threadIdx.x & ((1 << log2_lanes) - 1);
   const uint32_t group = (blockIdx.x * kThreads + threadIdx.x) >> log2_lanes;
   const uint32_t nth = group / (uint32_t)parts;
@@ -56,15 +64,31 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_
   };
   float next[8] = {};
   load(part, next);  // on its way during the angles; then always one head ahead
+  const uint32_t per = kThreads >> log2_lanes, nth0 = blockIdx.x * per / (uint32_t)parts;
+  const int angles = (int)((blockIdx.x * per + per - 1) / (uint32_t)parts - nth0 + 1) * pairs;
+#pragma nounroll
+  for (int i = threadIdx.x; i < angles; i += kThreads) {
+    const int tok = i / pairs, pair = i - tok * pairs;
+    const int64_t t = token0 + nth0 + tok;
+    f32x2 cs{1.0f, 0.0f};
+    if (t < a.n) {
+      const int ax = a.axis == nullptr ? 0 : a.axis[pair];
+      if (ax >= 0 && ax < a.axes) {
+        float s, c;
+        turn(a.positions[ax * a.pos_stride + t], a.freq[pair], &s, &c);
+        cs = f32x2{c, s};
+      }
+    }
+    turns[i] = cs;
+  }
+  __syncthreads();
   float sn[4], cs[4];
+  if (turned) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    sn[i] = 0.0f;
-    cs[i] = 1.0f;
-    if (live && turned) {
-      const int ax = a.axis == nullptr ? 0 : a.axis[4 * u + i];
-      if (ax >= 0 && ax < a.axes)
-        turn(a.positions[ax * a.pos_stride + token], a.freq[4 * u + i], &sn[i], &cs[i]);
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 v = turns[(int)(nth - nth0) * pairs + 4 * u + i];
+      cs[i] = v.x;
+      sn[i] = v.y;
     }
   }
   const float mean = 1.0f / (float)D, eps = (float)a.eps;
@@ -116,14 +140,13 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_
   }
 }
 
-// How many groups of lanes share a token's heads: enough for eight waves on each
-// SIMD (8191 x 40 heads of 128, bf16, on 3 axes: 49 us with four, 43 with eight, 50
-// with twelve), but four heads for each group, which share its angles (1024 tokens: 13.0 us
-// with one or two, 10.0 with four, 11.5 with eight), as long as that leaves a wave
-// for each SIMD (128 tokens: 4.7 us with one head, 5.0 with four).
+// How many groups of lanes share a token's heads: enough for five waves on each
+// SIMD, and five heads for a group at most (40 heads of 128, bf16. 256 tokens: 4.3 us with one
+// head, 5.1 with four; 1024: 9.0 with one, 7.9 with two, 8.6 with four; 4096: 17.6 with
+// three, 16.2 with five, 17.3 with eight; 8191: 32.2 with five, 33.1 with ten, 37 with twenty).
 constexpr int64_t kSimds = 256 * 4;
-constexpr int64_t kPerSimd = 8;
-constexpr int64_t kShared = 4;
+constexpr int64_t kPerSimd = 5;
+constexpr int64_t kShared = 5;
 constexpr int64_t kMaxLanes = 1LL << 31;  // of a launch: their number has 32 bits
 
 template <typename In, typename Out>
@@ -131,16 +154,14 @@ void launch_as(const qmat_rope_args& a, hipStream_t stream) {
   int log2_lanes = 0;
   while ((8 << log2_lanes) < a.head_dim) ++log2_lanes;
   const int64_t heads = a.heads + a.kv_heads;
-  const int64_t one = (kSimds * kWave >> log2_lanes) / a.n;  // for a wave on each SIMD
-  const int64_t most_shared = (heads + kShared - 1) / kShared;
-  int64_t parts = (kPerSimd * kSimds * kWave >> log2_lanes) / a.n;
-  if (parts > most_shared) parts = one > most_shared ? one : most_shared;
-  parts = parts < 1 ? 1 : parts > heads ? heads : parts;
+  const int64_t fill = (kPerSimd * kSimds * kWave >> log2_lanes) / a.n, least = (heads + kShared - 1) / kShared;
+  const int64_t parts = fill < least ? least : fill < heads ? fill : heads;
   const int64_t per = kThreads >> log2_lanes, most = (kMaxLanes >> log2_lanes) / parts;
   for (int64_t t = 0; t < a.n; t += most) {
-    const int64_t n = a.n - t < most ? a.n - t : most;
-    hipLaunchKernelGGL((rope_kernel<In, Out>), dim3((unsigned)((n * parts + per - 1) / per)), dim3(kThreads), 0,
-                       stream, a, t, log2_lanes, (int)parts);
+    qmat_rope_args now = a;  // the last workgroup's spare lanes have no tokens of the next launch
+    if (a.n - t > most) now.n = t + most;
+    hipLaunchKernelGGL((rope_kernel<In, Out>), dim3((unsigned)(((now.n - t) * parts + per - 1) / per)), dim3(kThreads),
+                       0, stream, now, t, log2_lanes, (int)parts);
   }
 }
 
