@@ -5,14 +5,17 @@
 // pages asked for, pages and tokens granted), then one independent number for each page
 // and token. All of it is small and waits for itself: a decode step of 64
 // requests reads and writes a few KB, so what counts is the length of the
-// chain of loads and barriers, and the number of launches.
+// chain of loads and barriers, and the number of launches: 48 sequences 4.2 us, 200
+// sequences with 60000 rows of tokens 7.6, 1000 with as many 11.9, 4000 with 4000 rows 36.
 //
-// One kernel where the step is small: one workgroup, a thread for each sequence, then a
-// few tokens' rows for each thread. Else two: the sums need every sequence,
-// and lengths, table and stack are changed in place, which no other workgroup
-// may see half done, so a first workgroup goes through the sequences 1024 at a
-// time, twice (pages given back have to be known before one is granted), and a
-// second kernel writes the tokens' rows with as many workgroups as they need.
+// One workgroup goes through the sequences, a thread for each, since the sums need every
+// sequence, and lengths, table and stack are changed in place, which no other workgroup
+// may see half done. Up to 256 sequences it has 256 threads (48 sequences 4 us, with 1024
+// threads 7: every barrier waits for all waves), else 1024; more sequences are taken 1024 at a
+// time, twice (pages given back have to be known before one is granted).
+// The tokens' rows: a few for each of its threads (48 sequences, 600 rows: 5.5 us, 6.2 in a
+// second kernel), else by a second kernel with as many workgroups as they need (2048 rows:
+// 6.7 us, 8.9 in the first).
 //
 // Where a granted page comes from follows from the prefix sum alone: the k-th
 // one in the order of (sequence, page) is stack entry top - 1 - k. So a token
@@ -132,15 +135,16 @@ __device__ __forceinline__ void token_row(const qmat_page_args& a, const int32_t
   if (a.token_seq != nullptr) a.token_seq[t] = seq;
 }
 
-// kAlone: at most kThreads sequences, and this kernel writes the tokens' rows.
-template <int kThreads, bool kAlone>
+// kOne: at most kThreads sequences. Without a step_out this kernel writes the tokens'
+// rows (kOne only).
+template <int kThreads, bool kOne>
 __global__ __launch_bounds__(kThreads) void page_step_kernel(qmat_page_args a, int shift,
                                                              Step* step_out, Seq* seqs_out) {
   __shared__ int64_t sums[2 * kThreads / kWave];
   __shared__ int64_t back_ends[kThreads];  // pages given back up to a sequence's last
   __shared__ int32_t back_from[kThreads];  // its first page given back
-  __shared__ int32_t ends[kAlone ? kThreads : 1];
-  __shared__ Seq seqs[kAlone ? kThreads : 1];
+  __shared__ int32_t ends[kOne ? kThreads : 1];
+  __shared__ Seq seqs[kOne ? kThreads : 1];
   const int tid = threadIdx.x;
   const int64_t free = a.free_count[0];
   const int64_t count = free < 0 ? 0 : free > a.pages ? a.pages : free;
@@ -167,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void page_step_kernel(qmat_page_args a, i
   };
 
   int64_t back = 0;
-  if constexpr (!kAlone) {
+  if constexpr (!kOne) {
     int64_t before = 0;
     for (int64_t b0 = 0; b0 < a.n_seqs; b0 += kThreads) {
       int64_t v[1] = {ask(b0 + tid, before).back}, total[1];
@@ -181,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void page_step_kernel(qmat_page_args a, i
     const Asked q = ask(b, asked_tokens);
     int64_t v[2] = {q.back, q.need}, total[2];
     block_scan<kThreads>(v, total, sums);
-    if constexpr (kAlone) back = total[0];
+    if constexpr (kOne) back = total[0];
     top = count + back < a.pages ? count + back : a.pages;
     back_ends[tid] = v[0];
     back_from[tid] = q.l.now;
@@ -210,21 +214,20 @@ __global__ __launch_bounds__(kThreads) void page_step_kernel(qmat_page_args a, i
       a.q_start[b + 1] = end;
       if (ok) a.kv_len[b] = (int32_t)q.l.goal;
       const Seq s{(int32_t)q.l.kept, q.l.old, (int32_t)first, 0};
-      if constexpr (kAlone) {
+      if constexpr (kOne) {
         ends[tid] = end;
         seqs[tid] = s;
-      } else {
-        seqs_out[b] = s;
       }
+      if (!kOne || seqs_out != nullptr) seqs_out[b] = s;
     }
   }
   const Step step{tokens, top};
   if (tid == 0) {
     a.q_start[0] = 0;
     a.free_count[0] = (int32_t)(top - pages);
-    if constexpr (!kAlone) *step_out = step;
+    if (!kOne || step_out != nullptr) *step_out = step;
   }
-  if constexpr (kAlone) {
+  if (kOne && step_out == nullptr) {
     __syncthreads();  // ends, seqs and the pages given back
     for (int64_t t = tid; t < a.max_tokens; t += kThreads) token_row(a, ends, seqs, step, shift, t);
   }
@@ -242,36 +245,33 @@ constexpr int kManyThreads = 1024;
 constexpr int kFewThreads = 256;
 constexpr int kEach = 4;  // tokens' rows of a thread, where one kernel does it all
 
+int64_t threads(const qmat_page_args& a) { return a.n_seqs <= kFewThreads ? kFewThreads : kManyThreads; }
+
 // A thread for each sequence and kEach rows for each thread.
-bool alone(const qmat_page_args& a, int64_t threads) {
-  return a.n_seqs <= threads && a.max_tokens <= kEach * threads;
+bool alone(const qmat_page_args& a) { return a.n_seqs <= kManyThreads && a.max_tokens <= kEach * threads(a); }
+
+template <int kThreads, bool kOne>
+void launch(const qmat_page_args& a, int shift, Step* step, Seq* seqs, hipStream_t stream) {
+  hipLaunchKernelGGL((page_step_kernel<kThreads, kOne>), dim3(1), dim3(kThreads), 0, stream, a, shift, step, seqs);
 }
 
 }  // namespace
 
 int64_t page_workspace_bytes(const qmat_page_args& a) {
-  return alone(a, kManyThreads) ? 0 : (int64_t)sizeof(Step) + a.n_seqs * (int64_t)sizeof(Seq);
+  return alone(a) ? 0 : (int64_t)sizeof(Step) + a.n_seqs * (int64_t)sizeof(Seq);
 }
 
 hipError_t launch_page_step(const qmat_page_args& a, void* workspace, hipStream_t stream) {
   int shift = 0;
   while ((1LL << shift) < a.page_size) ++shift;
-  if (alone(a, kFewThreads)) {
-    hipLaunchKernelGGL((page_step_kernel<kFewThreads, true>), dim3(1), dim3(kFewThreads), 0, stream, a,
-                       shift, nullptr, nullptr);
-    return hipGetLastError();
-  }
-  if (alone(a, kManyThreads)) {
-    hipLaunchKernelGGL((page_step_kernel<kManyThreads, true>), dim3(1), dim3(kManyThreads), 0,
-                       stream, a, shift, nullptr, nullptr);
-    return hipGetLastError();
-  }
-  Step* step = static_cast<Step*>(workspace);
-  Seq* seqs = reinterpret_cast<Seq*>(step + 1);
-  hipLaunchKernelGGL((page_step_kernel<kManyThreads, false>), dim3(1), dim3(kManyThreads), 0,
-                     stream, a, shift, step, seqs);
+  const bool all = alone(a);
+  Step* step = all ? nullptr : static_cast<Step*>(workspace);
+  Seq* seqs = all ? nullptr : reinterpret_cast<Seq*>(step + 1);
+  a.n_seqs <= kFewThreads    ? launch<kFewThreads, true>(a, shift, step, seqs, stream)
+  : a.n_seqs <= kManyThreads ? launch<kManyThreads, true>(a, shift, step, seqs, stream)
+                             : launch<kManyThreads, false>(a, shift, step, seqs, stream);
   const int64_t wgs = (a.max_tokens + kRowThreads - 1) / kRowThreads;
-  if (wgs > 0)
+  if (!all && wgs > 0)
     hipLaunchKernelGGL(page_rows_kernel, dim3((unsigned)wgs), dim3(kRowThreads), 0, stream, a,
                        shift, step, seqs);
   return hipGetLastError();
