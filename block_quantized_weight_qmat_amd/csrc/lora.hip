@@ -3,10 +3,18 @@
 //
 //   z[t][r] = sum_k a[r][k] x[t][k],   y[t][m] = base[t][m] + s sum_r b[m][r] z[t][r]
 //
-// with a, b and s of the token's adapter. Two kernels, since every row of y
-// needs all of z: the first reads the Q8_0 rows and a, the second b and y. Few
-// operations for each byte: bound by HBM bandwidth for prompts (y is read and
-// written, 8 bytes for 4 rank operations), by the chain of loads for a decode batch.
+// with a, b and s of the token's adapter. Every row of y needs all of z. For a
+// few tokens of each sequence one kernel takes a token at a time, each workgroup
+// computing all of z for itself; else two kernels, the first reading the Q8_0 rows and a, the
+// second b and y (lora_plan.hpp chooses, with both sides measured).
+//
+// Few operations for each byte: the floor of prompts is reading and writing y (8
+// bytes for 4 rank operations). Measured: 1519 tokens of 7 prompts, rank 64, 11008 ->
+// 4096: 31 us, half of it each kernel: the second moves 50 MB at 3.3 TB/s, the
+// first has the latency of five chunks of K one after the other, since 456
+// workgroups are all that there is to share. 64 tokens of a decode batch, 24 adapters
+// of rank 16, 4096 -> 11008: 9 us, a chain of loads (start, adapter, code, a, b) of which
+// nothing can be asked for before the one in front has come.
 //
 // Tiles of tokens lie within one sequence: of the aligned runs of 32 (or 16) tokens, a
 // sequence has those that it reaches into, cut at its ends. So a tile has one
@@ -351,7 +359,7 @@ __device__ __forceinline__ void split(half8_t w, bf16x8 (&o)[2]) {
 // each token's y, 64 of them in neighbouring lanes.
 //
 // z has fp32's precision and b 8 or 11 bits: in the matrix cores' fp32 form the
-// products took longer than reading y (64 ranks: 7 of 24 us). Split into bf16
+// products took 7 us of this kernel's then 24 (64 ranks). Split into bf16
 // parts they take three (bf16) or six (fp16) products of 32 ranks, 16 cycles each
 // instead of eight of 32, and lose nothing.
 template <typename T, int kTT>
@@ -583,10 +591,9 @@ void launch_down(const qmat_lora_args& a, const LoraPlan& p, float* z, hipStream
 
 template <typename T, int kTT>
 void launch_both(const qmat_lora_args& a, const LoraPlan& p, float* z, hipStream_t stream) {
-  if (p.parts > 0)
-    p.rank_tiles == 1   ? launch_down<T, 1, kTT>(a, p, z, stream)
-    : p.rank_tiles == 2 ? launch_down<T, 2, kTT>(a, p, z, stream)
-                        : launch_down<T, 4, kTT>(a, p, z, stream);
+  p.rank_tiles == 1   ? launch_down<T, 1, kTT>(a, p, z, stream)
+  : p.rank_tiles == 2 ? launch_down<T, 2, kTT>(a, p, z, stream)
+                      : launch_down<T, 4, kTT>(a, p, z, stream);
   const int64_t rows = p.tiles < kMaxGridY ? p.tiles : kMaxGridY;
   const dim3 grid((unsigned)((a.M + p.up_rows - 1) / p.up_rows), (unsigned)rows, (unsigned)((p.tiles + rows - 1) / rows));
   hipLaunchKernelGGL((lora_up_kernel<T, kTT>), grid, dim3(kUpThreads), 3 * 16 * kTT * (p.up_ranks + 8) * 2, stream,

@@ -59,9 +59,9 @@ inline LoraPlan lora_plan(const qmat_lora_args& a) {
   p.groups = (int32_t)up(rank_tiles, p.rank_tiles);
   p.tiles = lora_tiles(a, 16 * p.token_tiles);
   // K is divided until there are two workgroups for each CU, or two blocks for
-  // each wave
+  // each wave (K is not 0: that takes a token at a time)
   const int64_t blocks = a.K / 32, wgs = p.tiles * p.groups;
-  p.parts = blocks == 0 ? 0 : cut(wgs > 0 ? 512 / wgs : 1, 1, blocks / 16);
+  p.parts = cut(wgs > 0 ? 512 / wgs : 1, 1, blocks / 16);
   p.up_ranks = (int32_t)up(a.rank, 32) * 32;
   p.up_rows = 512;
   return p;
