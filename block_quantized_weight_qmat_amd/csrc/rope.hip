@@ -5,8 +5,9 @@
 //
 // A copy with eight multiplications for four elements: bound by HBM bandwidth
 // where there are many tokens, by one chain of loads where there are few. 8191
-// tokens of 40 heads of 128, bf16, on 3 axes: 32 us, 5.2 TB/s, a large copy's rate;
-// 64 tokens: 3.8 us, most of it the fetch of the code, of the axes, of the positions.
+// tokens of 40 heads of 128, bf16, on 3 axes: 37 us from inputs that the caches do not
+// hold, 4.5 TB/s of a copy's 5.1 (32 us from those that they do in part); 64 tokens: 3.0 us,
+// most of it the fetches of code, axes and positions, one after the other.
 // What could bound it instead are the angles: in 64 bits (fp32 knows an angle of
 // 10^6 to 0.03, fp64 to 2^-34), about a hundred instructions each.
 //
@@ -17,7 +18,9 @@
 // from how many are needed to fill the GPU. A workgroup computes the sines and
 // cosines of its tokens once, a thread for each, and shares them in LDS: where each lane
 // had its own four, all waves began with 5 us of arithmetic without a load on its
-// way (8191 tokens 43 us, 1024 10.0 instead of 7.9).
+// way (8191 tokens 43 us, 1024 10.0 instead of 7.6). Which elements make a pair is
+// known when the code is compiled: fewer instructions for each head (11.0 -> 10.7 us, 2048
+// tokens) and a smaller kernel to fetch.
 #include "kv_device.hpp"
 #include "qmat_launch.hpp"
 
@@ -35,7 +38,7 @@ __device__ __forceinline__ void turn(int32_t pos, double freq, float* s, float* 
 }
 
 // log2_lanes: lanes of a head; parts: groups of lanes that share a token.
-template <typename In, typename Out>
+template <typename In, typename Out, bool kNeighbours>
 __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_t token0,
                                                         int log2_lanes, int parts) {
   // cosines and sines of the workgroup's tokens: with one part a token for each group of
@@ -51,8 +54,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_
   const bool live = token < a.n && 8 * u < D;
   // the lane's runs of four elements: of halves where its pairs are turned
   const bool turned = 8 * u < 2 * pairs;
-  const int e0 = turned && !a.neighbours ? 4 * u : 8 * u;
-  const int e1 = turned && !a.neighbours ? pairs + 4 * u : 8 * u + 4;
+  const int e0 = turned && !kNeighbours ? 4 * u : 8 * u;
+  const int e1 = turned && !kNeighbours ? pairs + 4 * u : 8 * u + 4;
   const int heads = (int)(a.heads + a.kv_heads), q_heads = (int)a.heads;
   const In* const q = static_cast<const In*>(a.q) + token * a.q_stride;
   const In* const k = static_cast<const In*>(a.k) + token * a.k_stride;
@@ -121,16 +124,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // pair i: elements i and 4 + i (halves), or 2i and 2i + 1 of the eight
-        const float x = a.neighbours ? v[2 * i] : v[i];
-        const float y = a.neighbours ? v[2 * i + 1] : v[4 + i];
-        const float p = x * cs[i] - y * sn[i], t = y * cs[i] + x * sn[i];
-        if (a.neighbours) {
-          v[2 * i] = p;
-          v[2 * i + 1] = t;
-        } else {
-          v[i] = p;
-          v[4 + i] = t;
-        }
+        float &x = v[kNeighbours ? 2 * i : i], &y = v[kNeighbours ? 2 * i + 1 : 4 + i];
+        const float p = fmaf(x, cs[i], -(y * sn[i]));
+        y = fmaf(y, cs[i], x * sn[i]);
+        x = p;
       }
     }
     Out* out = is_k ? static_cast<Out*>(a.k_out) + token * a.k_out_stride + (h - q_heads) * D
@@ -141,16 +138,17 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(qmat_rope_args a, int64_
 }
 
 // How many groups of lanes share a token's heads: enough for five waves on each
-// SIMD, and five heads for a group at most (40 heads of 128, bf16. 256 tokens: 4.3 us with one
-// head, 5.1 with four; 1024: 9.0 with one, 7.9 with two, 8.6 with four; 4096: 17.6 with
-// three, 16.2 with five, 17.3 with eight; 8191: 32.2 with five, 33.1 with ten, 37 with twenty).
+// SIMD, and five heads for a group at most (40 heads of 128, bf16, inputs in the caches.
+// 256 tokens: 4.3 us with one head, 5.1 with four; 1024: 9.0 with one, 7.9 with two, 8.6 with
+// four; 4096: 17.6 with three, 16.2 with five, 17.3 with eight; 8191: 32.2 with five, 33.1
+// with ten, 37 with twenty).
 constexpr int64_t kSimds = 256 * 4;
 constexpr int64_t kPerSimd = 5;
 constexpr int64_t kShared = 5;
 constexpr int64_t kMaxLanes = 1LL << 31;  // of a launch: their number has 32 bits
 
-template <typename In, typename Out>
-void launch_as(const qmat_rope_args& a, hipStream_t stream) {
+template <typename In, typename Out, bool kNeighbours>
+void launch_pairs(const qmat_rope_args& a, hipStream_t stream) {
   int log2_lanes = 0;
   while ((8 << log2_lanes) < a.head_dim) ++log2_lanes;
   const int64_t heads = a.heads + a.kv_heads;
@@ -160,9 +158,14 @@ void launch_as(const qmat_rope_args& a, hipStream_t stream) {
   for (int64_t t = 0; t < a.n; t += most) {
     qmat_rope_args now = a;  // the last workgroup's spare lanes have no tokens of the next launch
     if (a.n - t > most) now.n = t + most;
-    hipLaunchKernelGGL((rope_kernel<In, Out>), dim3((unsigned)(((now.n - t) * parts + per - 1) / per)), dim3(kThreads),
+    hipLaunchKernelGGL((rope_kernel<In, Out, kNeighbours>), dim3((unsigned)(((now.n - t) * parts + per - 1) / per)), dim3(kThreads),
                        0, stream, now, t, log2_lanes, (int)parts);
   }
+}
+
+template <typename In, typename Out>
+void launch_as(const qmat_rope_args& a, hipStream_t stream) {
+  a.neighbours ? launch_pairs<In, Out, true>(a, stream) : launch_pairs<In, Out, false>(a, stream);
 }
 
 template <typename In>
