@@ -298,3 +298,23 @@ def test_same_bits_again(lib):
             torch.cuda.synchronize()
             assert torch.equal(y, first)
             assert torch.equal(c.run(lib, max_q=max_q), first)
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_two_calls_at_once(lib, max_q):
+    """Calls on two streams, each with its own workspace, give what they give alone."""
+    import torch
+    cases = [Case([40, 1, 64], [0, 2, 1], 3, 32, LONG, 520, seed=5), Case([1, 64, 33], [1, 0, 2], 3, 32, LONG, 520, seed=6)]
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    alone = [c.run(lib, max_q=max_q) for c in cases]
+    held = [(torch.from_numpy(c.x).cuda(), c.a.cuda(), c.b.cuda(), ints(c.of), ints(c.starts)) for c in cases]
+    more = [(c.base.cuda(), c.scale.cuda(), torch.zeros(c.n, 520, device="cuda")) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for h, (base, scale, y), s in zip(held, more, streams):
+            with torch.cuda.stream(s):
+                lib.lora(*h, y, base=base, scale=scale, max_q=max_q)
+    torch.cuda.synchronize()
+    for (_, _, y), first in zip(more, alone):
+        assert torch.equal(y, first)

@@ -239,3 +239,50 @@ def test_captured(lib):
         torch.cuda.synchronize()
         compare(got, pool.step(n, None, 400), state, pool)
         assert int(add.sum()) == sum(n)
+
+
+@pytest.mark.parametrize("seqs,rows,each", [(7, 3000, 5), (256, 2000, 5), (256, 60000, 3), (257, 5000, 5), (1024, 5000, 5), (1024, 60000, 3),
+                                            (1030, 2100, 5), (2100, 90000, 3)])
+def test_refused_and_taken_back_in_large_steps(lib, seqs, rows, each):
+    """Steps whose rows a second kernel writes: too long for a table row, for the tokens, for the pages; pages given back and taken again."""
+    r = random.Random(seqs)
+    page, wide = 8, 12
+    pages = each * seqs
+    pool = Pool(seqs, pages, page, wide, 0)
+    for b in range(seqs):
+        pool.hold(b, r.randrange(4 * page))
+    pool.release()
+    state = pool.tensors()
+    seen = set()
+    for _ in range(5):
+        add = [r.choice((0, 1, 3, r.randrange(wide * page + 20))) if r.random() < (0.3 if each > 3 else 0.8) else r.randrange(2) for _ in range(seqs)]
+        keep = None if r.random() < 0.3 else [max(0, n - r.randrange(20)) for n in pool.kv]
+        want = pool.step(add, keep, rows)
+        got = lib.page_step(add=ints(add), keep=ints(keep), page_size=page, max_tokens=rows, **state)
+        compare(got, want, state, pool)
+        seen |= set(want[4])
+    assert 0 in seen and (seqs < 100 or 1 in seen) and (each > 3 or 2 in seen)  # a few sequences may all fit
+
+
+def test_large_step_captured(lib):
+    """Two kernels and their workspace in a graph, replayed beside eager steps of another pool."""
+    import torch
+    pool, other = Pool(300, 3000, 16, 32, 3000), Pool(300, 3000, 16, 32, 3000, table_seed=5)
+    state, state2 = pool.tensors(), other.tensors()
+    add = ints([0] * 300)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lib.page_step(add=add, page_size=16, max_tokens=6000, **state)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        got = lib.page_step(add=add, page_size=16, max_tokens=6000, **state)
+    r = random.Random(3)
+    for _ in range(4):
+        n, m = [r.randrange(20) for _ in range(300)], [r.randrange(20) for _ in range(300)]
+        add.copy_(ints(n))
+        graph.replay()
+        eager = lib.page_step(add=ints(m), page_size=16, max_tokens=6000, **state2)
+        torch.cuda.synchronize()
+        compare(got, pool.step(n, None, 6000), state, pool)
+        compare(eager, other.step(m, None, 6000), state2, other)

@@ -155,3 +155,20 @@ def test_nothing_to_do(lib):
     q = torch.zeros((0, 2, 64), device="cuda")
     got = lib.rope(q, q, torch.zeros(0, dtype=torch.int32, device="cuda"), lib.rope_freq(64), dtype=torch.float16)
     assert got[0].shape == (0, 2, 64) and got[1].dtype == torch.float16
+
+
+@pytest.mark.parametrize("n,heads,kv_heads,D,rot", [(300, 7, 0, 128, 128), (301, 5, 1, 72, 64), (129, 11, 2, 512, 512), (1000, 3, 0, 8, 8),
+                                                    (9000, 1, 2, 8, 8), (4097, 7, 4, 64, 64)])
+def test_tokens_across_workgroups(lib, n, heads, kv_heads, D, rot):
+    """Heads shared out in parts that do not divide a workgroup's groups of lanes: its tokens begin and end within it."""
+    run(lib, n, heads, kv_heads, D, rot, axes=2, seed=n)
+    run(lib, n, heads, kv_heads, D, rot, neighbours=True, norm=True, in_place=True, dtype="bf16", out="bf16", seed=n)
+
+
+def test_keys_alone(lib):
+    import torch
+    g = torch.Generator().manual_seed(4)
+    k = torch.randn(5, 2, 64, generator=g).cuda()
+    pos, freq = torch.arange(5, dtype=torch.int32, device="cuda"), lib.rope_freq(64)
+    none, got = lib.rope(k[:, :0], k, pos, freq)
+    assert none.shape == (5, 0, 64) and torch.equal(got, lib.rope(k, None, pos, freq)[0])
