@@ -11,6 +11,7 @@ the HIP runtime torch already loaded (both name it libamdhip64.so.7).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -172,8 +173,13 @@ def block_bytes(fmt) -> int:
     return int(load_library().qmat_block_bytes(_fmt(fmt)))
 
 
+@functools.lru_cache(maxsize=256)
+def _row_bytes(f: int, K: int) -> int:
+    return int(load_library().qmat_row_bytes(f, K))
+
+
 def row_bytes(fmt, K: int) -> int:
-    rb = int(load_library().qmat_row_bytes(_fmt(fmt), int(K)))
+    rb = _row_bytes(_fmt(fmt), int(K))
     if rb < 0:
         raise ValueError(f"K={K} is not a multiple of the block size of format {fmt!r}")
     return rb
@@ -412,6 +418,8 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     shape, stride = t.shape, t.stride()
+    if t.is_contiguous() and shape[0] > 0:
+        return stride[0] if shape[0] > 1 else max(t.numel(), 1)
     if len(shape) == 2 and stride[1] == 1 and shape[0] > 1:
         return stride[0]
     row = 1
@@ -829,7 +837,7 @@ def page_step(kv_len: torch.Tensor, add: torch.Tensor, page_table: torch.Tensor,
             status is None:
         # one allocation, slots in front: kv_store takes them at 16 bytes
         buf = torch.empty(3 * max_tokens + 2 * n_seqs + 1, dtype=torch.int32, device=device)
-        slots, positions, token_seq, q_start, status = buf.split_with_sizes(
+        slots, positions, token_seq, q_start, status = buf.unsafe_split_with_sizes(
             (max_tokens, max_tokens, max_tokens, n_seqs + 1, n_seqs))
     else:
         q_start = _ints(q_start, "q_start", n_seqs + 1, device)

@@ -11,8 +11,8 @@
 // Few operations for each byte: the floor of prompts is reading and writing y (8
 // bytes for 4 rank operations). Measured: 1519 tokens of 7 prompts, rank 64, 11008 ->
 // 4096: 31 us, half of it each kernel: the second moves 50 MB at 3.3 TB/s, the
-// first has the latency of five chunks of K one after the other, since 456
-// workgroups are all that there is to share. 64 tokens of a decode batch, 24 adapters
+// first brings its chunks of a and x into LDS at 43 KB/us for each CU, however many are
+// on their way. 64 tokens of a decode batch, 24 adapters
 // of rank 16, 4096 -> 11008: 9 us, a chain of loads (start, adapter, code, a, b) of which
 // nothing can be asked for before the one in front has come.
 //
