@@ -737,7 +737,8 @@ int qmat_page_step(const qmat_page_args *args, void *workspace, int64_t workspac
  *   Alignment: x_q8, a, b, y, base 16 bytes; scale, ranks, adapter, q_start 4.
  *   x_q8, a and b may be NULL when there are no adapters or K is 0 (b: no
  *   adapters), adapter and q_start when there are no sequences. n_tokens == 0
- *   or M == 0 enqueues nothing.
+ *   or M == 0 enqueues nothing. Calls that share a workspace must not overlap
+ *   in time.
  */
 typedef struct qmat_lora_args {
   int32_t dtype;
