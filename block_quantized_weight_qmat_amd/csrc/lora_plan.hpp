@@ -42,14 +42,15 @@ inline LoraPlan lora_plan(const qmat_lora_args& a) {
   // Up to four tokens of a sequence, 4096 x 4096 unless said: rank 16, 64 / 256 sequences of 1
   // token: 8 / 10 against 20 / 37; rank 64, 1 token: 9 against 11, 64: 14 against 15; 11008 x 4096,
   // rank 64, 1 token: 22 against 13, 64: 24 against 29.
-  // More: a workgroup reads all of a first (2 MB: 47 us), then n rank K products of the first
-  // kind cost 1.1 us each 10^7, of the second 3.5, and a workgroup's start 7 each 1000 tokens. 140
+  // More tokens: a workgroup reads all of a first (so no larger ones than 1 MB), then every 10^7
+  // products with a take about 1.1 us, with b 3.5, and the start of 1000 workgroups 7. 140
   // tokens of rank 64, 1632 -> 8706: 31 against 17; 311 of rank 40, 1280 -> 7403: 38 against 19; 1600
   // of rank 8, 352 -> 917: 21 against 13; 356 of rank 16, 544 -> 1178: 8 against 12; 256 of rank
-  // 16, 4096 -> 4096: 10 against 12, 512: 21 against 19; 110 of rank 64, 8576 -> 408: 15 against 18.
+  // 16, 4096 -> 4096: 10 against 12, 512: 21 against 19.
   const int64_t elems = a.rank * a.K;
-  p.few = a.K <= 1 << 14 && (a.max_q <= 4 ? elems <= 1 << 18 || (elems <= 1 << 20 && a.n_tokens >= 32)
-                                          : elems <= 1 << 19 && a.n_tokens * (elems + 3 * a.rank * a.M + (1 << 16)) <= 5 << 24);
+  p.few = a.K <= 1 << 14 && (a.K == 0 ? true
+                             : a.max_q <= 4 ? elems <= 1 << 18 || (elems <= 1 << 20 && a.n_tokens >= 32)
+                                            : elems <= 1 << 19 && a.n_tokens * (elems + 3 * a.rank * a.M + (1 << 16)) <= 5 << 24);
   if (p.few) {
     while (8 << p.few_log2 < a.rank) ++p.few_log2;
     // a workgroup for each CU, and whole threads of rows
