@@ -36,27 +36,28 @@ inline LoraPlan lora_plan(const qmat_lora_args& a) {
   LoraPlan p{};
   const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   const auto cut = [](int64_t v, int64_t lo, int64_t hi) { return (int32_t)(v > hi ? hi > lo ? hi : lo : v < lo ? lo : v); };
-  // A token at a time reads an adapter's a once more for every 256th of all rows of b, and b for
-  // every token, but is one short launch; tiles read them once for 32 tokens of a sequence, but a
-  // decode batch has one token in each. (us, a token at a time against tiles.)
-  // Up to four tokens of a sequence, 4096 x 4096 unless said: rank 16, 64 / 256 sequences of 1
-  // token: 8 / 10 against 20 / 37; rank 64, 1 token: 9 against 11, 64: 14 against 15; 11008 x 4096,
-  // rank 64, 1 token: 22 against 13, 64: 24 against 29.
-  // More tokens: a workgroup reads all of a first (so no larger ones than 1 MB), then every 10^7
-  // products with a take about 1.1 us, with b 3.5, and the start of 1000 workgroups 7. 140
-  // tokens of rank 64, 1632 -> 8706: 31 against 17; 311 of rank 40, 1280 -> 7403: 38 against 19; 1600
-  // of rank 8, 352 -> 917: 21 against 13; 356 of rank 16, 544 -> 1178: 8 against 12; 256 of rank
-  // 16, 4096 -> 4096: 10 against 12, 512: 21 against 19.
-  const int64_t elems = a.rank * a.K;
-  p.few = a.K <= 1 << 14 && (a.K == 0 ? true
-                             : a.max_q <= 4 ? elems <= 1 << 18 || (elems <= 1 << 20 && a.n_tokens >= 32)
-                                            : elems <= 1 << 19 && a.n_tokens * (elems + 3 * a.rank * a.M + (1 << 16)) <= 5 << 24);
-  if (p.few) {
+  const int64_t elems = a.rank * a.K, max_q = a.max_q > 0 ? a.max_q : 1;
+  if (a.K <= 1 << 14) {
     while (8 << p.few_log2 < a.rank) ++p.few_log2;
     // a workgroup for each CU, and whole threads of rows
     const int64_t splits = up(256, a.n_tokens > 0 ? a.n_tokens : 1);
     p.few_rows = up(up(a.M, splits), 1024) * 1024;
-    return p;
+    // A token at a time reads all of an adapter's a in every workgroup, and b for every token, but is
+    // one short launch; tiles read them once for up to 32 tokens of a sequence (16 where it has no
+    // more), but a decode batch has one token in each. In us, as measured; a token at a time: a
+    // workgroup's start, its elements of a, its rows of b by lanes of eight ranks, a workgroup for each CU
+    // at once; tiles: two launches, and what a tile costs, with as few tiles as there can be.
+    // 1 / 32 / 512 sequences of 1 token, rank 64, 4096 x 4096: 9, 12, 42 against 11, 13, 74;
+    // 128 / 512 sequences of 4: 43, 159 against 35, 98; of rank 16: 17, 63 against 24, 69. Rank 64,
+    // 11008 -> 4096, 1 and 64 sequences of 1 token: 22, 24 against 13, 29. One sequence: 311 tokens of
+    // rank 40, 1280 -> 7403: 38 against 19; 356 of rank 16, 544 -> 1178: 8 against 12.
+    const int64_t rows = a.M < p.few_rows ? a.M : p.few_rows;
+    const double a_time = 2.5e-5 * (double)elems, b_time = 3.8e-5 * (double)(8 << p.few_log2) * (double)rows;
+    const double few = 3 + (2 + a_time + b_time) * (double)up(a.n_tokens * up(a.M, p.few_rows > 0 ? p.few_rows : 1), 256);
+    const double tile = 0.03 + 2.4e-5 * (double)a.M + 1e-7 * (double)elems;
+    const double tiles = 13 + tile * (double)a.n_tokens / (double)(max_q < 32 ? max_q : 32);
+    p.few = a.K == 0 || few <= tiles;
+    if (p.few) return p;
   }
   p.token_tiles = a.max_q <= 16 ? 1 : 2;
   p.z_stride = up(a.rank, 16) * 16;
