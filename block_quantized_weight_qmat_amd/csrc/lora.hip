@@ -175,9 +175,9 @@ __device__ __forceinline__ typename Vec8<T>::type codes(uint32_t lo, uint32_t hi
 
 constexpr int kDownWaves = 8;
 constexpr int kDownThreads = kDownWaves * kWave;
-constexpr int kChunk = 8;                  // blocks of K at a time: one for each wave
-constexpr int kAPitch = kChunk * 64 + 16;  // bytes of a rank's row in LDS
-constexpr int kXBytes = kChunk * 34;       // of a token's
+constexpr int kChunk = kLoraChunk;  // blocks of K at a time: one for each wave
+constexpr int kAPitch = kLoraAPitch, kXBytes = kLoraXBytes;
+static_assert(kChunk == kDownWaves, "a block of the chunk for each wave");
 
 // A workgroup: a tile of up to 16 * kTT tokens, one part of K, kRT tiles of 16
 // ranks. A chunk of eight blocks of all rows is copied into LDS, side by side as it
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(qmat_lora_args 
   typedef typename Vec8<T>::type vec8;
   typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
   constexpr int kSums = kRT * kTT, kSumWaves = kDownWaves / 2;
-  constexpr int kABytes = 16 * kRT * kAPitch, kBuffer = kABytes + 16 * kTT * kXBytes;
+  constexpr int kABytes = lora_a_bytes(kRT), kBuffer = lora_chunk_bytes(kRT, kTT);
   constexpr int kSumBytes = kSumWaves * kSums * kWave * 16;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kBuffer > kSumBytes ? kBuffer : kSumBytes];
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(qmat_lora_args 
         w[rt] = *reinterpret_cast<const vec8*>(lds + (16 * rt + col) * kAPitch + 64 * wave + 16 * g);
       // an even block's codes lie across words, an odd one's in words
       const uint8_t* x = lds + kABytes + col * kXBytes + 34 * wave;
-      const uint32_t* x_words = reinterpret_cast<const uint32_t*>(x + 2 * (wave & 1) + 8 * g);
+      const uint32_t* x_words = reinterpret_cast<const uint32_t*>(lds + kABytes + lora_codes_at(col, wave, g));
       const int skip = wave & 1 ? 0 : 2;
 #pragma unroll
       for (int tt = 0; tt < kTT; ++tt) {

@@ -10,6 +10,28 @@ namespace qmat {
 
 constexpr int64_t kLoraMaxRank = 256;
 
+// A chunk of the first product in LDS: eight blocks of K, one for each wave, of
+// 16 * rank_tiles rows of a, then of 16 * token_tiles tokens.
+constexpr int kLoraChunk = 8;
+constexpr int kLoraAPitch = kLoraChunk * 64 + 16;  // bytes of a rank's row
+constexpr int kLoraXBytes = kLoraChunk * 34;       // of a token's
+
+constexpr int lora_a_bytes(int rank_tiles) { return 16 * rank_tiles * kLoraAPitch; }
+
+// Where lane 16 g + col of a wave reads its eight codes of token col, three words
+// from here, counted from the first token's first byte. An even block's codes lie
+// across words and take all three, an odd one's in words: its third is
+// read all the same and not used, for the last token's last codes behind them.
+constexpr int lora_codes_at(int col, int wave, int g) {
+  return col * kLoraXBytes + 34 * wave + 2 * (wave & 1) + 8 * g;
+}
+constexpr int kLoraCodeBytes = 12;
+constexpr int kLoraTail = 16;  // the room for that
+
+constexpr int lora_chunk_bytes(int rank_tiles, int token_tiles) {
+  return lora_a_bytes(rank_tiles) + 16 * token_tiles * kLoraXBytes + kLoraTail;
+}
+
 struct LoraPlan {
   bool few;             // one kernel, a token at a time
   int32_t few_log2;     // log2 of its lanes of a row of b: eight ranks each
