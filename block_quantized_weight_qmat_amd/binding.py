@@ -650,7 +650,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     x [n, K] (fp32, fp16 or bf16; tokens any stride apart) and weight [K] (fp32).
     want: "q8" for y as Q8_0 blocks (what gemm takes), "rows" for y in x's type
     (gemv's x), "both". Returns (rows or None, q8 or None, h or None). h goes to
-    residual_out, which may be residual or x itself; rows may be x itself."""
+    residual_out, which may be residual or x itself; rows may be x itself, but is
+    neither the residual nor residual_out."""
     if want not in ("q8", "rows", "both"):
         raise ValueError(f'want must be "q8", "rows" or "both", not {want!r}')
     if x.dim() != 2:

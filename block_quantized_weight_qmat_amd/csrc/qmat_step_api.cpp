@@ -106,6 +106,9 @@ int qmat_norm(const qmat_norm_args* args, void* stream) {
               (a.residual_out == a.x && a.residual_out_stride != a.x_stride)))
     return QMAT_E_SHAPE;
   if (a.n > 0 && a.rows != nullptr && a.rows == a.x && a.rows_stride != a.x_stride) return QMAT_E_SHAPE;
+  // rows over the residual or over its sum: one of them would be lost
+  if (a.n > 0 && sum && a.rows != nullptr && (a.rows == a.residual_out || a.rows == a.residual))
+    return QMAT_E_SHAPE;
   if (a.n == 0 || a.K == 0) return QMAT_OK;
   if (a.rows == nullptr && a.q8 == nullptr) return QMAT_E_NULL;
   int rc = check_rows(a.x, a.x_stride, size);

@@ -559,8 +559,9 @@ int qmat_embed(int fmt, int dtype, const void *blocks, const int32_t *ids, void 
  *   x, residual, residual_out, rows: n rows of dtype, their strides in
  *     elements (>= K, whole multiples of 16 bytes). residual and residual_out
  *     are both given or both NULL. residual_out may be residual or x itself,
- *     and rows may be x itself, with the same stride (QMAT_E_SHAPE for another);
- *     nothing else overlaps.
+ *     and rows may be x itself, with the same stride (QMAT_E_SHAPE for another),
+ *     but not both x: rows are neither residual nor residual_out
+ *     (QMAT_E_SHAPE). Nothing else overlaps.
  *     Elements of a row past K are left as they were.
  *   weight: fp32 [K]. eps: finite, >= 0 (QMAT_E_SHAPE).
  *   rows, q8: at least one of them (QMAT_E_NULL). q8: n rows of
