@@ -733,8 +733,9 @@ int qmat_page_step(const qmat_page_args *args, void *workspace, int64_t workspac
  *   Limits (QMAT_E_SHAPE): K a multiple of 32, up to 2^20; rank a multiple of
  *   8, 8 to 256; n_tokens and n_seqs up to 2^20, M up to 2^23, n_adapters and
  *   the strides up to 2^24; max_q >= 0.
- *   max_q: no sequence has more tokens. An estimate: it chooses how the work is
- *   divided (1 for decode), and with it the order of a sum's last bits.
+ *   max_q: no sequence has more tokens. An estimate: with the sizes it chooses how the
+ *   work is divided (1 for decode), and with it the order of a sum's last bits. It takes
+ *   every sequence to have tokens: a batch of many without any may be divided worse.
  *   Alignment: x_q8, a, b, y, base 16 bytes; scale, ranks, adapter, q_start 4.
  *   x_q8, a and b may be NULL when there are no adapters or K is 0 (b: no
  *   adapters), adapter and q_start when there are no sequences. n_tokens == 0

@@ -1,5 +1,6 @@
 """What the adapters' host code decides for the kernels, on the CPU under
-sanitizers: the layout of a chunk in LDS."""
+sanitizers: the layout of a chunk in LDS, and which division of the work a batch
+gets."""
 import os
 import shutil
 import subprocess
@@ -25,3 +26,8 @@ def run(tmp_path, driver):
 @pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
 def test_a_chunk_is_read_inside_its_bytes(tmp_path):
     assert "all reads inside" in run(tmp_path, "lora_layout_driver.cpp")
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_the_division_of_batches_of_unlike_sequences(tmp_path):
+    assert "all batches as measured" in run(tmp_path, "lora_division_driver.cpp")
