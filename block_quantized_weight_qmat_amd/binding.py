@@ -820,7 +820,8 @@ def page_step(kv_len: torch.Tensor, add: torch.Tensor, page_table: torch.Tensor,
     token_seq [max_tokens each], status [seqs]): what kv_store, rope, attn and lora take;
     rows behind the last token have slot -1, position 0, sequence -1. status is 0
     where it was done, 1 where the table row or max_tokens, 2 where the
-    pages do not suffice: such a sequence is left as it was and has no tokens."""
+    pages do not suffice: such a sequence is left as it was and has no tokens.
+    Slots of one's own are 16-byte aligned if kv_store is to take them."""
     device = kv_len.device
     _gpu(kv_len, "kv_len", torch.int32)
     n_seqs = kv_len.numel()

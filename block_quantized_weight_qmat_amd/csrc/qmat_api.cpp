@@ -133,7 +133,7 @@ const char* qmat_strerror(int status) {
     case QMAT_E_SHAPE: return "invalid shape (negative, out of range, or K not a multiple of the block)";
     case QMAT_E_NULL: return "required pointer is NULL";
     case QMAT_E_HIP: return "HIP kernel launch failed";
-    case QMAT_E_ALIGN: return "pointer is not 16-byte aligned";
+    case QMAT_E_ALIGN: return "pointer or row stride is not aligned (16 bytes; some lists of integers: 4)";
     case QMAT_E_SCRATCH:
       return "the Q8_0 activations (N * row bytes) exceed the static workspace of "
              "qmat_prefill_noalloc (qmat_noalloc_scratch_bytes())";

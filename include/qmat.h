@@ -125,7 +125,8 @@ typedef enum qmat_status {
                        a size beyond the limits above                    */
   QMAT_E_NULL = 3,  /* a required pointer is NULL                         */
   QMAT_E_HIP = 4,   /* the HIP launch itself failed                       */
-  QMAT_E_ALIGN = 5, /* a pointer is not 16-byte aligned                   */
+  QMAT_E_ALIGN = 5, /* a pointer or the stride of rows is not aligned as the
+                       call asks: 16 bytes, for some lists of integers 4   */
   QMAT_E_SCRATCH = 6, /* qmat_prefill_noalloc: the activation workspace it
                         needs exceeds its static scratch                   */
   QMAT_E_WORKSPACE = 7, /* workspace NULL or smaller than the call's
@@ -668,7 +669,8 @@ int qmat_rope(const qmat_rope_args *args, void *stream);
  *   token_seq[t] = b. Rows behind the last token get slot -1 (which
  *   qmat_kv_store skips), position 0 and sequence -1.
  *
- *   All pointers are DEVICE pointers, 4-byte aligned (keep, positions and token_seq
+ *   All pointers are DEVICE pointers, 4-byte aligned; slots 16-byte where
+ *   qmat_kv_store or qmat_kv_load is to take them as they are (keep, positions and token_seq
  *   may be NULL; slots may be when max_tokens is 0, page_table when pages_per_seq is 0,
  *   free_pages when pages is 0, the arrays of sequences when n_seqs is 0). free_pages
  *   has room for pages numbers.

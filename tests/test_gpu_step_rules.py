@@ -28,3 +28,25 @@ def test_norm_refuses_rows_over_the_residual(lib, want, K):
         assert e.value.status == 2
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((x, r, h), before))
+
+
+@pytest.mark.parametrize("seqs,tokens", [(1, 1), (3, 2), (5, 7), (2, 33)])
+def test_a_steps_results_fit_the_calls_behind(lib, seqs, tokens):
+    """What page_step allocates goes into kv_store (slots at 16 bytes), rope and attn as it is, whatever the sizes."""
+    import torch
+    page, pages, heads, D = 16, 20, 2, 64
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    kv, table = ints([0] * seqs), torch.full((seqs, 4), -1, dtype=torch.int32, device="cuda")
+    q_start, slots, positions, _, status = lib.page_step(kv, ints([tokens] * seqs), table, ints(list(range(pages))), ints([pages]), page,
+                                                         seqs * tokens + 1)
+    assert status.tolist() == [0] * seqs and slots.data_ptr() % 16 == 0
+    n = seqs * tokens + 1
+    x = torch.randn(n, heads, D, device="cuda")
+    q, k = lib.rope(x, x.clone(), positions, lib.rope_freq(D))
+    caches = [torch.zeros((pages * page, lib.row_bytes("q8_0", heads * D)), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    lib.kv_store("q8_0", "q8_0", k, x, slots, *caches)
+    out = lib.attn("q8_0", "q8_0", q, *caches, table, q_start, kv, heads, page, max_q=tokens)
+    assert torch.isfinite(out).all().item() and out[:-1].any(-1).all().item()
+    with pytest.raises(lib.QmatError) as e:  # a slice that begins between 16 bytes
+        lib.kv_store("q8_0", "q8_0", k, x, torch.cat((slots[:1], slots))[1:], *caches)
+    assert e.value.status == 5
