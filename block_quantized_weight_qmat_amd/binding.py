@@ -821,7 +821,9 @@ def page_step(kv_len: torch.Tensor, add: torch.Tensor, page_table: torch.Tensor,
     rows behind the last token have slot -1, position 0, sequence -1. status is 0
     where it was done, 1 where the table row or max_tokens, 2 where the
     pages do not suffice: such a sequence is left as it was and has no tokens.
-    Slots of one's own are 16-byte aligned if kv_store is to take them."""
+    One that can never fit counts all the same: set its add to 0, or those behind
+    it wait with it. A page is held by one sequence. Slots of one's own are 16-byte
+    aligned if kv_store is to take them."""
     device = kv_len.device
     _gpu(kv_len, "kv_len", torch.int32)
     n_seqs = kv_len.numel()

@@ -8,6 +8,9 @@
 // chain of loads and barriers, and the number of launches: 48 sequences 4.2 us, 200
 // sequences with 60000 rows of tokens 7.6, 1000 with as many 11.9, 4000 with 4000 rows 36.
 //
+// A sequence that does not fit its table row asks for its tokens like any other (the caller takes it
+// out), but for no pages: it will never get one.
+//
 // One workgroup goes through the sequences, a thread for each, since the sums need every
 // sequence, and lengths, table and stack are changed in place, which no other workgroup
 // may see half done. Up to 256 sequences it has 256 threads (48 sequences 4 us, with 1024

@@ -661,6 +661,15 @@ int qmat_rope(const qmat_rope_args *args, void *stream);
  *   excepted) exceed the free ones (and it needs any): whoever comes first is
  *   served first, and a large one that waits is not overtaken by later ones
  *   that need pages. status[b] = 0: done.
+ *   The tokens of a refused sequence count as asked for, also of one whose goal no
+ *   table row or whose add no step can hold: while it asks for more than max_tokens,
+ *   every sequence behind it that adds any is refused with it, step after step. A
+ *   caller ends such a request, or sets its add to 0, when it sees status 1 for it.
+ *
+ *   A page has one owner: a number that stands in the held part of two table rows, or
+ *   of one and in the stack, is given back by each that held it and may then be
+ *   granted twice. Pages that several requests share are kept out of the
+ *   rows that this call changes.
  *
  *   Outputs: kv_len[b] = goal (in place); the pages taken in page_table;
  *   free_pages and free_count[0] updated; q_start[n_seqs + 1], the prefix sum of the

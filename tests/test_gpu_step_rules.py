@@ -50,3 +50,18 @@ def test_a_steps_results_fit_the_calls_behind(lib, seqs, tokens):
     with pytest.raises(lib.QmatError) as e:  # a slice that begins between 16 bytes
         lib.kv_store("q8_0", "q8_0", k, x, torch.cat((slots[:1], slots))[1:], *caches)
     assert e.value.status == 5
+
+
+def test_a_request_that_never_fits_holds_up_those_behind_it(lib):
+    """As the header says: its tokens count while it asks for them, and no longer when its add is 0."""
+    import torch
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for large in (65, 40):  # more than its four pages of 16 hold; more than a step has
+        kv, table = ints([5, 0, 7]), ints([[0, -1, -1, -1], [-1] * 4, [1, -1, -1, -1]])
+        free, count, add = ints(list(range(2, 12)) + [0, 0]), ints([10]), ints([1, large, 1])
+        for _ in range(2):
+            got = lib.page_step(kv, add, table, free, count, 16, 32)
+            assert got[4].tolist() == [0, 1, 1]
+        add[1] = 0
+        got = lib.page_step(kv, add, table, free, count, 16, 32)
+        assert got[4].tolist() == [0, 0, 0] and kv.tolist() == [8, 0, 8] and count.tolist() == [10]
