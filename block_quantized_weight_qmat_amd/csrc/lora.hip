@@ -13,8 +13,9 @@
 // 4096: 31 us, half of it each kernel: the second moves 50 MB at 3.3 TB/s, the
 // first brings its chunks of a and x into LDS at 43 KB/us for each CU, however many are
 // on their way. 64 tokens of a decode batch, 24 adapters
-// of rank 16, 4096 -> 11008: 9 us, a chain of loads (start, adapter, code, a, b) of which
-// nothing can be asked for before the one in front has come.
+// of rank 16, 4096 -> 11008: 9 us, chains of loads: start and adapter, then its rank and b's first
+// rows; a's first elements are asked for behind the barrier at which the codes are there, base
+// behind z, although a waits only for the adapter's number and base for nothing.
 //
 // Tiles of tokens lie within one sequence: of the aligned runs of 32 (or 16) tokens, a
 // sequence has those that it reaches into, cut at its ends. So a tile has one

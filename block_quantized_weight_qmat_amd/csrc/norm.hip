@@ -239,6 +239,9 @@ void launch_rows(const qmat_norm_args& a, hipStream_t stream) {
   }
 }
 
+// Threads of a row: the next power of two, so that a K just past one leaves up to half of
+// them without elements. bf16, both results: 4096 rows of 4096 / 5120 / 8192 / 8384 run at 5.9, 5.7,
+// 5.6 and 3.8 TB/s (two units a thread in the last), 512 rows at 3.2, 3.3, 4.1 and 3.6.
 template <typename T>
 void launch_as(const qmat_norm_args& a, hipStream_t stream) {
   if (a.K <= 512)
